@@ -344,6 +344,173 @@ qg_status qgemv_q8g64_argmax_noalloc(const void *w_packed, const uint16_t *x_bf1
                                      int32_t *idx_out, int64_t m, int64_t N, int64_t K, int64_t ldx,
                                      int64_t ldy, void *hip_stream);
 
+/* ------------------------------------------- attention block, between GEMVs
+ * What a decode or chunked-prefill step runs between the QKV projection and
+ * the output projection: rotary positions with the new keys and values
+ * written into a paged cache, then attention over that cache.
+ *
+ * The cache, described by the caller: element (page, kv head h, slot s,
+ * dimension d) of keys and of values is at
+ *     page * page_stride + h * head_stride + s * slot_stride + d
+ * (strides in elements, the same for k and v).  A token's place is a slot
+ * number page * page_size + s.
+ *   k, v        device, 16-byte aligned, `pages` pages
+ *   k_scale,    device fp32, one per kv head, QG_KV_E4M3 only (else ignored):
+ *   v_scale     what an 8-bit code is multiplied by
+ *   page_size   tokens per page, a power of two up to 2^20
+ *   head_dim    a multiple of 16, up to 256
+ *   dtype       QG_KV_BF16, or QG_KV_E4M3 (8-bit floats: 4 exponent and 3
+ *               mantissa bits, largest 448, no infinity)
+ *   strides     0..2^31 elements, multiples of 16 bytes; rows must not overlap
+ * Errors of every call that takes one: QG_ERR_INVALID_ARG for a null pointer,
+ * a size below 1 or overlapping rows, QG_ERR_UNSUPPORTED for a head_dim,
+ * page_size or dtype outside the above, QG_ERR_ALIGNMENT for a pointer or
+ * stride. */
+#define QG_KV_BF16 0
+#define QG_KV_E4M3 1
+typedef struct qg_kv_cache {
+    void *k;
+    void *v;
+    const float *k_scale;
+    const float *v_scale;
+    int64_t pages;
+    int64_t page_stride;
+    int64_t head_stride;
+    int64_t slot_stride;
+    int32_t kv_heads;
+    int32_t page_size;
+    int32_t head_dim;
+    int32_t dtype;
+} qg_kv_cache;
+
+/* Rotary frequencies, made once per model by qg_rope_init (host only) and
+ * passed by value with every call: pair i < rot_dim / 2 of a head turns by
+ * position * f_i with
+ *     f_i = base^(-2 i / rot_dim)                       QG_ROPE_PLAIN
+ *     f_i = base^(-2 i / rot_dim) / factor              QG_ROPE_LINEAR
+ *     f_i between the two over a ramp of pairs          QG_ROPE_YARN
+ * The ramp runs from the pair that makes beta_fast turns over original_len
+ * positions (rounded down, unscaled before it) to the one that makes
+ * beta_slow (rounded up, divided by factor from it on).  `amplitude`
+ * multiplies the rotated dimensions; 0 asks for 1, or for
+ * 0.1 ln(factor) + 1 with QG_ROPE_YARN.  Pairs are (2i, 2i + 1) where
+ * `interleaved` is not 0, else (i, i + rot_dim / 2).  turns[i] is
+ * f_i / (2 pi) as a 64-bit binary fraction.
+ * QG_ERR_INVALID_ARG: rot_dim odd or below 2, base not above 1, factor below
+ * 1, original_len below 1, a beta not above 0, amplitude below 0, or a value
+ * not finite.  QG_ERR_UNSUPPORTED: rot_dim above 256, another scaling. */
+#define QG_ROPE_PLAIN 0
+#define QG_ROPE_LINEAR 1
+#define QG_ROPE_YARN 2
+typedef struct qg_rope {
+    int32_t rot_dim;
+    int32_t interleaved;
+    float amplitude;
+    int32_t reserved;
+    uint64_t turns[128];
+} qg_rope;
+qg_status qg_rope_init(qg_rope *rope, int32_t rot_dim, int32_t interleaved, double base, int32_t scaling,
+                       double factor, int64_t original_len, double beta_fast, double beta_slow, double amplitude);
+
+/* Rotates the queries into q_out and the keys into the cache, and copies the
+ * values into the cache, for `tokens` tokens in one launch:
+ *   q, k, v     device, fp32 (QG_SRC_F32, as the GEMV calls write) or bf16
+ *               (QG_SRC_BF16): element (t, h, d) at t * token_stride +
+ *               h * head_stride + d; views of one QKV row are fine
+ *   pos         device int32[tokens]: each token's position
+ *   slots       device int64[tokens]: each token's place in the cache; a slot
+ *               outside the cache (a negative one, for rows that only fill up
+ *               a batch) writes no key or value.  Two tokens must not share
+ *               one: either may win.
+ *   q_out       device bf16, strides as above; must not overlap q, k or v
+ * Dimensions from rot_dim on are copied.  Angles are exact to 2^-65 turns per
+ * position whatever the position; the rotation is fp32.  A bf16 cache takes
+ * values rounded to nearest even; an 8-bit one takes x / scale clamped to
+ * +-448 and rounded to nearest even, NaN kept.
+ * QG_ERR_INVALID_ARG: null pointer, tokens < 0, q_heads < 1, rot_dim above
+ * head_dim, a stride out of 0..2^31, overlapping q_out rows; tokens = 0 does
+ * nothing.  Pointers need their element's alignment; 16-byte aligned rows are
+ * read and written in wide accesses. */
+#define QG_SRC_F32 0
+#define QG_SRC_BF16 1
+qg_status qg_rope_append(const qg_kv_cache *cache, const qg_rope *rope, const void *q, const void *k, const void *v,
+                         int32_t src_dtype, int64_t q_token_stride, int64_t q_head_stride, int64_t k_token_stride,
+                         int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, const int32_t *pos,
+                         const int64_t *slots, uint16_t *q_out, int64_t out_token_stride, int64_t out_head_stride,
+                         int64_t tokens, int32_t q_heads, void *hip_stream);
+
+/* Attention of each sequence's new tokens over its cached tokens (the new
+ * ones among them).  For sequence b with n = q_start[b+1] - q_start[b] new
+ * tokens and kv_len[b] cached ones, new token i (row q_start[b] + i of q) is
+ * at position kv_len[b] - n + i and sees the keys j at positions
+ *     j <= its own, and with window > 0: j > its own - window:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j,   lse = log sum_j exp(scale * q . k_j)
+ * Query head h reads kv head h / (q_heads / kv_heads).  One token a sequence,
+ * a few drafted ones, whole chunks, or a mix of them in one call.  A row that
+ * sees no key gets zeros, and -infinity as its lse.  Keys that a row does not
+ * see do not reach it, whatever they hold.
+ *   q_bf16      device bf16, element (row, h, d) at row * q_token_stride +
+ *               h * q_head_stride + d; 16-byte aligned, strides in 16 bytes
+ *   out_bf16    device bf16; 8-byte aligned, strides in 8 bytes
+ *   lse         device fp32 (row, h) at row * lse_token_stride + h, or NULL
+ *   q_start     device int32[seqs + 1], ascending from 0 to tokens
+ *   kv_len      device int32[seqs]
+ *   page_table  device int32: page of tokens [c * page_size, ...) of sequence
+ *               b at b * table_stride + c, c < table_cols; read only where
+ *               kv_len reaches.  Keys of a page outside the cache count as
+ *               NaN.
+ *   tokens      rows of q, out and lse; rows of no sequence are not written
+ *   max_q,      host's bounds on n and on kv_len[b]: they size the launch and
+ *   max_kv      the workspace.  A longer sequence is cut to them (to
+ *               table_cols pages, to `tokens` rows), never read beyond.
+ *   workspace   device, >= qg_paged_attention_workspace_size(...) bytes,
+ *               16-byte aligned, all zero before the first call; a completed
+ *               call leaves it ready for the next, of any shape that needs no
+ *               more.  Calls that share one must not overlap in time.
+ * Scores, softmax statistics and sums are fp32; probabilities enter the
+ * second product as bf16.  The split of a sequence over work-groups and the
+ * order of every sum depend on the arguments alone: a result is the same bits
+ * from run to run.  QG_ERR_INVALID_ARG also for q_heads no multiple of
+ * kv_heads and a scale that is not finite. */
+size_t    qg_paged_attention_workspace_size(const qg_kv_cache *cache, int64_t tokens, int32_t q_heads, int32_t seqs,
+                                            int64_t max_q, int64_t max_kv);
+qg_status qg_paged_attention(const qg_kv_cache *cache, const uint16_t *q_bf16, int64_t q_token_stride,
+                             int64_t q_head_stride, uint16_t *out_bf16, int64_t out_token_stride,
+                             int64_t out_head_stride, float *lse, int64_t lse_token_stride, const int32_t *q_start,
+                             const int32_t *kv_len, const int32_t *page_table, int64_t table_stride,
+                             int64_t table_cols, int64_t tokens, int32_t q_heads, int32_t seqs, int64_t max_q,
+                             int64_t max_kv, float scale, int64_t window, void *workspace, size_t workspace_bytes,
+                             void *hip_stream);
+
+/* ---------------------------------------------------------- sampled tail
+ * A token per row of fp32 logits (the LM head's output), as the greedy tail
+ * but drawn.  With the row's tokens in the order (larger logit, then lower
+ * index) and weights w = exp((x - max x) / temperature), the tokens kept are
+ *   top_k       the first top_k                                (<= 0: all)
+ *   top_p       of those, the ones with a weight before them below top_p times
+ *               the weight of those, the first at least        (>= 1: all)
+ *   min_p       and of those, the ones with w >= min(min_p, 1)
+ * and idx_out[i] is the first token, by index, where the running sum of the
+ * kept weights passes u[i] times their sum.  temperature <= 0 (or NaN) is the
+ * greedy choice of qg_argmax_f32, as is a row that holds a NaN or nothing but
+ * -infinity.  A logit of -infinity is never drawn beside a finite one; equal
+ * logits of +infinity share the draw.  u at or above 1, or NaN, gives the
+ * greedy choice.
+ *   logits      device fp32, 4-byte aligned, m rows of N values, ldx >= N
+ *   u           device fp32[m], uniform in [0, 1)
+ *   temperature, top_p, min_p  device fp32[m], top_k device int32[m]; NULL for
+ *               1, 1, 0 and none
+ *   workspace   device, >= qg_sample_workspace_size(m, N) bytes, 16-byte
+ *               aligned, all zero before the first call; a completed call
+ *               leaves it ready for the next of any m and N that need no more.
+ *               Calls that share one must not overlap in time.
+ * Weights and sums are 64-bit; results do not depend on timing.
+ * 1 <= N < 2^31, m <= 65535; m = 0 is a no-op. */
+size_t    qg_sample_workspace_size(int64_t m, int64_t N);
+qg_status qg_sample_f32(const float *logits, int64_t m, int64_t N, int64_t ldx, const float *u,
+                        const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                        int32_t *idx_out, void *workspace, size_t workspace_bytes, void *hip_stream);
+
 /* ------------------------------------------------------------- test hooks
  * Host-side route counters, after the routing witnesses of the vllm.cpp pull
  * request #1936 commit log (process-global counters bumped once per dispatch

@@ -36,7 +36,24 @@ FMT_Q8G128_MMA = 9
 FMT_Q8PC_MMA = 10
 FMT_Q4G32_MMA = 11
 
+KV_BF16, KV_E4M3 = 0, 1
+SRC_F32, SRC_BF16 = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_YARN = 0, 1, 2
+
 _lib = None
+
+
+class _CacheStruct(ctypes.Structure):
+    """qg_kv_cache."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
+                + [(n, ctypes.c_int64) for n in ("pages", "page_stride", "head_stride", "slot_stride")]
+                + [(n, ctypes.c_int32) for n in ("kv_heads", "page_size", "head_dim", "dtype")])
+
+
+class _RopeStruct(ctypes.Structure):
+    """qg_rope."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * 128)]
 
 
 class QGError(RuntimeError):
@@ -58,6 +75,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         p, i64, i32, sz, st = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t,
                                ctypes.c_int)
+        f64 = ctypes.c_double
         sig = {
             "qg_status_string": ([ctypes.c_int], ctypes.c_char_p),
             "qg_abi_version": ([], ctypes.c_int),
@@ -103,6 +121,13 @@ def lib() -> ctypes.CDLL:
             "qgemv_q8g128_argmax": ([p, p, p, p, i64, i64, i64, i64, i64, p, sz, p], st),
             "qgemv_q8g64_argmax_noalloc": ([p, p, p, p, i64, i64, i64, i64, i64, p], st),
             "qg_argmax_f32": ([p, i64, i64, i64, p, p, sz, p], st),
+            "qg_rope_init": ([p, i32, i32, f64, i32, f64, i64, f64, f64, f64], st),
+            "qg_rope_append": ([p, p, p, p, p, i32] + [i64] * 6 + [p, p, p, i64, i64, i64, i32, p], st),
+            "qg_paged_attention_workspace_size": ([p, i64, i32, i32, i64, i64], sz),
+            "qg_paged_attention": ([p, p, i64, i64, p, i64, i64, p, i64, p, p, p, i64, i64, i64, i32, i32, i64, i64,
+                                    ctypes.c_float, i64, p, sz, p], st),
+            "qg_sample_workspace_size": ([i64, i64], sz),
+            "qg_sample_f32": ([p, i64, i64, i64, p, p, p, p, p, p, p, sz, p], st),
             "qg_route_counts_reset": ([], None),
             "qg_route_count": ([ctypes.c_char_p], ctypes.c_uint64),
             "qg_variant_name": ([ctypes.c_int, i64, i64, i64, ctypes.c_char_p, sz], st),
@@ -651,6 +676,223 @@ def qgemv_q8g128_argmax(w_packed, x, logits, idx_out, workspace, N: int, K: int,
                                                        K, m, ldx, ldy, stream, "qgemv_q8g128_argmax"))
     if check:
         _check(st, "qgemv_q8g128_argmax")
+    return st
+
+
+# ------------------------------------- attention block and sampling (decode)
+
+class KVCache:
+    """The paged cache of one layer, over tensors that the caller owns.
+
+    k, v: device bfloat16 or float8_e4m3fn tensors [page][kv head][slot][dim]
+    (any strides with the dimension innermost, the same for both); k_scale,
+    v_scale: device float32 [kv heads], for float8 only.  A token's slot number
+    is page * page_size + slot.  Holds references to the tensors."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        where = "KVCache"
+        kinds = {"bfloat16": KV_BF16, "float8_e4m3fn": KV_E4M3}
+        kind = str(k.dtype).replace("torch.", "")
+        if kind not in kinds or v.dtype != k.dtype:
+            raise QGError(QG_ERR_INVALID_ARG, where + ": k and v must both be bfloat16 or float8_e4m3fn")
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1 or k.numel() == 0:
+            raise QGError(QG_ERR_INVALID_ARG, where + ": k and v must be [page][kv head][slot][dim] of one shape and "
+                          "strides, the dimension contiguous")
+        self.k, self.v = k, v
+        pages, heads, size, dim = k.shape
+        if kinds[kind] == KV_E4M3:
+            if k_scale is None or v_scale is None:
+                raise QGError(QG_ERR_INVALID_ARG, where + ": a float8 cache needs k_scale and v_scale")
+            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                _need(t, where, name, _F32, heads)
+                if t.dim() != 1 or t.numel() != heads or not t.is_contiguous():
+                    raise QGError(QG_ERR_INVALID_ARG, "%s: %s must be contiguous [kv heads]" % (where, name))
+        else:
+            k_scale = v_scale = None
+        _on_gpu(where, k=k, v=v, k_scale=k_scale, v_scale=v_scale)
+        _one_device(where, k, v, k_scale, v_scale)
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.kv_heads, self.page_size, self.head_dim = heads, size, dim
+        self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), pages, _step(k, 0),
+                                    _step(k, 1), _step(k, 2), heads, size, dim, kinds[kind])
+        self._ref = ctypes.addressof(self._struct)
+
+
+class Rope:
+    """Rotary frequencies of a model (qg_rope_init), host memory only.
+
+    rot_dim: rotated dimensions of a head, the rest is copied; interleaved:
+    pairs (2i, 2i+1) in place of (i, i + rot_dim/2); scaling: None or "none",
+    "linear" (positions divided by factor) or "yarn" (factor, original_len,
+    beta_fast, beta_slow); amplitude: factor on the rotated dimensions, by
+    default 1, or 0.1 ln(factor) + 1 with yarn."""
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling=None,
+                 factor: float = 1.0, original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 amplitude: float = 0.0):
+        kinds = {None: ROPE_PLAIN, "none": ROPE_PLAIN, "linear": ROPE_LINEAR, "yarn": ROPE_YARN}
+        if scaling not in kinds:
+            raise QGError(QG_ERR_UNSUPPORTED, "Rope: scaling %r" % (scaling,))
+        self._struct = _RopeStruct()
+        self._ref = ctypes.addressof(self._struct)
+        _check(lib().qg_rope_init(self._ref, rot_dim, int(bool(interleaved)), base, kinds[scaling], factor,
+                                  original_len, beta_fast, beta_slow, amplitude), "qg_rope_init")
+        self.rot_dim = rot_dim
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _step(t, dim: int) -> int:
+    """Stride of a dimension; 0 where it has one entry (its stride is then arbitrary)."""
+    return t.stride(dim) if t.shape[dim] > 1 else 0
+
+
+def _one_device(where: str, *tensors) -> None:
+    """Every tensor on the first one's device."""
+    for t in tensors:
+        if t is not None and t.device != tensors[0].device:
+            raise QGError(QG_ERR_INVALID_ARG, "%s: tensors on different devices" % where)
+
+
+def _rows(t, where: str, what: str, dtypes, shape) -> None:
+    """Element type and shape of a tensor whose last dimension is contiguous."""
+    dt = str(t.dtype).replace("torch.", "")
+    if dt not in dtypes:
+        raise QGError(QG_ERR_INVALID_ARG, "%s: %s has dtype %s, needs %s" % (where, what, dt, "/".join(dtypes)))
+    if tuple(t.shape) != tuple(shape):
+        raise QGError(QG_ERR_INVALID_ARG, "%s: %s has shape %s, needs %s" % (where, what, tuple(t.shape), tuple(shape)))
+    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise QGError(QG_ERR_INVALID_ARG, "%s: the last dimension of %s must be contiguous" % (where, what))
+
+
+def rope_append(cache: KVCache, rope: Rope, q, k, v, pos, slots, q_out, stream=None, check=True):
+    """Rotates q [tokens][heads][dim] into q_out (bfloat16) and k into the
+    cache at each token's slot, and copies v there, in one launch.
+
+    q, k, v: device float32 or bfloat16, any token and head strides (views of
+    one QKV row); pos: device int32 [tokens]; slots: device int64 [tokens], a
+    negative one writes nothing to the cache.  Enqueued on ``stream`` (default:
+    torch's current stream); returns the status (raises on error when
+    ``check``)."""
+    where = "qg_rope_append"
+    if q.dim() != 3:
+        raise QGError(QG_ERR_INVALID_ARG, where + ": q must be [tokens][heads][dim]")
+    tokens, heads, dim = q.shape
+    kinds = ("float32", "bfloat16")
+    _rows(q, where, "q", kinds, (tokens, heads, cache.head_dim))
+    _rows(k, where, "k", kinds, (tokens, cache.kv_heads, dim))
+    _rows(v, where, "v", kinds, (tokens, cache.kv_heads, dim))
+    _rows(q_out, where, "q_out", ("bfloat16",), (tokens, heads, dim))
+    _rows(pos, where, "pos", _I32, (tokens,))
+    _rows(slots, where, "slots", ("int64",), (tokens,))
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise QGError(QG_ERR_INVALID_ARG, where + ": q, k and v must have one dtype")
+    _on_gpu(where, q=q, k=k, v=v, pos=pos, slots=slots, q_out=q_out)
+    _one_device(where, cache.k, q, k, v, pos, slots, q_out)
+    if tokens == 0:
+        return QG_OK
+    st = lib().qg_rope_append(cache._ref, rope._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                              SRC_F32 if q.element_size() == 4 else SRC_BF16, _step(q, 0), _step(q, 1), _step(k, 0),
+                              _step(k, 1), _step(v, 0), _step(v, 1), pos.data_ptr(), slots.data_ptr(),
+                              q_out.data_ptr(), _step(q_out, 0), _step(q_out, 1), tokens, heads,
+                              _stream_handle(stream))
+    if check:
+        _check(st, where)
+    return st
+
+
+def paged_attention_workspace_size(cache: KVCache, tokens: int, q_heads: int, seqs: int, max_q: int,
+                                   max_kv: int) -> int:
+    """Bytes of workspace for paged_attention with these bounds; raises for
+    arguments the call would refuse."""
+    size = int(lib().qg_paged_attention_workspace_size(cache._ref, tokens, q_heads, seqs, max_q, max_kv))
+    if size == 0:
+        raise QGError(QG_ERR_INVALID_ARG, "qg_paged_attention_workspace_size")
+    return size
+
+
+def paged_attention(cache: KVCache, q, out, q_start, kv_len, page_table, workspace, max_q: int, max_kv: int,
+                    scale=None, window: int = 0, lse=None, stream=None, check=True):
+    """Attention of each sequence's new tokens over its cached ones, causal,
+    with a sliding window where window > 0.
+
+    q, out: device bfloat16 [tokens][heads][dim]; q_start: device int32
+    [seqs + 1], where each sequence's rows begin; kv_len: device int32 [seqs],
+    cached tokens with the new ones; page_table: device int32 [seqs][columns];
+    workspace: device tensor of paged_attention_workspace_size(...) bytes,
+    zero before the first call; max_q, max_kv: the host's bounds on new and
+    cached tokens; scale: by default dim ** -0.5; lse: device float32
+    [tokens][heads] or None."""
+    where = "qg_paged_attention"
+    if q.dim() != 3 or page_table.dim() != 2:
+        raise QGError(QG_ERR_INVALID_ARG, where + ": q must be [tokens][heads][dim], page_table [seqs][columns]")
+    tokens, heads, dim = q.shape
+    seqs, cols = page_table.shape
+    _rows(q, where, "q", ("bfloat16",), (tokens, heads, cache.head_dim))
+    _rows(out, where, "out", ("bfloat16",), (tokens, heads, dim))
+    _rows(q_start, where, "q_start", _I32, (seqs + 1,))
+    _rows(kv_len, where, "kv_len", _I32, (seqs,))
+    _rows(page_table, where, "page_table", _I32, (seqs, cols))
+    if lse is not None:
+        _rows(lse, where, "lse", _F32, (tokens, heads))
+    if not workspace.is_contiguous():
+        raise QGError(QG_ERR_INVALID_ARG, where + ": workspace must be contiguous")
+    _on_gpu(where, q=q, out=out, q_start=q_start, kv_len=kv_len, page_table=page_table, workspace=workspace, lse=lse)
+    _one_device(where, cache.k, q, out, q_start, kv_len, page_table, workspace, lse)
+    if tokens == 0 or seqs == 0:
+        return QG_OK
+    if cols == 0:
+        raise QGError(QG_ERR_INVALID_ARG, where + ": page_table has no column")
+    st = lib().qg_paged_attention(cache._ref, q.data_ptr(), _step(q, 0), _step(q, 1), out.data_ptr(), _step(out, 0),
+                                  _step(out, 1), _ptr(lse), 0 if lse is None else _step(lse, 0), q_start.data_ptr(),
+                                  kv_len.data_ptr(), page_table.data_ptr(), _step(page_table, 0), cols, tokens, heads,
+                                  seqs, max_q, max_kv, dim ** -0.5 if scale is None else scale, window,
+                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                  _stream_handle(stream))
+    if check:
+        _check(st, where)
+    return st
+
+
+def sample_workspace_size(m: int, N: int) -> int:
+    return int(lib().qg_sample_workspace_size(m, N))
+
+
+def sample_f32(logits, u, idx_out, workspace, temperature=None, top_k=None, top_p=None, min_p=None, stream=None,
+               check=True):
+    """Draws a token per row of device fp32 logits [m][N] into idx_out (int32
+    [m]) from uniform numbers u (float32 [m]).
+
+    temperature, top_p, min_p: device float32 [m] or None (1, 1, 0); top_k:
+    device int32 [m] or None; a temperature of 0 is the greedy choice.
+    workspace: device tensor of sample_workspace_size(m, N) bytes, zero before
+    the first call."""
+    where = "qg_sample_f32"
+    if logits.dim() != 2:
+        raise QGError(QG_ERR_INVALID_ARG, where + ": logits must be [m][N]")
+    m, N = logits.shape
+    _rows(logits, where, "logits", _F32, (m, N))
+    _rows(u, where, "u", _F32, (m,))
+    _rows(idx_out, where, "idx_out", _I32, (m,))
+    for what, t, kinds in (("temperature", temperature, _F32), ("top_k", top_k, _I32), ("top_p", top_p, _F32),
+                           ("min_p", min_p, _F32)):
+        if t is not None:
+            _rows(t, where, what, kinds, (m,))
+    if not workspace.is_contiguous():
+        raise QGError(QG_ERR_INVALID_ARG, where + ": workspace must be contiguous")
+    _on_gpu(where, logits=logits, u=u, idx_out=idx_out, workspace=workspace, temperature=temperature, top_k=top_k,
+            top_p=top_p, min_p=min_p)
+    _one_device(where, logits, u, idx_out, workspace, temperature, top_k, top_p, min_p)
+    if m == 0:
+        return QG_OK
+    ldx = _step(logits, 0) or N
+    st = lib().qg_sample_f32(logits.data_ptr(), m, N, ldx, u.data_ptr(), _ptr(temperature), _ptr(top_k), _ptr(top_p),
+                             _ptr(min_p), idx_out.data_ptr(), workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    if check:
+        _check(st, where)
     return st
 
 
