@@ -13,6 +13,7 @@ namespace {
 
 constexpr int64_t kMaxCount = (int64_t(1) << 31) - 1;
 // Elements a stride may span: products with a 31-bit index stay in 63 bits.
+constexpr int64_t kMaxCachedTokens = int64_t(1) << 30;   // of one sequence
 constexpr int64_t kMaxStride = int64_t(1) << 31;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -167,7 +168,8 @@ static qg_status check_attention_shape(const qg_kv_cache* cache, int64_t tokens,
     if (tokens < 0 || tokens > kMaxCount || seqs < 0 || max_q < 0 || max_q > kMaxCount || max_kv < 0 ||
         max_kv > kMaxCount || q_heads < 1 || q_heads % view->kv_heads != 0)
         return QG_ERR_INVALID_ARG;
-    if (seqs > 65535 || q_heads > 65535) return QG_ERR_UNSUPPORTED;
+    if (seqs > 65535 || q_heads > 65535 || max_kv > kMaxCachedTokens || tokens * q_heads > kMaxCount)
+        return QG_ERR_UNSUPPORTED;
     return QG_OK;
 }
 
@@ -176,7 +178,7 @@ size_t qg_paged_attention_workspace_size(const qg_kv_cache* cache, int64_t token
 {
     qg::CacheView view;
     if (check_attention_shape(cache, tokens, q_heads, seqs, max_q, max_kv, &view) != QG_OK) return 0;
-    return qg::attention_workspace_bytes(tokens, q_heads, view.kv_heads, view.head_dim, seqs, max_q, max_kv);
+    return qg::attention_workspace_bytes(view.e4m3, tokens, q_heads, view.kv_heads, view.head_dim, seqs, max_q, max_kv);
 }
 
 qg_status qg_paged_attention(const qg_kv_cache* cache, const uint16_t* q_bf16, int64_t q_token_stride,
@@ -203,7 +205,7 @@ qg_status qg_paged_attention(const qg_kv_cache* cache, const uint16_t* q_bf16, i
         out_token_stride % 4 != 0 || out_head_stride % 4 != 0 || (lse && !aligned(lse, 4)) || !aligned(q_start, 4) ||
         !aligned(kv_len, 4) || !aligned(page_table, 4) || !aligned(workspace, 16))
         return QG_ERR_ALIGNMENT;
-    if (workspace_bytes < qg::attention_workspace_bytes(tokens, q_heads, p.cache.kv_heads, p.cache.head_dim, seqs,
+    if (workspace_bytes < qg::attention_workspace_bytes(p.cache.e4m3, tokens, q_heads, p.cache.kv_heads, p.cache.head_dim, seqs,
                                                         max_q, max_kv))
         return QG_ERR_INVALID_ARG;
     if (tokens == 0 || seqs == 0 || max_q == 0) return QG_OK;

@@ -62,8 +62,8 @@ struct AttnParams {
     void* workspace;
 };
 
-size_t attention_workspace_bytes(int64_t tokens, int q_heads, int kv_heads, int head_dim, int seqs, int64_t max_q,
-                                 int64_t max_kv);
+size_t attention_workspace_bytes(bool e4m3, int64_t tokens, int q_heads, int kv_heads, int head_dim, int seqs,
+                                 int64_t max_q, int64_t max_kv);
 hipError_t launch_attention(const AttnParams& p, hipStream_t s);
 
 struct SampleParams {
