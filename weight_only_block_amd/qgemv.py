@@ -716,6 +716,7 @@ class KVCache:
         self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), pages, _step(k, 0),
                                     _step(k, 1), _step(k, 2), heads, size, dim, kinds[kind])
         self._ref = ctypes.addressof(self._struct)
+        self.device = k.get_device()
 
 
 class Rope:
@@ -756,15 +757,58 @@ def _one_device(where: str, *tensors) -> None:
             raise QGError(QG_ERR_INVALID_ARG, "%s: tensors on different devices" % where)
 
 
-def _rows(t, where: str, what: str, dtypes, shape) -> None:
-    """Element type and shape of a tensor whose last dimension is contiguous."""
-    dt = str(t.dtype).replace("torch.", "")
-    if dt not in dtypes:
-        raise QGError(QG_ERR_INVALID_ARG, "%s: %s has dtype %s, needs %s" % (where, what, dt, "/".join(dtypes)))
-    if tuple(t.shape) != tuple(shape):
-        raise QGError(QG_ERR_INVALID_ARG, "%s: %s has shape %s, needs %s" % (where, what, tuple(t.shape), tuple(shape)))
-    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise QGError(QG_ERR_INVALID_ARG, "%s: the last dimension of %s must be contiguous" % (where, what))
+# These calls come between GEMVs of a few microseconds, so their checks are
+# kept to a few attribute reads a tensor: dtypes compare as torch's objects
+# and the message is put together only once something is wrong.
+_DT = None
+
+
+def _dtypes():
+    """torch's dtype objects, taken when the first call needs them (the module
+    itself does not import torch)."""
+    global _DT
+    import torch
+
+    class kinds:
+        f32 = (torch.float32,)
+        i32 = (torch.int32,)
+        i64 = (torch.int64,)
+        bf16 = (torch.bfloat16,)
+        src = (torch.float32, torch.bfloat16)
+    # the raw handle without a torch.cuda.Stream around it (1 us less a call),
+    # where this torch has it
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    kinds.current_stream = staticmethod(raw or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+    _DT = kinds
+    return kinds
+
+
+def _fits(t, where: str, what: str, kinds, shape, device: int):
+    """Refuses a tensor of another dtype, shape or device, or whose last
+    dimension is not contiguous; returns its strides."""
+    steps = t.stride()
+    if t.dtype in kinds and t.shape == shape and t.get_device() == device and device >= 0 and \
+            (steps[-1] == 1 or shape[-1] <= 1):
+        return steps
+    if t.device.type != "cuda":
+        raise QGError(QG_ERR_INVALID_ARG, "%s: %s is not a GPU tensor" % (where, what))
+    raise QGError(QG_ERR_INVALID_ARG, "%s: %s is %s %s with strides %s on %s, needs %s %s, the last dimension contiguous, "
+                  "on cuda:%d" % (where, what, t.dtype, tuple(t.shape), steps, t.device,
+                                  "/".join(str(k) for k in kinds), tuple(shape), device))
+
+
+def _space(t, where: str, device: int) -> int:
+    """Bytes of a workspace tensor."""
+    if t.get_device() != device or not t.is_contiguous():
+        raise QGError(QG_ERR_INVALID_ARG, where + ": workspace must be contiguous and on the same GPU")
+    return t.numel() * t.element_size()
+
+
+def _stream_of(stream, device: int):
+    """As _stream_handle, None for the current stream of the tensors' device."""
+    if stream is None:
+        return _DT.current_stream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def rope_append(cache: KVCache, rope: Rope, q, k, v, pos, slots, q_out, stream=None, check=True):
@@ -777,28 +821,31 @@ def rope_append(cache: KVCache, rope: Rope, q, k, v, pos, slots, q_out, stream=N
     torch's current stream); returns the status (raises on error when
     ``check``)."""
     where = "qg_rope_append"
+    dt = _DT or _dtypes()
     if q.dim() != 3:
         raise QGError(QG_ERR_INVALID_ARG, where + ": q must be [tokens][heads][dim]")
-    tokens, heads, dim = q.shape
-    kinds = ("float32", "bfloat16")
-    _rows(q, where, "q", kinds, (tokens, heads, cache.head_dim))
-    _rows(k, where, "k", kinds, (tokens, cache.kv_heads, dim))
-    _rows(v, where, "v", kinds, (tokens, cache.kv_heads, dim))
-    _rows(q_out, where, "q_out", ("bfloat16",), (tokens, heads, dim))
-    _rows(pos, where, "pos", _I32, (tokens,))
-    _rows(slots, where, "slots", ("int64",), (tokens,))
-    if k.dtype != q.dtype or v.dtype != q.dtype:
-        raise QGError(QG_ERR_INVALID_ARG, where + ": q, k and v must have one dtype")
-    _on_gpu(where, q=q, k=k, v=v, pos=pos, slots=slots, q_out=q_out)
-    _one_device(where, cache.k, q, k, v, pos, slots, q_out)
-    if tokens == 0:
-        return QG_OK
+    shape = q.shape
+    tokens, heads, dim = shape
+    if dim != cache.head_dim:
+        raise QGError(QG_ERR_INVALID_ARG, "%s: q has dimension %d, the cache %d" % (where, dim, cache.head_dim))
+    dev = cache.device
+    kind = (q.dtype,) if q.dtype in dt.src else dt.src
+    kv = (tokens, cache.kv_heads, dim)
+    sq = _fits(q, where, "q", kind, shape, dev)
+    sk = _fits(k, where, "k", kind, kv, dev)
+    sv = _fits(v, where, "v", kind, kv, dev)
+    so = _fits(q_out, where, "q_out", dt.bf16, shape, dev)
+    _fits(pos, where, "pos", dt.i32, (tokens,), dev)
+    _fits(slots, where, "slots", dt.i64, (tokens,), dev)
+    if tokens <= 1 or heads == 1 or kv[1] == 1:
+        if tokens == 0:
+            return QG_OK
+        sq, sk, sv, so = [(_step(t, 0), _step(t, 1)) for t in (q, k, v, q_out)]
     st = lib().qg_rope_append(cache._ref, rope._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                              SRC_F32 if q.element_size() == 4 else SRC_BF16, _step(q, 0), _step(q, 1), _step(k, 0),
-                              _step(k, 1), _step(v, 0), _step(v, 1), pos.data_ptr(), slots.data_ptr(),
-                              q_out.data_ptr(), _step(q_out, 0), _step(q_out, 1), tokens, heads,
-                              _stream_handle(stream))
-    if check:
+                              SRC_F32 if kind == dt.f32 else SRC_BF16, sq[0], sq[1], sk[0], sk[1],
+                              sv[0], sv[1], pos.data_ptr(), slots.data_ptr(), q_out.data_ptr(), so[0], so[1], tokens,
+                              heads, _stream_of(stream, dev))
+    if check and st:
         _check(st, where)
     return st
 
@@ -826,32 +873,34 @@ def paged_attention(cache: KVCache, q, out, q_start, kv_len, page_table, workspa
     cached tokens; scale: by default dim ** -0.5; lse: device float32
     [tokens][heads] or None."""
     where = "qg_paged_attention"
+    dt = _DT or _dtypes()
     if q.dim() != 3 or page_table.dim() != 2:
         raise QGError(QG_ERR_INVALID_ARG, where + ": q must be [tokens][heads][dim], page_table [seqs][columns]")
-    tokens, heads, dim = q.shape
-    seqs, cols = page_table.shape
-    _rows(q, where, "q", ("bfloat16",), (tokens, heads, cache.head_dim))
-    _rows(out, where, "out", ("bfloat16",), (tokens, heads, dim))
-    _rows(q_start, where, "q_start", _I32, (seqs + 1,))
-    _rows(kv_len, where, "kv_len", _I32, (seqs,))
-    _rows(page_table, where, "page_table", _I32, (seqs, cols))
+    shape = q.shape
+    tokens, heads, dim = shape
+    seqs, cols = table_shape = page_table.shape
+    if dim != cache.head_dim or cols == 0:
+        raise QGError(QG_ERR_INVALID_ARG, "%s: q has dimension %d, the cache %d; page_table has %d columns"
+                      % (where, dim, cache.head_dim, cols))
+    dev = cache.device
+    sq = _fits(q, where, "q", dt.bf16, shape, dev)
+    so = _fits(out, where, "out", dt.bf16, shape, dev)
+    _fits(q_start, where, "q_start", dt.i32, (seqs + 1,), dev)
+    _fits(kv_len, where, "kv_len", dt.i32, (seqs,), dev)
+    row = _fits(page_table, where, "page_table", dt.i32, table_shape, dev)[0]
     if lse is not None:
-        _rows(lse, where, "lse", _F32, (tokens, heads))
-    if not workspace.is_contiguous():
-        raise QGError(QG_ERR_INVALID_ARG, where + ": workspace must be contiguous")
-    _on_gpu(where, q=q, out=out, q_start=q_start, kv_len=kv_len, page_table=page_table, workspace=workspace, lse=lse)
-    _one_device(where, cache.k, q, out, q_start, kv_len, page_table, workspace, lse)
-    if tokens == 0 or seqs == 0:
-        return QG_OK
-    if cols == 0:
-        raise QGError(QG_ERR_INVALID_ARG, where + ": page_table has no column")
-    st = lib().qg_paged_attention(cache._ref, q.data_ptr(), _step(q, 0), _step(q, 1), out.data_ptr(), _step(out, 0),
-                                  _step(out, 1), _ptr(lse), 0 if lse is None else _step(lse, 0), q_start.data_ptr(),
-                                  kv_len.data_ptr(), page_table.data_ptr(), _step(page_table, 0), cols, tokens, heads,
-                                  seqs, max_q, max_kv, dim ** -0.5 if scale is None else scale, window,
-                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                  _stream_handle(stream))
-    if check:
+        _fits(lse, where, "lse", dt.f32, (tokens, heads), dev)
+    room = _space(workspace, where, dev)
+    if tokens <= 1 or heads == 1 or seqs <= 1:
+        if tokens == 0 or seqs == 0:
+            return QG_OK
+        sq, so, row = (_step(q, 0), _step(q, 1)), (_step(out, 0), _step(out, 1)), _step(page_table, 0)
+    st = lib().qg_paged_attention(cache._ref, q.data_ptr(), sq[0], sq[1], out.data_ptr(), so[0], so[1], _ptr(lse),
+                                  0 if lse is None else _step(lse, 0), q_start.data_ptr(), kv_len.data_ptr(),
+                                  page_table.data_ptr(), row, cols, tokens, heads, seqs, max_q, max_kv,
+                                  dim ** -0.5 if scale is None else scale, window, workspace.data_ptr(), room,
+                                  _stream_of(stream, dev))
+    if check and st:
         _check(st, where)
     return st
 
@@ -870,28 +919,32 @@ def sample_f32(logits, u, idx_out, workspace, temperature=None, top_k=None, top_
     workspace: device tensor of sample_workspace_size(m, N) bytes, zero before
     the first call."""
     where = "qg_sample_f32"
+    dt = _DT or _dtypes()
     if logits.dim() != 2:
         raise QGError(QG_ERR_INVALID_ARG, where + ": logits must be [m][N]")
-    m, N = logits.shape
-    _rows(logits, where, "logits", _F32, (m, N))
-    _rows(u, where, "u", _F32, (m,))
-    _rows(idx_out, where, "idx_out", _I32, (m,))
-    for what, t, kinds in (("temperature", temperature, _F32), ("top_k", top_k, _I32), ("top_p", top_p, _F32),
-                           ("min_p", min_p, _F32)):
-        if t is not None:
-            _rows(t, where, what, kinds, (m,))
-    if not workspace.is_contiguous():
-        raise QGError(QG_ERR_INVALID_ARG, where + ": workspace must be contiguous")
-    _on_gpu(where, logits=logits, u=u, idx_out=idx_out, workspace=workspace, temperature=temperature, top_k=top_k,
-            top_p=top_p, min_p=min_p)
-    _one_device(where, logits, u, idx_out, workspace, temperature, top_k, top_p, min_p)
-    if m == 0:
-        return QG_OK
-    ldx = _step(logits, 0) or N
+    shape = logits.shape
+    m, N = shape
+    dev = logits.get_device()
+    rows = (m,)
+    ldx = _fits(logits, where, "logits", dt.f32, shape, dev)[0]
+    _fits(u, where, "u", dt.f32, rows, dev)
+    _fits(idx_out, where, "idx_out", dt.i32, rows, dev)
+    if temperature is not None:
+        _fits(temperature, where, "temperature", dt.f32, rows, dev)
+    if top_k is not None:
+        _fits(top_k, where, "top_k", dt.i32, rows, dev)
+    if top_p is not None:
+        _fits(top_p, where, "top_p", dt.f32, rows, dev)
+    if min_p is not None:
+        _fits(min_p, where, "min_p", dt.f32, rows, dev)
+    room = _space(workspace, where, dev)
+    if m <= 1:
+        if m == 0:
+            return QG_OK
+        ldx = N
     st = lib().qg_sample_f32(logits.data_ptr(), m, N, ldx, u.data_ptr(), _ptr(temperature), _ptr(top_k), _ptr(top_p),
-                             _ptr(min_p), idx_out.data_ptr(), workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(), _stream_handle(stream))
-    if check:
+                             _ptr(min_p), idx_out.data_ptr(), workspace.data_ptr(), room, _stream_of(stream, dev))
+    if check and st:
         _check(st, where)
     return st
 
