@@ -2,8 +2,25 @@
 // given uniform numbers.
 //
 // The tokens that survive the cuts are always the first ones of the order
-// (larger logit, then lower index), so each cut is a place in that order: a
-// key and, where several logits equal it, the last index kept.
+// (larger logit, then lower index), so all cuts together are one 64-bit key
+// of that order (argmax_key): a token is kept when its key is not below it.
+// Sums over the order's head (top-p) are integers in fixed point, and sums
+// over indices (the draw) are fp64 in a fixed order, so nothing depends on
+// the order in which atomics arrive.
+//
+// A row is split into chunks, one work-group each, in three launches:
+//   1. the largest key of each chunk;
+//   2. where some cut is asked for, a histogram of the row over bins of
+//      (largest - logit): counts, and for top-p weights;
+//   3. from the histogram, the bins that the cuts fall into: tokens above are
+//      kept for sure and summed, tokens in those bins become candidates; the
+//      row's last work-group ranks the candidates against each other, which
+//      gives the key, adds the kept ones to their chunks' sums, finds the
+//      chunk that the uniform number falls into and the token in it.
+// Bound by reading the logits (64 rows of 151936: 39 MB) and, for few rows, by
+// the launches' latency.  Rows of up to 8192 logits, and rows whose cut falls
+// into a bin of more than 4096 tokens (many nearly equal logits), are done by
+// one work-group, which finds the key by a radix selection.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -17,165 +34,249 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
 constexpr int kBins = 2048;
-constexpr int kTile = kThreads * 4;
+constexpr int kCandidates = 4096;
+constexpr int kMaxChunks = 64;
+constexpr int64_t kSmallRow = 8192;        // one work-group at once
+constexpr int64_t kResident = 512;         // work-groups the chip holds at once
 
-// Weights in fixed point for the sums over the order's head: integer sums do
-// not depend on the order of the atomics.  N weights of at most 1 fit 62 bits.
+// Row r's part of the workspace.
+struct RowSpace {
+    unsigned long long weight[kBins];
+    unsigned int count[kBins];
+    unsigned long long key[kMaxChunks];
+    unsigned long long sum[kMaxChunks];    // fp64 bits
+    unsigned long long candidate[kCandidates];
+    unsigned int candidates, arrived, pad[14];
+};
+
+// Weights in fixed point: N weights of at most 1 fit 62 bits.
 __device__ __forceinline__ int weight_bits(int64_t N)
 {
-    int b = 62 - (64 - __clzll(uint64_t(N)));
+    const int b = 62 - (64 - __clzll((long long)N));
     return b > 52 ? 52 : b;
 }
 
 __device__ __forceinline__ uint32_t order_of(float v) { return uint32_t(argmax_key(v, 0) >> 32); }
 
-__device__ __forceinline__ double weight_of(float x, float top, double t)
+__device__ __forceinline__ float value_of(uint32_t order)
 {
-    if (x == top) return 1.0;
-    if (x == -INFINITY) return 0.0;
-    return exp((double(x) - double(top)) / t);
+    return __uint_as_float((order & 0x80000000u) ? order & 0x7fffffffu : ~order);
+}
+
+// A row's settings; weights are 2^y with y = (x - top) log2(e) / temperature.
+struct Row {
+    float top;
+    double rate;          // log2(e) / temperature
+    int64_t N, k;
+    double top_p, floor;
+    int bits;
+    bool greedy;
+    int32_t top_idx;
+
+    __device__ __forceinline__ double exponent(float v) const
+    {
+        return v == top ? 0.0 : (double(v) - double(top)) * rate;
+    }
+    // Far below the smallest fp64 weight (or -infinity): never drawn, and left
+    // out of the ranks behind every token that can be.
+    static __device__ __forceinline__ bool nothing(double y) { return !(y >= -1100.0); }
+
+    // 2^y for y <= 0: 2^round(y) times the Taylor series of 2^f, |f| <= 1/2,
+    // whose 13th term is below 2^-52.
+    static __device__ __forceinline__ double weight(double y)
+    {
+        if (nothing(y)) return 0.0;
+        const double n = __builtin_rint(y);
+        const double f = (y - n) * 0.69314718055994530942;
+        double p = 1.0 / 479001600.0;
+        p = __builtin_fma(p, f, 1.0 / 39916800.0);
+        p = __builtin_fma(p, f, 1.0 / 3628800.0);
+        p = __builtin_fma(p, f, 1.0 / 362880.0);
+        p = __builtin_fma(p, f, 1.0 / 40320.0);
+        p = __builtin_fma(p, f, 1.0 / 5040.0);
+        p = __builtin_fma(p, f, 1.0 / 720.0);
+        p = __builtin_fma(p, f, 1.0 / 120.0);
+        p = __builtin_fma(p, f, 1.0 / 24.0);
+        p = __builtin_fma(p, f, 1.0 / 6.0);
+        p = __builtin_fma(p, f, 0.5);
+        p = __builtin_fma(p, f, 1.0);
+        p = __builtin_fma(p, f, 1.0);
+        return ldexp(p, int(n));
+    }
+    __device__ __forceinline__ unsigned long long fixed(double w) const
+    {
+        return (unsigned long long)(ldexp(w, bits) + 0.5);
+    }
+    // Weight of a kept token in the draw.
+    __device__ __forceinline__ double drawn(float v) const
+    {
+        const double w = weight(exponent(v));
+        return w >= floor ? w : 0.0;
+    }
+    __device__ __forceinline__ bool cut() const { return k < N || top_p < 1.0; }
+};
+
+__device__ __forceinline__ Row row_of(const SampleParams& p, int64_t row, uint64_t best)
+{
+    Row r;
+    r.top_idx = key_index(best);
+    r.top = p.x[row * p.ldx + r.top_idx];
+    const float t = p.temperature ? p.temperature[row] : 1.0f;
+    // greedy, or nothing to weigh: a NaN wins, and a row of -infinity gives its first
+    r.greedy = !(t > 0.0f) || r.top != r.top || r.top == -INFINITY;
+    r.rate = 1.44269504088896340736 / double(t);
+    r.N = p.N;
+    r.k = p.top_k && p.top_k[row] > 0 ? min(int64_t(p.top_k[row]), p.N) : p.N;
+    const float tp = p.top_p ? p.top_p[row] : 1.0f, mp = p.min_p ? p.min_p[row] : 0.0f;
+    r.top_p = tp < 1.0f ? double(tp) : 1.0;          // NaN: none
+    r.floor = mp != mp ? 0.0 : fmin(double(mp), 1.0);
+    r.bits = weight_bits(p.N);
+    return r;
+}
+
+// Bins of d = top - x, finest near the top in proportion (d < 1: 32 an octave
+// down to 2^-12), then 32 a unit to 33, then 32 an octave.
+__device__ __forceinline__ int bin_of(float top, float v)
+{
+    if (v == top) return 0;
+    const float d = top - v;
+    if (d < 1.0f) return d < 0x1p-12f ? 0 : int((__float_as_uint(d) - 0x39800000u) >> 18);
+    if (d < 33.0f) return 384 + int((d - 1.0f) * 32.0f);
+    return min(1408 + int((__float_as_uint(d) - 0x42040000u) >> 18), kBins - 1);
+}
+
+template <class T>
+struct ScanSpace {
+    T wave[kWaves];
+};
+
+// Inclusive sums over the block in thread order, a fixed tree; the total in *total.
+template <class T>
+__device__ __forceinline__ T scan(ScanSpace<T>& s, T v, T* total)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const T o = __shfl_up(v, off, 64);
+        if (lane >= off) v += o;
+    }
+    __syncthreads();
+    if (lane == 63) s.wave[wave] = v;
+    __syncthreads();
+    T before = T(0), all = T(0);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w == wave) before = all;
+        all += s.wave[w];
+    }
+    *total = all;
+    return before + v;
 }
 
 struct Shared {
     unsigned long long weight[kBins];
     unsigned int count[kBins];
-    unsigned long long key[kWaves];
-    double wave_sum[kWaves];
-    unsigned int wave_cnt[kWaves];
-    uint32_t prefix;
-    uint64_t above_count, above_weight, in_bin;
-    int64_t pick;
+    ScanSpace<double> d;
+    ScanSpace<unsigned long long> u;
+    ScanSpace<unsigned int> n;
+    unsigned long long best[kWaves];
+    unsigned long long above_weight, sum_k, cut, pick;
+    unsigned int above_count, in_bin;
+    int bin, bin2, flag;
 };
 
-// The last kept key of a cut: by count (the k-th element) or by weight (the
-// last one whose preceding weight is below `limit`).  Three passes over the
-// key's 11, 11 and 10 bits.
-__device__ void select(Shared& s, const float* x, int64_t N, float top, double t, bool by_count, uint64_t k,
-                       double limit, uint32_t* cut, uint64_t* above_count, uint64_t* above_weight, uint64_t* ties)
+__device__ __forceinline__ uint64_t block_max(Shared& s, uint64_t best)
 {
-    const int bits = weight_bits(N);
+#pragma unroll
+    for (int off = 32; off; off >>= 1) best = max_key(best, __shfl_xor((unsigned long long)best, off, 64));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) s.best[threadIdx.x >> 6] = best;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) best = max_key(best, s.best[w]);
+    return best;
+}
+
+// ------------------------------------------------ one work-group for a row
+
+// The last kept key of a cut, by count (the k-th token) or by weight (the last
+// one whose preceding weight is below `limit`): three passes over the order's
+// 11, 11 and 10 bits.
+__device__ void select(Shared& s, const Row& r, const float* x, bool by_count, uint64_t k, double limit, uint32_t* cut,
+                       uint64_t* above_count, uint64_t* above_weight, uint64_t* ties)
+{
     uint32_t prefix = 0, known = 0;
     uint64_t ac = 0, aw = 0;
     for (int level = 0; level < 3; ++level) {
-        const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
-        const int width = level == 2 ? 10 : 11;
-        for (int i = threadIdx.x; i < kBins; i += kThreads) s.weight[i] = 0, s.count[i] = 0;
+        const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, width = level == 2 ? 10 : 11;
         __syncthreads();
-        for (int64_t i = threadIdx.x; i < N; i += kThreads) {
+        for (int i = threadIdx.x; i < kBins; i += kThreads) s.weight[i] = 0, s.count[i] = 0;
+        if (threadIdx.x == 0) s.bin = -1;
+        __syncthreads();
+        for (int64_t i = threadIdx.x; i < r.N; i += kThreads) {
             const float v = x[i];
             const uint32_t o = order_of(v);
             if ((o & known) != prefix) continue;
             const int bin = int((o >> shift) & ((1u << width) - 1));
             atomicAdd(&s.count[bin], 1u);
-            const double w = weight_of(v, top, t);
-            atomicAdd(&s.weight[bin], (unsigned long long)(ldexp(w, bits) + 0.5));
+            atomicAdd(&s.weight[bin], r.fixed(Row::weight(r.exponent(v))));
         }
         __syncthreads();
-        if (threadIdx.x == 0) {
-            uint64_t c = ac, w = aw;
-            int found = -1;
-            uint64_t fc = 0, fw = 0;
-            for (int bin = kBins - 1; bin >= 0; --bin) {
-                if (!s.count[bin]) continue;
-                if (by_count ? c >= k : (found >= 0 && !(double(w) < limit))) break;
-                found = bin, fc = c, fw = w;
-                c += s.count[bin];
-                w += s.weight[bin];
-            }
-            s.prefix = prefix | (uint32_t(found) << shift);
-            s.above_count = fc;
-            s.above_weight = fw;
-            s.in_bin = s.count[found];
+        // thread t holds bins kBins - 1 - 2 t and the one below: descending
+        const int hi = kBins - 1 - 2 * threadIdx.x, lo = hi - 1;
+        const unsigned int c0 = s.count[hi], c1 = s.count[lo];
+        const unsigned long long w0 = s.weight[hi], w1 = s.weight[lo];
+        unsigned int call;
+        unsigned long long wall;
+        const uint64_t cb = ac + scan(s.n, c0 + c1, &call) - (c0 + c1);
+        const uint64_t wb = aw + scan(s.u, w0 + w1, &wall) - (w0 + w1);
+        // the last bin (lowest) with something in it that begins inside the cut
+        const auto inside = [&](uint64_t c, uint64_t w) { return by_count ? c < k : c == 0 || double(w) < limit; };
+        int mine = -1;
+        if (c0 && inside(cb, wb)) mine = 2 * threadIdx.x;
+        if (c1 && inside(cb + c0, wb + w0)) mine = 2 * threadIdx.x + 1;
+        if (mine >= 0) atomicMax(&s.bin, mine);
+        __syncthreads();
+        const int at = s.bin;
+        if (at >> 1 == int(threadIdx.x)) {
+            s.above_count = unsigned(at & 1 ? cb + c0 : cb);
+            s.above_weight = at & 1 ? wb + w0 : wb;
+            s.in_bin = at & 1 ? c1 : c0;
         }
         __syncthreads();
-        prefix = s.prefix;
+        prefix |= uint32_t(kBins - 1 - at) << shift;
         known |= ((1u << width) - 1) << shift;
-        ac = s.above_count, aw = s.above_weight;
-        *ties = s.in_bin;
-        __syncthreads();
+        ac = s.above_count, aw = s.above_weight, *ties = s.in_bin;
     }
     *cut = prefix;
     *above_count = ac;
     *above_weight = aw;
 }
 
-// Inclusive sums over the block in thread order; total of all in *total.
-__device__ double scan(Shared& s, double v, double* total)
+// The row's cut as a key.
+__device__ uint64_t cut_by_selection(Shared& s, const Row& r, const float* x)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int off = 1; off < 64; off <<= 1) {
-        const double o = __shfl_up(v, off, 64);
-        if (lane >= off) v += o;
-    }
-    if (lane == 63) s.wave_sum[wave] = v;
-    __syncthreads();
-    double before = 0.0, all = 0.0;
-    for (int w = 0; w < kWaves; ++w) {
-        if (w == wave) before = all;
-        all += s.wave_sum[w];
-    }
-    __syncthreads();
-    *total = all;
-    return before + v;
-}
-
-__global__ __launch_bounds__(kThreads) void sample_rows(SampleParams p)
-{
-    __shared__ Shared s;
-    const int64_t row = blockIdx.x;
-    const float* x = p.x + row * p.ldx;
-    const int64_t N = p.N;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint64_t best = 0;
-    for (int64_t i = threadIdx.x; i < N; i += kThreads) best = max_key(best, argmax_key(x[i], uint32_t(i)));
-    for (int off = 32; off; off >>= 1) best = max_key(best, __shfl_xor((unsigned long long)best, off, 64));
-    if (lane == 0) s.key[wave] = best;
-    __syncthreads();
-    for (int w = 0; w < kWaves; ++w) best = max_key(best, s.key[w]);
-    const int32_t top_idx = key_index(best);
-    const float top = x[top_idx];
-    const float temp = p.temperature ? p.temperature[row] : 1.0f;
-    // greedy, or nothing to weigh: a NaN wins, and a row of -inf gives its first
-    if (!(temp > 0.0f) || top != top || top == -INFINITY) {
-        if (threadIdx.x == 0) p.idx[row] = top_idx;
-        return;
-    }
-    const double t = temp;
-    const int bits = weight_bits(N);
-    const int64_t k = p.top_k && p.top_k[row] > 0 ? min(int64_t(p.top_k[row]), N) : N;
-    const float top_p = p.top_p ? p.top_p[row] : 1.0f;
-    const float min_p = p.min_p ? p.min_p[row] : 0.0f;
     uint32_t cut = 0;
-    uint64_t kept_ties = N, ties = N;
-    double sum = -1.0;
-    __syncthreads();
-    if (k < N) {
+    uint64_t kept = uint64_t(r.N), ties = uint64_t(r.N);
+    uint64_t sum = 0;
+    if (r.k < r.N) {
         uint64_t ac, aw;
-        select(s, x, N, top, t, true, uint64_t(k), 0.0, &cut, &ac, &aw, &ties);
-        kept_ties = uint64_t(k) - ac;
-        const uint32_t raw = (cut & 0x80000000u) ? cut & 0x7fffffffu : ~cut;
-        const uint64_t w = (unsigned long long)(ldexp(weight_of(__uint_as_float(raw), top, t), bits) + 0.5);
-        sum = double(aw + w * kept_ties);
+        select(s, r, x, true, uint64_t(r.k), 0.0, &cut, &ac, &aw, &ties);
+        kept = uint64_t(r.k) - ac;
+        sum = aw + kept * r.fixed(Row::weight(r.exponent(value_of(cut))));
     }
-    if (top_p < 1.0f) {
-        if (sum < 0.0) {
-            // the whole row's weight, in the same fixed point
-            if (threadIdx.x == 0) s.above_weight = 0;
-            __syncthreads();
-            unsigned long long mine = 0;
-            for (int64_t i = threadIdx.x; i < N; i += kThreads)
-                mine += (unsigned long long)(ldexp(weight_of(x[i], top, t), bits) + 0.5);
-            atomicAdd((unsigned long long*)&s.above_weight, mine);
-            __syncthreads();
-            sum = double(s.above_weight);
-            __syncthreads();
+    if (r.top_p < 1.0) {
+        if (r.k >= r.N) {
+            unsigned long long mine = 0, all;
+            for (int64_t i = threadIdx.x; i < r.N; i += kThreads) mine += r.fixed(Row::weight(r.exponent(x[i])));
+            scan(s.u, mine, &all);
+            sum = all;
         }
         uint32_t pcut;
         uint64_t ac, aw, pties;
-        const double limit = double(top_p) * sum;
-        select(s, x, N, top, t, false, 0, limit, &pcut, &ac, &aw, &pties);
-        const uint32_t raw = (pcut & 0x80000000u) ? pcut & 0x7fffffffu : ~pcut;
-        const uint64_t w = (unsigned long long)(ldexp(weight_of(__uint_as_float(raw), top, t), bits) + 0.5);
+        const double limit = r.top_p * double(sum);
+        select(s, r, x, false, 0, limit, &pcut, &ac, &aw, &pties);
+        const uint64_t w = r.fixed(Row::weight(r.exponent(value_of(pcut))));
         // ties j = 0, 1, ... are kept while the weight before them is below the limit
         uint64_t lo = 1, hi = pties;
         while (lo < hi) {
@@ -183,90 +284,446 @@ __global__ __launch_bounds__(kThreads) void sample_rows(SampleParams p)
             if (double(aw + w * (mid - 1)) < limit) lo = mid;
             else hi = mid - 1;
         }
-        if (pcut > cut || (pcut == cut && lo < kept_ties)) cut = pcut, kept_ties = lo, ties = pties;
+        if (pcut > cut || (pcut == cut && lo < kept)) cut = pcut, kept = lo, ties = pties;
     }
-    // Index of the last tie kept.
-    int64_t last_tie = N;
-    if (kept_ties < ties) {
-        uint64_t seen = 0;
-        for (int64_t base = 0; base < N && last_tie == N; base += kTile) {
-            int mine = 0;
-            for (int j = 0; j < 4; ++j) {
-                const int64_t i = base + threadIdx.x * 4 + j;
-                if (i < N && order_of(x[i]) == cut) ++mine;
-            }
-            double total;
-            const uint64_t upto = seen + uint64_t(scan(s, double(mine), &total));
-            if (threadIdx.x == 0) s.pick = N;
-            __syncthreads();
-            uint64_t at = upto - mine;
-            for (int j = 0; j < 4; ++j) {
-                const int64_t i = base + threadIdx.x * 4 + j;
-                if (i < N && order_of(x[i]) == cut && ++at == kept_ties) s.pick = i;
-            }
-            __syncthreads();
-            last_tie = s.pick;
-            seen += uint64_t(total);
-            __syncthreads();
-        }
+    if (kept >= ties) return uint64_t(cut) << 32;
+    // index of the last tie kept
+    uint64_t seen = 0;
+    for (int64_t base = 0; base < r.N; base += kThreads) {
+        const int64_t i = base + threadIdx.x;
+        const unsigned int is = i < r.N && order_of(x[i]) == cut;
+        unsigned int all;
+        const uint64_t upto = seen + scan(s.n, is, &all);
+        if (is && upto == kept) s.cut = uint64_t(cut) << 32 | uint64_t(~uint32_t(i));
+        seen += all;
+        if (seen >= kept) break;
     }
-    const double floor_w = min_p != min_p ? 0.0 : fmin(double(min_p), 1.0);
-    const double u = p.u[row];
-    auto kept = [&](int64_t i) -> double {
-        if (i >= N) return 0.0;
-        const uint32_t o = order_of(x[i]);
-        if (o < cut || (o == cut && i > last_tie)) return 0.0;
-        const double w = weight_of(x[i], top, t);
-        return w >= floor_w ? w : 0.0;
+    __syncthreads();
+    return s.cut;
+}
+
+// The token of [from, to) where the running sum of kept weights, from `run`
+// on, passes `target`; r.N if none does.  `cut` is the kept tokens' key.
+// Groups of 64 q tokens are summed by a wave each, then one wave walks the
+// group that holds the token.  *sum: the kept weight of the range.
+__device__ int64_t walk(Shared& s, const Row& r, const float* x, int64_t from, int64_t to, uint64_t cut, double run,
+                        double target, bool must, double* sum)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    double* group_sum = reinterpret_cast<double*>(s.weight);      // kThreads of them
+    const int64_t q = (to - from + 64 * kThreads - 1) / (64 * kThreads), size = 64 * q;
+    const auto weight = [&](int64_t i) {
+        if (i >= to) return 0.0;
+        const float v = x[i];
+        return argmax_key(v, uint32_t(i)) >= cut ? r.drawn(v) : 0.0;
     };
-    double all = 0.0;
-    for (int64_t base = 0; base < N; base += kTile) {
-        double mine = 0.0, total;
-        for (int j = 0; j < 4; ++j) mine += kept(base + threadIdx.x * 4 + j);
-        scan(s, mine, &total);
-        all += total;
+    __syncthreads();
+    for (int g = wave; g < kThreads; g += kWaves) {
+        double w = 0.0;
+        if (from + g * size < to)
+            for (int64_t j = 0; j < q; ++j) w += weight(from + g * size + j * 64 + lane);
+#pragma unroll
+        for (int off = 32; off; off >>= 1) w += __shfl_xor(w, off, 64);
+        if (lane == 0) group_sum[g] = w;
     }
-    const double target = u * all;
-    double run = 0.0;
-    for (int64_t base = 0; base < N; base += kTile) {
-        double w[4], mine = 0.0, total;
-        for (int j = 0; j < 4; ++j) mine += w[j] = kept(base + threadIdx.x * 4 + j);
-        const double upto = scan(s, mine, &total);
-        if (run + total > target) {
-            if (threadIdx.x == 0) s.pick = N;
-            __syncthreads();
-            double cum = run + (upto - mine);
-            int64_t pick = N;
-            for (int j = 3; j >= 0; --j) {
-                double c = cum;
-                for (int q = 0; q <= j; ++q) c += w[q];
-                if (w[j] > 0.0 && c > target) pick = base + threadIdx.x * 4 + j;
+    if (threadIdx.x == 0) s.bin = kThreads, s.bin2 = -1, s.pick = (unsigned long long)r.N;
+    __syncthreads();
+    double all;
+    const double mine = group_sum[threadIdx.x];
+    const double upto = scan(s.d, mine, &all);
+    *sum = all;
+    if (mine > 0.0 && run + upto > target) atomicMin(&s.bin, int(threadIdx.x));
+    if (mine > 0.0) atomicMax(&s.bin2, int(threadIdx.x));         // the last group with a kept token
+    __syncthreads();
+    int g = s.bin;
+    if (g == kThreads) {
+        if (!must || s.bin2 < 0) return r.N;
+        g = s.bin2;                                               // rounding left the target past the end
+    }
+    if (int(threadIdx.x) == g) s.d.wave[0] = run + (upto - mine);
+    __syncthreads();
+    if (wave == 0) {
+        double cum = s.d.wave[0];
+        int64_t last = r.N, found = r.N;
+        for (int64_t j = 0; j < q && found == r.N; ++j) {
+            const int64_t i = from + g * size + j * 64 + lane;
+            double w = weight(i), v = w;
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                const double o = __shfl_up(v, off, 64);
+                if (lane >= off) v += o;
             }
-            if (pick < N) atomicMin((unsigned long long*)&s.pick, (unsigned long long)pick);
-            __syncthreads();
-            if (s.pick < N) {
-                if (threadIdx.x == 0) p.idx[row] = int32_t(s.pick);
-                return;
+            const uint64_t past = __ballot(w > 0.0 && cum + v > target), some = __ballot(w > 0.0);
+            const int64_t base = i - lane;
+            if (past) found = base + __ffsll((unsigned long long)past) - 1;
+            if (some) last = base + 63 - __clzll((long long)some);
+            cum += __shfl(v, 63, 64);
+        }
+        if (lane == 0) s.pick = (unsigned long long)(found < r.N ? found : last);
+    }
+    __syncthreads();
+    return int64_t(s.pick);
+}
+
+__device__ void draw_by_one(Shared& s, const SampleParams& p, int64_t row, const Row& r)
+{
+    const float* x = p.x + row * p.ldx;
+    const uint64_t cut = r.cut() ? cut_by_selection(s, r, x) : 0;
+    double all, sum;
+    const double u = p.u[row];
+    walk(s, r, x, 0, r.N, cut, 0.0, INFINITY, false, &all);
+    int64_t pick = r.N;
+    if (u < 1.0) pick = walk(s, r, x, 0, r.N, cut, 0.0, u * all, true, &sum);
+    if (threadIdx.x == 0) p.idx[row] = pick < r.N ? int32_t(pick) : r.top_idx;
+}
+
+__global__ __launch_bounds__(kThreads) void sample_small(SampleParams p)
+{
+    __shared__ Shared s;
+    const int64_t row = blockIdx.x;
+    const float* x = p.x + row * p.ldx;
+    uint64_t best = 0;
+    for (int64_t i = threadIdx.x; i < p.N; i += kThreads) best = max_key(best, argmax_key(x[i], uint32_t(i)));
+    const Row r = row_of(p, row, block_max(s, best));
+    if (r.greedy) {
+        if (threadIdx.x == 0) p.idx[row] = r.top_idx;
+        return;
+    }
+    draw_by_one(s, p, row, r);
+}
+
+// ------------------------------------------------------------ three launches
+
+__device__ __forceinline__ void chunk_of(const SampleParams& p, int64_t* from, int64_t* to)
+{
+    const int64_t size = (p.N + gridDim.x - 1) / gridDim.x;
+    *from = min(p.N, blockIdx.x * size);
+    *to = min(p.N, *from + size);
+}
+
+__global__ __launch_bounds__(kThreads) void sample_top(SampleParams p)
+{
+    __shared__ Shared s;
+    const int64_t row = blockIdx.y;
+    RowSpace& ws = static_cast<RowSpace*>(p.workspace)[row];
+    const float* x = p.x + row * p.ldx;
+    int64_t from, to;
+    chunk_of(p, &from, &to);
+    uint64_t best = 0;
+#pragma unroll 4
+    for (int64_t i = from + threadIdx.x; i < to; i += kThreads) best = max_key(best, argmax_key(x[i], uint32_t(i)));
+    // the row's histogram and counters begin at zero for the launches below
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < kBins; i += gridDim.x * kThreads) ws.weight[i] = 0, ws.count[i] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) ws.candidates = 0, ws.arrived = 0;
+    best = block_max(s, best);
+    if (threadIdx.x == 0) ws.key[blockIdx.x] = best;
+}
+
+// The row's largest key from its chunks' (at most 64).
+__device__ __forceinline__ uint64_t row_best(const RowSpace& ws)
+{
+    const int lane = threadIdx.x & 63;
+    uint64_t best = lane < int(gridDim.x) ? ws.key[lane] : 0;
+#pragma unroll
+    for (int off = 32; off; off >>= 1) best = max_key(best, __shfl_xor((unsigned long long)best, off, 64));
+    return best;
+}
+
+__global__ __launch_bounds__(kThreads) void sample_histogram(SampleParams p)
+{
+    __shared__ unsigned long long weight[kBins];
+    __shared__ unsigned int count[kBins];
+    const int64_t row = blockIdx.y;
+    RowSpace& ws = static_cast<RowSpace*>(p.workspace)[row];
+    const Row r = row_of(p, row, row_best(ws));
+    if (r.greedy || !r.cut()) return;
+    const float* x = p.x + row * p.ldx;
+    for (int i = threadIdx.x; i < kBins; i += kThreads) weight[i] = 0, count[i] = 0;
+    __syncthreads();
+    int64_t from, to;
+    chunk_of(p, &from, &to);
+    const bool weigh = r.top_p < 1.0;
+#pragma unroll 2
+    for (int64_t i = from + threadIdx.x; i < to; i += kThreads) {
+        const float v = x[i];
+        const double y = r.exponent(v);
+        if (Row::nothing(y)) continue;
+        const int bin = bin_of(r.top, v);
+        atomicAdd(&count[bin], 1u);
+        if (weigh) atomicAdd(&weight[bin], r.fixed(Row::weight(y)));
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBins; i += kThreads)
+        if (count[i]) {
+            atomicAdd(&ws.count[i], count[i]);
+            if (weigh) atomicAdd(&ws.weight[i], weight[i]);
+        }
+}
+
+__device__ __forceinline__ void put(unsigned long long* p, unsigned long long v)
+{
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ unsigned long long get(const unsigned long long* p)
+{
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Bins that the cuts fall into: tokens of bins below `first` are kept,
+// candidates are in [first, second] or in `kbin`.
+struct Bins {
+    int first, second, kbin;
+    uint64_t first_count, first_weight;   // before bin `first`
+    uint64_t k_count, k_weight;           // before bin `kbin`
+    uint64_t total_weight;
+    bool by_k;                            // top-k takes tokens away
+};
+
+__device__ Bins find_bins(Shared& s, const Row& r, const RowSpace& ws)
+{
+    Bins b;
+    const int i0 = 2 * threadIdx.x;
+    const unsigned int c0 = ws.count[i0], c1 = ws.count[i0 + 1];
+    const unsigned long long w0 = ws.weight[i0], w1 = ws.weight[i0 + 1];
+    unsigned int call;
+    unsigned long long wall;
+    const unsigned int cb = scan(s.n, c0 + c1, &call) - (c0 + c1);
+    const unsigned long long wb = scan(s.u, w0 + w1, &wall) - (w0 + w1);
+    b.total_weight = wall;
+    b.by_k = uint64_t(r.k) < call;
+    b.kbin = kBins;
+    b.k_count = call, b.k_weight = wall;
+    uint64_t upper = wall;
+    if (b.by_k) {
+        for (int e = 0; e < 2; ++e) {
+            const uint64_t c = e ? cb + c0 : cb, n = e ? c1 : c0;
+            if (c < uint64_t(r.k) && uint64_t(r.k) <= c + n) {
+                s.bin = i0 + e;
+                s.above_count = unsigned(c);
+                s.above_weight = e ? wb + w0 : wb;
+                s.sum_k = e ? wb + w0 + w1 : wb + w0;
             }
         }
-        run += total;
+        __syncthreads();
+        b.kbin = s.bin;
+        b.k_count = s.above_count;
+        b.k_weight = s.above_weight;
+        upper = s.sum_k;
+    }
+    b.first = b.second = b.kbin;
+    b.first_count = b.k_count, b.first_weight = b.k_weight;
+    if (r.top_p < 1.0) {
+        // the sum that top-p refers to lies between these, its last bin then too
+        const double lo = r.top_p * double(b.by_k ? b.k_weight : wall), hi = r.top_p * double(upper);
+        __syncthreads();
+        if (threadIdx.x == 0) s.bin = 0, s.bin2 = 0;
+        __syncthreads();
+        for (int e = 0; e < 2; ++e) {
+            if (!(e ? c1 : c0)) continue;
+            const double w = double(e ? wb + w0 : wb);
+            if (w < lo) atomicMax(&s.bin, i0 + e);
+            if (w < hi) atomicMax(&s.bin2, i0 + e);
+        }
+        __syncthreads();
+        b.first = s.bin, b.second = s.bin2;
+        if (b.first >> 1 == int(threadIdx.x)) {
+            s.above_count = b.first & 1 ? cb + c0 : cb;
+            s.above_weight = b.first & 1 ? wb + w0 : wb;
+        }
+        __syncthreads();
+        b.first_count = s.above_count, b.first_weight = s.above_weight;
+    }
+    return b;
+}
+
+// The cut's key from the row's candidates.  Candidates of one bin range are
+// ranked by comparing each with all (keys differ): their rank and the weight
+// before them in the row's order follow from what the histogram holds before.
+__device__ uint64_t cut_of_candidates(Shared& s, const Row& r, const Bins& b, const unsigned long long* key, int n)
+{
+    constexpr int kEach = kCandidates / kThreads;
+    unsigned long long mine[kEach], before[kEach], w[kEach];
+    unsigned int greater[kEach];
+    bool in_k[kEach], in_p[kEach];
+    unsigned long long* weight = s.weight;      // kBins entries hold half of the list at a time
+    unsigned int range = 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const int i = e * kThreads + threadIdx.x;
+        mine[e] = i < n ? key[i] : 0;
+        before[e] = 0;
+        greater[e] = 0;
+        const float v = value_of(uint32_t(mine[e] >> 32));
+        w[e] = i < n ? r.fixed(Row::weight(r.exponent(v))) : 0;
+        const int bin = i < n ? bin_of(r.top, v) : -1;
+        in_k[e] = bin == b.kbin;
+        in_p[e] = i < n && bin >= b.first && bin <= b.second;
+        range += in_p[e];
+    }
+    unsigned int in_range;
+    scan(s.n, range, &in_range);
+    for (int base = 0; base < n; base += kBins) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int i = e * kThreads + threadIdx.x - base;
+            if (i >= 0 && i < kBins) weight[i] = w[e];
+        }
+        __syncthreads();
+        const int m = min(kBins, n - base);
+#pragma unroll 4
+        for (int j = 0; j < m; ++j) {
+            const unsigned long long o = key[base + j], ow = weight[j];
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+                if (e * kThreads >= n) break;
+                const bool g = o > mine[e];
+                greater[e] += g;
+                before[e] += g ? ow : 0;
+            }
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) s.sum_k = b.by_k ? b.k_weight : b.total_weight, s.cut = ~0ull, s.flag = 0;
+    __syncthreads();
+    uint64_t rank[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        rank[e] = in_p[e] ? b.first_count + greater[e] : b.k_count + greater[e] - in_range;
+        if (b.by_k && in_k[e] && rank[e] < uint64_t(r.k)) atomicAdd(&s.sum_k, w[e]);
+    }
+    __syncthreads();
+    const double limit = r.top_p * double(s.sum_k);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const bool keep = in_p[e] && rank[e] < uint64_t(r.k) &&
+                          (r.top_p >= 1.0 || rank[e] == 0 || double(b.first_weight + before[e]) < limit);
+        if (keep) atomicMin(&s.cut, mine[e]);
+    }
+    __syncthreads();
+    return s.cut;
+}
+
+__global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p)
+{
+    __shared__ Shared s;
+    __shared__ unsigned long long key[kCandidates];
+    __shared__ double chunk_sum[kMaxChunks];
+    const int64_t row = blockIdx.y;
+    RowSpace& ws = static_cast<RowSpace*>(p.workspace)[row];
+    const Row r = row_of(p, row, row_best(ws));
+    if (r.greedy) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) p.idx[row] = r.top_idx;
+        return;
+    }
+    const float* x = p.x + row * p.ldx;
+    int64_t from, to;
+    chunk_of(p, &from, &to);
+    Bins b;
+    b.first = b.second = b.kbin = kBins;
+    b.by_k = false;
+    const bool cut = r.cut();
+    if (cut) b = find_bins(s, r, ws);
+    double mine = 0.0;
+#pragma unroll 2
+    for (int64_t i = from + threadIdx.x; i < to; i += kThreads) {
+        const float v = x[i];
+        const int bin = cut ? bin_of(r.top, v) : 0;
+        if (bin < b.first) {
+            mine += r.drawn(v);
+        } else if ((bin <= b.second || bin == b.kbin) && !Row::nothing(r.exponent(v))) {
+            const unsigned int at = atomicAdd(&ws.candidates, 1u);
+            if (at < kCandidates) put(&ws.candidate[at], argmax_key(v, uint32_t(i)));
+        }
+    }
+    double all;
+    scan(s.d, mine, &all);
+    if (threadIdx.x == 0) put(&ws.sum[blockIdx.x], (unsigned long long)__double_as_longlong(all));
+    // every store of the work-group is at the device-wide level before it counts itself
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) s.flag = atomicAdd(&ws.arrived, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!s.flag) return;
+
+    // ---- the row's last work-group
+    const unsigned int n = __hip_atomic_load(&ws.candidates, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (n > kCandidates) {
+        draw_by_one(s, p, row, r);
+        return;
+    }
+    for (int i = threadIdx.x; i < int(n); i += kThreads) key[i] = get(&ws.candidate[i]);
+    if (threadIdx.x < gridDim.x)
+        chunk_sum[threadIdx.x] = __longlong_as_double((long long)get(&ws.sum[threadIdx.x]));
+    __syncthreads();
+    const uint64_t last = n ? cut_of_candidates(s, r, b, key, int(n)) : 0;
+    // kept candidates join their chunks' sums, a wave a chunk
+    const int64_t size = (p.N + gridDim.x - 1) / gridDim.x;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __syncthreads();
+    double* kept = reinterpret_cast<double*>(s.weight);
+    int* chunk = reinterpret_cast<int*>(s.count);
+    for (int base = 0; base < int(n); base += kBins) {
+        const int m = min(kBins, int(n) - base);
+        for (int i = threadIdx.x; i < m; i += kThreads) {
+            const unsigned long long k = key[base + i];
+            kept[i] = k >= last ? r.drawn(value_of(uint32_t(k >> 32))) : 0.0;
+            chunk[i] = int(int64_t(~uint32_t(k)) / size);
+        }
+        __syncthreads();
+        for (int c = wave; c < int(gridDim.x); c += kWaves) {
+            // the list's order differs from run to run: in fixed point, where
+            // the smallest kept weight still counts
+            unsigned long long sum = 0;
+            for (int i = lane; i < m; i += 64)
+                if (chunk[i] == c && kept[i] > 0.0) sum += max(1ull, r.fixed(kept[i]));
+#pragma unroll
+            for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
+            if (lane == 0) chunk_sum[c] += ldexp(double(sum), -r.bits);
+        }
         __syncthreads();
     }
-    // u of 1 or more, or a NaN: the most likely token
-    if (threadIdx.x == 0) p.idx[row] = top_idx;
+    const double u = p.u[row];
+    double total = 0.0;
+    for (int c = 0; c < int(gridDim.x); ++c) total += chunk_sum[c];
+    int64_t pick = p.N;
+    if (u < 1.0) {
+        const double target = u * total;
+        double run = 0.0;
+        for (int c = 0; c < int(gridDim.x) && pick == p.N; ++c) {
+            if (run + chunk_sum[c] > target) {
+                double sum;
+                const int64_t f = min(p.N, c * size);
+                pick = walk(s, r, x, f, min(p.N, f + size), last, run, target, true, &sum);
+            }
+            run += chunk_sum[c];
+        }
+    }
+    if (threadIdx.x == 0) p.idx[row] = pick < p.N ? int32_t(pick) : r.top_idx;
 }
 
 }  // namespace
 
 size_t sample_workspace_bytes(int64_t m, int64_t N)
 {
-    (void)m, (void)N;
-    return 256;
+    return N <= kSmallRow || m == 0 ? 256 : size_t(m) * sizeof(RowSpace);
 }
 
 hipError_t launch_sample(const SampleParams& p, hipStream_t s)
 {
-    hipLaunchKernelGGL(sample_rows, dim3(unsigned(p.m)), dim3(kThreads), 0, s, p);
+    if (p.N <= kSmallRow) {
+        hipLaunchKernelGGL(sample_small, dim3(unsigned(p.m)), dim3(kThreads), 0, s, p);
+        return hipGetLastError();
+    }
+    // about as many chunks as the chip holds work-groups, of at least 4096 logits
+    int64_t chunks = (p.N + 4095) / 4096;
+    const int64_t fit = (kResident + p.m - 1) / p.m;
+    if (chunks > fit) chunks = fit;
+    if (chunks > kMaxChunks) chunks = kMaxChunks;
+    const dim3 grid{unsigned(chunks), unsigned(p.m), 1};
+    hipLaunchKernelGGL(sample_top, grid, dim3(kThreads), 0, s, p);
+    if (p.top_k || p.top_p) hipLaunchKernelGGL(sample_histogram, grid, dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL(sample_draw, grid, dim3(kThreads), 0, s, p);
     return hipGetLastError();
 }
 
