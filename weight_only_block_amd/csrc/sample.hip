@@ -18,9 +18,10 @@
 //      gives the key, adds the kept ones to their chunks' sums, finds the
 //      chunk that the uniform number falls into and the token in it.
 // Bound by reading the logits (64 rows of 151936: 39 MB) and, for few rows, by
-// the launches' latency.  Rows of up to 8192 logits, and rows whose cut falls
-// into a bin of more than 4096 tokens (many nearly equal logits), are done by
-// one work-group, which finds the key by a radix selection.
+// the launches' latency.  Rows of up to 8192 logits, and rows of any length
+// where there are 512 and more, are a work-group's each, with all steps in one
+// launch.  A row whose cut falls into bins of more than 4096 tokens (many
+// nearly equal logits) gets its key by a radix selection over the row.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -39,7 +40,32 @@ constexpr int kMaxChunks = 64;
 constexpr int64_t kSmallRow = 8192;        // one work-group at once
 constexpr int64_t kResident = 512;         // work-groups the chip holds at once
 
-// Row r's part of the workspace.
+// How a row is divided: chunks of a work-group each, groups of 256 q tokens,
+// at most 1024 a chunk, whose kept weight is remembered so that only one of
+// them is read again for the draw.
+struct Division {
+    int64_t chunk, group;
+    int chunks, groups;       // groups of a chunk
+};
+
+__host__ __device__ inline Division division(int64_t m, int64_t N)
+{
+    Division d;
+    // about as many chunks as the chip holds work-groups, of at least 4096 logits
+    int64_t chunks = (N + 4095) / 4096;
+    const int64_t fit = (kResident + m - 1) / m;
+    if (chunks > fit) chunks = fit;
+    if (chunks > kMaxChunks) chunks = kMaxChunks;
+    if (N <= kSmallRow) chunks = 1;
+    const int64_t size = (N + chunks - 1) / chunks;
+    d.group = 256 * ((size + 256 * kThreads - 1) / (256 * kThreads));
+    d.groups = int((size + d.group - 1) / d.group);
+    d.chunk = d.group * d.groups;
+    d.chunks = int((N + d.chunk - 1) / d.chunk);
+    return d;
+}
+
+// Row r's part of the workspace; the groups' sums of all rows follow the last.
 struct RowSpace {
     unsigned long long weight[kBins];
     unsigned int count[kBins];
@@ -120,7 +146,7 @@ __device__ __forceinline__ Row row_of(const SampleParams& p, int64_t row, uint64
 {
     Row r;
     r.top_idx = key_index(best);
-    r.top = p.x[row * p.ldx + r.top_idx];
+    r.top = value_of(uint32_t(best >> 32));
     const float t = p.temperature ? p.temperature[row] : 1.0f;
     // greedy, or nothing to weigh: a NaN wins, and a row of -infinity gives its first
     r.greedy = !(t > 0.0f) || r.top != r.top || r.top == -INFINITY;
@@ -171,6 +197,13 @@ __device__ __forceinline__ T scan(ScanSpace<T>& s, T v, T* total)
     }
     *total = all;
     return before + v;
+}
+
+// The largest value of an ascending thread's: that of the wave's last thread that has one.
+__device__ __forceinline__ void wave_max(int* at, int v)
+{
+    const uint64_t some = __ballot(v > 0);
+    if (some && int(threadIdx.x & 63) == 63 - __clzll((long long)some)) atomicMax(at, v);
 }
 
 struct Shared {
@@ -302,62 +335,52 @@ __device__ uint64_t cut_by_selection(Shared& s, const Row& r, const float* x)
     return s.cut;
 }
 
-// The token of [from, to) where the running sum of kept weights, from `run`
-// on, passes `target`; r.N if none does.  `cut` is the kept tokens' key.
-// Groups of 64 q tokens are summed by a wave each, then one wave walks the
-// group that holds the token.  *sum: the kept weight of the range.
-__device__ int64_t walk(Shared& s, const Row& r, const float* x, int64_t from, int64_t to, uint64_t cut, double run,
-                        double target, bool must, double* sum)
+// The group (one a thread, `mine` its kept weight) in which the running sum
+// from `run` on passes `target`, the last one with a kept token if rounding
+// left the target past the end, -1 without any; the sum before it in
+// s.d.wave[0].
+__device__ int pick_group(Shared& s, double mine, double run, double target)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    double* group_sum = reinterpret_cast<double*>(s.weight);      // kThreads of them
-    const int64_t q = (to - from + 64 * kThreads - 1) / (64 * kThreads), size = 64 * q;
-    const auto weight = [&](int64_t i) {
-        if (i >= to) return 0.0;
-        const float v = x[i];
-        return argmax_key(v, uint32_t(i)) >= cut ? r.drawn(v) : 0.0;
-    };
-    __syncthreads();
-    for (int g = wave; g < kThreads; g += kWaves) {
-        double w = 0.0;
-        if (from + g * size < to)
-            for (int64_t j = 0; j < q; ++j) w += weight(from + g * size + j * 64 + lane);
-#pragma unroll
-        for (int off = 32; off; off >>= 1) w += __shfl_xor(w, off, 64);
-        if (lane == 0) group_sum[g] = w;
-    }
-    if (threadIdx.x == 0) s.bin = kThreads, s.bin2 = -1, s.pick = (unsigned long long)r.N;
-    __syncthreads();
+    if (threadIdx.x == 0) s.bin = kThreads, s.bin2 = 0;
     double all;
-    const double mine = group_sum[threadIdx.x];
     const double upto = scan(s.d, mine, &all);
-    *sum = all;
-    if (mine > 0.0 && run + upto > target) atomicMin(&s.bin, int(threadIdx.x));
-    if (mine > 0.0) atomicMax(&s.bin2, int(threadIdx.x));         // the last group with a kept token
+    const uint64_t past = __ballot(mine > 0.0 && run + upto > target);
+    if (past && int(threadIdx.x & 63) == __ffsll((unsigned long long)past) - 1) atomicMin(&s.bin, int(threadIdx.x));
+    wave_max(&s.bin2, mine > 0.0 ? int(threadIdx.x) + 1 : 0);
     __syncthreads();
-    int g = s.bin;
-    if (g == kThreads) {
-        if (!must || s.bin2 < 0) return r.N;
-        g = s.bin2;                                               // rounding left the target past the end
-    }
+    const int g = s.bin < kThreads ? s.bin : s.bin2 - 1;
     if (int(threadIdx.x) == g) s.d.wave[0] = run + (upto - mine);
     __syncthreads();
-    if (wave == 0) {
-        double cum = s.d.wave[0];
+    return g;
+}
+
+// The token of [from, to) where the running sum of kept weights passes
+// `target`, else the last kept one: the first wave takes 64 at a time.
+__device__ int64_t walk_group(Shared& s, const Row& r, const float* x, int64_t from, int64_t to, uint64_t cut, double run,
+                              double target)
+{
+    const int lane = threadIdx.x & 63;
+    if (threadIdx.x < 64) {
         int64_t last = r.N, found = r.N;
-        for (int64_t j = 0; j < q && found == r.N; ++j) {
-            const int64_t i = from + g * size + j * 64 + lane;
-            double w = weight(i), v = w;
+        for (int64_t base = from; base < to && found == r.N; base += 256) {
+            float v[4];
 #pragma unroll
-            for (int off = 1; off < 64; off <<= 1) {
-                const double o = __shfl_up(v, off, 64);
-                if (lane >= off) v += o;
+            for (int e = 0; e < 4; ++e) v[e] = base + 64 * e + lane < to ? x[base + 64 * e + lane] : -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int64_t i = base + 64 * e + lane;
+                const double w = i < to && argmax_key(v[e], uint32_t(i)) >= cut ? r.drawn(v[e]) : 0.0;
+                double upto = w;
+#pragma unroll
+                for (int off = 1; off < 64; off <<= 1) {
+                    const double o = __shfl_up(upto, off, 64);
+                    if (lane >= off) upto += o;
+                }
+                const uint64_t past = __ballot(w > 0.0 && run + upto > target), some = __ballot(w > 0.0);
+                if (past && found == r.N) found = base + 64 * e + __ffsll((unsigned long long)past) - 1;
+                if (some) last = base + 64 * e + 63 - __clzll((long long)some);
+                run += __shfl(upto, 63, 64);
             }
-            const uint64_t past = __ballot(w > 0.0 && cum + v > target), some = __ballot(w > 0.0);
-            const int64_t base = i - lane;
-            if (past) found = base + __ffsll((unsigned long long)past) - 1;
-            if (some) last = base + 63 - __clzll((long long)some);
-            cum += __shfl(v, 63, 64);
         }
         if (lane == 0) s.pick = (unsigned long long)(found < r.N ? found : last);
     }
@@ -365,57 +388,101 @@ __device__ int64_t walk(Shared& s, const Row& r, const float* x, int64_t from, i
     return int64_t(s.pick);
 }
 
-__device__ void draw_by_one(Shared& s, const SampleParams& p, int64_t row, const Row& r)
+// The token of a row in which the running sum of kept weights passes u times
+// their sum; r.N without any.  Groups of 256 q tokens are summed by a wave
+// each, then one wave walks the group that holds the token.
+__device__ int64_t draw_row(Shared& s, const Row& r, const float* x, uint64_t cut, double u)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    double* group_sum = reinterpret_cast<double*>(s.weight);      // kThreads of them
+    const int64_t size = 256 * ((r.N + 256 * kThreads - 1) / (256 * kThreads));
+    const int groups = int((r.N + size - 1) / size);
+    __syncthreads();
+    group_sum[threadIdx.x] = 0.0;
+    __syncthreads();
+    for (int g = wave; g < groups; g += kWaves) {
+        double w = 0.0;
+        for (int64_t base = g * size; base < (g + 1) * size; base += 256) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = base + 64 * e + lane < r.N ? x[base + 64 * e + lane] : -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (base + 64 * e + lane < r.N && argmax_key(v[e], uint32_t(base + 64 * e + lane)) >= cut) w += r.drawn(v[e]);
+        }
+#pragma unroll
+        for (int off = 32; off; off >>= 1) w += __shfl_xor(w, off, 64);
+        if (lane == 0) group_sum[g] = w;
+    }
+    __syncthreads();
+    const double mine = group_sum[threadIdx.x];
+    double all;
+    scan(s.d, mine, &all);
+    const double target = u * all;
+    const int g = pick_group(s, mine, 0.0, target);
+    if (g < 0) return r.N;
+    return walk_group(s, r, x, g * size, min(r.N, (g + 1) * size), cut, s.d.wave[0], target);
+}
+
+__device__ void draw_by_selection(Shared& s, const SampleParams& p, int64_t row, const Row& r)
 {
     const float* x = p.x + row * p.ldx;
     const uint64_t cut = r.cut() ? cut_by_selection(s, r, x) : 0;
-    double all, sum;
     const double u = p.u[row];
-    walk(s, r, x, 0, r.N, cut, 0.0, INFINITY, false, &all);
     int64_t pick = r.N;
-    if (u < 1.0) pick = walk(s, r, x, 0, r.N, cut, 0.0, u * all, true, &sum);
+    if (u < 1.0) pick = draw_row(s, r, x, cut, u);
     if (threadIdx.x == 0) p.idx[row] = pick < r.N ? int32_t(pick) : r.top_idx;
-}
-
-__global__ __launch_bounds__(kThreads) void sample_small(SampleParams p)
-{
-    __shared__ Shared s;
-    const int64_t row = blockIdx.x;
-    const float* x = p.x + row * p.ldx;
-    uint64_t best = 0;
-    for (int64_t i = threadIdx.x; i < p.N; i += kThreads) best = max_key(best, argmax_key(x[i], uint32_t(i)));
-    const Row r = row_of(p, row, block_max(s, best));
-    if (r.greedy) {
-        if (threadIdx.x == 0) p.idx[row] = r.top_idx;
-        return;
-    }
-    draw_by_one(s, p, row, r);
 }
 
 // ------------------------------------------------------------ three launches
 
-__device__ __forceinline__ void chunk_of(const SampleParams& p, int64_t* from, int64_t* to)
+// The largest key of [from, to).
+__device__ __forceinline__ uint64_t top_of(Shared& s, const float* x, int64_t from, int64_t to)
 {
-    const int64_t size = (p.N + gridDim.x - 1) / gridDim.x;
-    *from = min(p.N, blockIdx.x * size);
-    *to = min(p.N, *from + size);
+    uint64_t best = 0;
+    for (int64_t i = from + threadIdx.x; i < to; i += 8 * kThreads) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = i + e * kThreads < to ? x[i + e * kThreads] : -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (i + e * kThreads < to) best = max_key(best, argmax_key(v[e], uint32_t(i + e * kThreads)));
+    }
+    return block_max(s, best);
 }
 
-__global__ __launch_bounds__(kThreads) void sample_top(SampleParams p)
+// Adds [from, to) to the histogram in LDS: counts for top-k, weights for top-p.
+__device__ __forceinline__ void add_to_bins(Shared& s, const Row& r, const float* x, int64_t from, int64_t to)
+{
+    for (int i = threadIdx.x; i < kBins; i += kThreads) s.weight[i] = 0, s.count[i] = 0;
+    __syncthreads();
+    const bool weigh = r.top_p < 1.0, rank = r.k < r.N;
+    for (int64_t i = from + threadIdx.x; i < to; i += 8 * kThreads) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = i + e * kThreads < to ? x[i + e * kThreads] : -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const double y = r.exponent(v[e]);
+            if (Row::nothing(y)) continue;
+            const int bin = bin_of(r.top, v[e]);
+            if (rank) atomicAdd(&s.count[bin], 1u);
+            if (weigh) atomicAdd(&s.weight[bin], r.fixed(Row::weight(y)));
+        }
+    }
+    __syncthreads();
+}
+
+__global__ __launch_bounds__(kThreads) void sample_top(SampleParams p, Division dv)
 {
     __shared__ Shared s;
     const int64_t row = blockIdx.y;
     RowSpace& ws = static_cast<RowSpace*>(p.workspace)[row];
-    const float* x = p.x + row * p.ldx;
-    int64_t from, to;
-    chunk_of(p, &from, &to);
-    uint64_t best = 0;
-#pragma unroll 4
-    for (int64_t i = from + threadIdx.x; i < to; i += kThreads) best = max_key(best, argmax_key(x[i], uint32_t(i)));
+    const int64_t from = blockIdx.x * dv.chunk, to = min(p.N, from + dv.chunk);
     // the row's histogram and counters begin at zero for the launches below
     for (int i = blockIdx.x * kThreads + threadIdx.x; i < kBins; i += gridDim.x * kThreads) ws.weight[i] = 0, ws.count[i] = 0;
     if (blockIdx.x == 0 && threadIdx.x == 0) ws.candidates = 0, ws.arrived = 0;
-    best = block_max(s, best);
+    const uint64_t best = top_of(s, p.x + row * p.ldx, from, to);
     if (threadIdx.x == 0) ws.key[blockIdx.x] = best;
 }
 
@@ -429,35 +496,19 @@ __device__ __forceinline__ uint64_t row_best(const RowSpace& ws)
     return best;
 }
 
-__global__ __launch_bounds__(kThreads) void sample_histogram(SampleParams p)
+__global__ __launch_bounds__(kThreads) void sample_histogram(SampleParams p, Division dv)
 {
-    __shared__ unsigned long long weight[kBins];
-    __shared__ unsigned int count[kBins];
+    __shared__ Shared s;
     const int64_t row = blockIdx.y;
     RowSpace& ws = static_cast<RowSpace*>(p.workspace)[row];
     const Row r = row_of(p, row, row_best(ws));
     if (r.greedy || !r.cut()) return;
-    const float* x = p.x + row * p.ldx;
-    for (int i = threadIdx.x; i < kBins; i += kThreads) weight[i] = 0, count[i] = 0;
-    __syncthreads();
-    int64_t from, to;
-    chunk_of(p, &from, &to);
-    const bool weigh = r.top_p < 1.0;
-#pragma unroll 2
-    for (int64_t i = from + threadIdx.x; i < to; i += kThreads) {
-        const float v = x[i];
-        const double y = r.exponent(v);
-        if (Row::nothing(y)) continue;
-        const int bin = bin_of(r.top, v);
-        atomicAdd(&count[bin], 1u);
-        if (weigh) atomicAdd(&weight[bin], r.fixed(Row::weight(y)));
+    const int64_t from = blockIdx.x * dv.chunk, to = min(p.N, from + dv.chunk);
+    add_to_bins(s, r, p.x + row * p.ldx, from, to);
+    for (int i = threadIdx.x; i < kBins; i += kThreads) {
+        if (s.count[i]) atomicAdd(&ws.count[i], s.count[i]);
+        if (s.weight[i]) atomicAdd(&ws.weight[i], s.weight[i]);
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < kBins; i += kThreads)
-        if (count[i]) {
-            atomicAdd(&ws.count[i], count[i]);
-            if (weigh) atomicAdd(&ws.weight[i], weight[i]);
-        }
 }
 
 __device__ __forceinline__ void put(unsigned long long* p, unsigned long long v)
@@ -479,18 +530,18 @@ struct Bins {
     bool by_k;                            // top-k takes tokens away
 };
 
-__device__ Bins find_bins(Shared& s, const Row& r, const RowSpace& ws)
+__device__ Bins find_bins(Shared& s, const Row& r, const unsigned int* count, const unsigned long long* weight)
 {
     Bins b;
     const int i0 = 2 * threadIdx.x;
-    const unsigned int c0 = ws.count[i0], c1 = ws.count[i0 + 1];
-    const unsigned long long w0 = ws.weight[i0], w1 = ws.weight[i0 + 1];
+    const unsigned int c0 = count[i0], c1 = count[i0 + 1];
+    const unsigned long long w0 = weight[i0], w1 = weight[i0 + 1];
     unsigned int call;
     unsigned long long wall;
     const unsigned int cb = scan(s.n, c0 + c1, &call) - (c0 + c1);
     const unsigned long long wb = scan(s.u, w0 + w1, &wall) - (w0 + w1);
     b.total_weight = wall;
-    b.by_k = uint64_t(r.k) < call;
+    b.by_k = r.k < r.N && uint64_t(r.k) < call;
     b.kbin = kBins;
     b.k_count = call, b.k_weight = wall;
     uint64_t upper = wall;
@@ -518,12 +569,15 @@ __device__ Bins find_bins(Shared& s, const Row& r, const RowSpace& ws)
         __syncthreads();
         if (threadIdx.x == 0) s.bin = 0, s.bin2 = 0;
         __syncthreads();
+        int at_lo = 0, at_hi = 0;
         for (int e = 0; e < 2; ++e) {
-            if (!(e ? c1 : c0)) continue;
+            if (!(e ? w1 : w0)) continue;       // (weights of 0 lie past every limit)
             const double w = double(e ? wb + w0 : wb);
-            if (w < lo) atomicMax(&s.bin, i0 + e);
-            if (w < hi) atomicMax(&s.bin2, i0 + e);
+            if (w < lo) at_lo = i0 + e;
+            if (w < hi) at_hi = i0 + e;
         }
+        wave_max(&s.bin, at_lo);
+        wave_max(&s.bin2, at_hi);
         __syncthreads();
         b.first = s.bin, b.second = s.bin2;
         if (b.first >> 1 == int(threadIdx.x)) {
@@ -536,130 +590,214 @@ __device__ Bins find_bins(Shared& s, const Row& r, const RowSpace& ws)
     return b;
 }
 
-// The cut's key from the row's candidates.  Candidates of one bin range are
-// ranked by comparing each with all (keys differ): their rank and the weight
-// before them in the row's order follow from what the histogram holds before.
-__device__ uint64_t cut_of_candidates(Shared& s, const Row& r, const Bins& b, const unsigned long long* key, int n)
+// Sorts the first n keys (at most kCandidates), largest first, zeros after
+// them, by a bitonic network over the next power of two.  Up to 1024 keys are
+// a register of each thread: comparisons within a wave exchange lanes, the
+// others go through LDS.
+__device__ void sort_keys(unsigned long long* key, int n)
 {
-    constexpr int kEach = kCandidates / kThreads;
-    unsigned long long mine[kEach], before[kEach], w[kEach];
-    unsigned int greater[kEach];
+    int size = 64;
+    while (size < n) size *= 2;
+    for (int i = n + threadIdx.x; i < size; i += kThreads) key[i] = 0;
+    __syncthreads();
+    if (size <= kThreads) {
+        const int i = threadIdx.x;
+        const bool mine = i < size;
+        unsigned long long a = mine ? key[i] : 0;
+        for (int k = 2; k <= size; k *= 2)
+            for (int j = k / 2; j >= 1; j /= 2) {
+                unsigned long long o;
+                if (j >= 64) {
+                    if (mine) key[i] = a;
+                    __syncthreads();
+                    o = mine ? key[i ^ j] : 0;
+                    __syncthreads();
+                } else {
+                    if (!mine) continue;
+                    o = __shfl_xor(a, j, 64);
+                }
+                // the pair's lower place takes the larger key where its run descends
+                const bool larger = ((i & k) == 0) == ((i & j) == 0);
+                a = (o > a) == larger ? o : a;
+            }
+        if (mine) key[i] = a;
+        __syncthreads();
+        return;
+    }
+    for (int k = 2; k <= size; k *= 2)
+        for (int j = k / 2; j >= 1; j /= 2) {
+            for (int t = threadIdx.x; t < size / 2; t += kThreads) {
+                const int i = 2 * t - (t & (j - 1));
+                const unsigned long long a = key[i], b = key[i + j];
+                if ((a < b) == ((i & k) == 0)) key[i] = b, key[i + j] = a;
+            }
+            __syncthreads();
+        }
+}
+
+// The cut's key from the row's candidates: sorted, their ranks and the weight
+// before them in the row's order follow from what the histogram holds before.
+template <int kEach>
+__device__ uint64_t cut_of_candidates(Shared& s, const Row& r, const Bins& b, unsigned long long* key, int n)
+{
+    sort_keys(key, n);
+    unsigned long long w[kEach], sum = 0, all;
     bool in_k[kEach], in_p[kEach];
-    unsigned long long* weight = s.weight;      // kBins entries hold half of the list at a time
-    unsigned int range = 0;
+    int range = 0;
+    const int at = kEach * threadIdx.x;          // this thread's candidates, in order
+    if (threadIdx.x == 0) s.bin = 0, s.sum_k = b.by_k ? b.k_weight : b.total_weight, s.cut = ~0ull;
+    __syncthreads();
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-        const int i = e * kThreads + threadIdx.x;
-        mine[e] = i < n ? key[i] : 0;
-        before[e] = 0;
-        greater[e] = 0;
-        const float v = value_of(uint32_t(mine[e] >> 32));
-        w[e] = i < n ? r.fixed(Row::weight(r.exponent(v))) : 0;
-        const int bin = i < n ? bin_of(r.top, v) : -1;
+        w[e] = 0;
+        in_k[e] = in_p[e] = false;
+        if (at + e >= n) continue;
+        const float v = value_of(uint32_t(key[at + e] >> 32));
+        const int bin = bin_of(r.top, v);
+        w[e] = r.fixed(Row::weight(r.exponent(v)));
         in_k[e] = bin == b.kbin;
-        in_p[e] = i < n && bin >= b.first && bin <= b.second;
-        range += in_p[e];
+        in_p[e] = bin >= b.first && bin <= b.second;
+        if (in_p[e]) range = at + e + 1;
+        sum += w[e];
     }
-    unsigned int in_range;
-    scan(s.n, range, &in_range);
-    for (int base = 0; base < n; base += kBins) {
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-            const int i = e * kThreads + threadIdx.x - base;
-            if (i >= 0 && i < kBins) weight[i] = w[e];
-        }
-        __syncthreads();
-        const int m = min(kBins, n - base);
-#pragma unroll 4
-        for (int j = 0; j < m; ++j) {
-            const unsigned long long o = key[base + j], ow = weight[j];
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                if (e * kThreads >= n) break;
-                const bool g = o > mine[e];
-                greater[e] += g;
-                before[e] += g ? ow : 0;
-            }
-        }
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) s.sum_k = b.by_k ? b.k_weight : b.total_weight, s.cut = ~0ull, s.flag = 0;
-    __syncthreads();
+    wave_max(&s.bin, range);                     // candidates of [first, second], the first ones
+    unsigned long long before = scan(s.u, sum, &all) - sum;
+    const int in_range = s.bin;
     uint64_t rank[kEach];
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-        rank[e] = in_p[e] ? b.first_count + greater[e] : b.k_count + greater[e] - in_range;
+        rank[e] = in_p[e] ? b.first_count + (at + e) : b.k_count + (at + e) - in_range;
         if (b.by_k && in_k[e] && rank[e] < uint64_t(r.k)) atomicAdd(&s.sum_k, w[e]);
     }
     __syncthreads();
     const double limit = r.top_p * double(s.sum_k);
+    int keep = 0;                                // kept candidates come first too
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-        const bool keep = in_p[e] && rank[e] < uint64_t(r.k) &&
-                          (r.top_p >= 1.0 || rank[e] == 0 || double(b.first_weight + before[e]) < limit);
-        if (keep) atomicMin(&s.cut, mine[e]);
+        if (in_p[e] && rank[e] < uint64_t(r.k) &&
+            (r.top_p >= 1.0 || rank[e] == 0 || double(b.first_weight + before) < limit))
+            keep = at + e + 1;
+        before += w[e];
     }
+    if (threadIdx.x == 0) s.bin2 = 0;
     __syncthreads();
-    return s.cut;
+    wave_max(&s.bin2, keep);
+    __syncthreads();
+    return s.bin2 ? key[s.bin2 - 1] : ~0ull;
 }
 
-__global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p)
+// ONE: a work-group has the whole row and does the first two steps as well.
+template <bool ONE>
+__global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p, Division dv)
 {
     __shared__ Shared s;
     __shared__ unsigned long long key[kCandidates];
     __shared__ double chunk_sum[kMaxChunks];
     const int64_t row = blockIdx.y;
-    RowSpace& ws = static_cast<RowSpace*>(p.workspace)[row];
-    const Row r = row_of(p, row, row_best(ws));
+    RowSpace& ws = static_cast<RowSpace*>(p.workspace)[ONE ? 0 : row];
+    const float* x = p.x + row * p.ldx;
+    const int64_t from = blockIdx.x * dv.chunk, to = min(p.N, from + dv.chunk);
+    const Row r = row_of(p, row, ONE ? top_of(s, x, from, to) : row_best(ws));
     if (r.greedy) {
         if (blockIdx.x == 0 && threadIdx.x == 0) p.idx[row] = r.top_idx;
         return;
     }
-    const float* x = p.x + row * p.ldx;
-    int64_t from, to;
-    chunk_of(p, &from, &to);
     Bins b;
     b.first = b.second = b.kbin = kBins;
     b.by_k = false;
     const bool cut = r.cut();
-    if (cut) b = find_bins(s, r, ws);
-    double mine = 0.0;
-#pragma unroll 2
-    for (int64_t i = from + threadIdx.x; i < to; i += kThreads) {
-        const float v = x[i];
-        const int bin = cut ? bin_of(r.top, v) : 0;
-        if (bin < b.first) {
-            mine += r.drawn(v);
-        } else if ((bin <= b.second || bin == b.kbin) && !Row::nothing(r.exponent(v))) {
-            const unsigned int at = atomicAdd(&ws.candidates, 1u);
-            if (at < kCandidates) put(&ws.candidate[at], argmax_key(v, uint32_t(i)));
+    if (cut) {
+        if (ONE) add_to_bins(s, r, x, from, to);
+        b = ONE ? find_bins(s, r, s.count, s.weight) : find_bins(s, r, ws.count, ws.weight);
+    }
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    double* group_sum = reinterpret_cast<double*>(s.weight);      // kThreads of them
+    unsigned long long* groups = reinterpret_cast<unsigned long long*>(static_cast<RowSpace*>(p.workspace) + p.m) +
+                                 (row * gridDim.x + blockIdx.x) * dv.groups;
+    __syncthreads();
+    group_sum[threadIdx.x] = 0.0;
+    __syncthreads();
+    if (threadIdx.x == 0) s.flag = 0;
+    __syncthreads();
+    // Four tokens a lane at a time, the next four on their way meanwhile.
+    const int rounds = int(dv.group / 256);
+    const auto load = [&](int g, int j, float* v) {
+        const int64_t at = from + g * dv.group + j * 256 + lane;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = g < dv.groups && at + 64 * e < to ? x[at + 64 * e] : -INFINITY;
+    };
+    float next[4];
+    load(wave, 0, next);
+    for (int g = wave; g < dv.groups; g += kWaves) {
+        double w = 0.0;
+        for (int j = 0; j < rounds; ++j) {
+            const int64_t at = from + g * dv.group + j * 256 + lane;
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = next[e];
+            if (j + 1 < rounds) load(g, j + 1, next);
+            else load(g + kWaves, 0, next);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int bin = cut ? bin_of(r.top, v[e]) : 0;
+                if (bin < b.first) {
+                    w += r.drawn(v[e]);
+                } else if ((bin <= b.second || bin == b.kbin) && !Row::nothing(r.exponent(v[e]))) {
+                    const int c = atomicAdd(&s.flag, 1);
+                    if (c < kCandidates) key[c] = argmax_key(v[e], uint32_t(at + 64 * e));
+                }
+            }
+        }
+#pragma unroll
+        for (int off = 32; off; off >>= 1) w += __shfl_xor(w, off, 64);
+        if (lane == 0) {
+            group_sum[g] = w;
+            if (!ONE) put(&groups[g], (unsigned long long)__double_as_longlong(w));
         }
     }
+    __syncthreads();
+    // the work-group's candidates join the row's list
+    const int found = s.flag;
+    if (!ONE && found) {
+        if (threadIdx.x == 0) s.in_bin = atomicAdd(&ws.candidates, unsigned(found));
+        __syncthreads();
+        const unsigned int at = s.in_bin;
+        for (int i = threadIdx.x; i < min(found, kCandidates); i += kThreads)
+            if (at + i < unsigned(kCandidates)) put(&ws.candidate[at + i], key[i]);
+    }
+    __syncthreads();
     double all;
-    scan(s.d, mine, &all);
-    if (threadIdx.x == 0) put(&ws.sum[blockIdx.x], (unsigned long long)__double_as_longlong(all));
-    // every store of the work-group is at the device-wide level before it counts itself
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (threadIdx.x == 0) s.flag = atomicAdd(&ws.arrived, 1u) == gridDim.x - 1;
-    __syncthreads();
-    if (!s.flag) return;
+    const double own_group = group_sum[threadIdx.x];
+    scan(s.d, own_group, &all);
+    unsigned int n = unsigned(found);
+    if (!ONE) {
+        if (threadIdx.x == 0) put(&ws.sum[blockIdx.x], (unsigned long long)__double_as_longlong(all));
+        // every store of the work-group is at the device-wide level before it counts itself
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (threadIdx.x == 0) s.flag = atomicAdd(&ws.arrived, 1u) == gridDim.x - 1;
+        __syncthreads();
+        if (!s.flag) return;
+        n = __hip_atomic_load(&ws.candidates, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
 
     // ---- the row's last work-group
-    const unsigned int n = __hip_atomic_load(&ws.candidates, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (n > kCandidates) {
-        draw_by_one(s, p, row, r);
+        draw_by_selection(s, p, row, r);
         return;
     }
-    for (int i = threadIdx.x; i < int(n); i += kThreads) key[i] = get(&ws.candidate[i]);
-    if (threadIdx.x < gridDim.x)
-        chunk_sum[threadIdx.x] = __longlong_as_double((long long)get(&ws.sum[threadIdx.x]));
+    if (!ONE) {
+        for (int i = threadIdx.x; i < int(n); i += kThreads) key[i] = get(&ws.candidate[i]);
+        if (threadIdx.x < gridDim.x)
+            chunk_sum[threadIdx.x] = __longlong_as_double((long long)get(&ws.sum[threadIdx.x]));
+    } else if (threadIdx.x == 0) {
+        chunk_sum[0] = all;
+    }
     __syncthreads();
-    const uint64_t last = n ? cut_of_candidates(s, r, b, key, int(n)) : 0;
+    const uint64_t last = n == 0           ? 0
+                          : n <= kThreads ? cut_of_candidates<1>(s, r, b, key, int(n))
+                                          : cut_of_candidates<kCandidates / kThreads>(s, r, b, key, int(n));
     // kept candidates join their chunks' sums, a wave a chunk
-    const int64_t size = (p.N + gridDim.x - 1) / gridDim.x;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     __syncthreads();
     double* kept = reinterpret_cast<double*>(s.weight);
     int* chunk = reinterpret_cast<int*>(s.count);
@@ -668,36 +806,57 @@ __global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p)
         for (int i = threadIdx.x; i < m; i += kThreads) {
             const unsigned long long k = key[base + i];
             kept[i] = k >= last ? r.drawn(value_of(uint32_t(k >> 32))) : 0.0;
-            chunk[i] = int(int64_t(~uint32_t(k)) / size);
+            chunk[i] = int(int64_t(~uint32_t(k)) / dv.chunk);
         }
         __syncthreads();
         for (int c = wave; c < int(gridDim.x); c += kWaves) {
-            // the list's order differs from run to run: in fixed point, where
-            // the smallest kept weight still counts
-            unsigned long long sum = 0;
-            for (int i = lane; i < m; i += 64)
-                if (chunk[i] == c && kept[i] > 0.0) sum += max(1ull, r.fixed(kept[i]));
+            double sum = 0.0;
+            for (int i = lane; i < m; i += 64) sum += chunk[i] == c ? kept[i] : 0.0;
 #pragma unroll
             for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
-            if (lane == 0) chunk_sum[c] += ldexp(double(sum), -r.bits);
+            if (lane == 0) chunk_sum[c] += sum;
         }
         __syncthreads();
     }
+    // the chunk in which the running sum passes the target: every wave finds it
     const double u = p.u[row];
-    double total = 0.0;
-    for (int c = 0; c < int(gridDim.x); ++c) total += chunk_sum[c];
+    const double own = lane < int(gridDim.x) ? chunk_sum[lane] : 0.0;
+    double upto = own;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const double o = __shfl_up(upto, off, 64);
+        if (lane >= off) upto += o;
+    }
+    const double target = u * __shfl(upto, 63, 64);
+    const uint64_t past = __ballot(own > 0.0 && upto > target);
     int64_t pick = p.N;
-    if (u < 1.0) {
-        const double target = u * total;
-        double run = 0.0;
-        for (int c = 0; c < int(gridDim.x) && pick == p.N; ++c) {
-            if (run + chunk_sum[c] > target) {
-                double sum;
-                const int64_t f = min(p.N, c * size);
-                pick = walk(s, r, x, f, min(p.N, f + size), last, run, target, true, &sum);
+    if (u < 1.0 && past) {
+        const int c = __ffsll((unsigned long long)past) - 1;
+        double run = __shfl(upto - own, c, 64);
+        // its groups: what the chunk's work-group summed, and the kept
+        // candidates, which lie in the list in the row's order
+        __syncthreads();
+        group_sum[threadIdx.x] = ONE ? own_group : int(threadIdx.x) < dv.groups
+            ? __longlong_as_double((long long)get(groups + (c - int(blockIdx.x)) * int64_t(dv.groups) + threadIdx.x)) : 0.0;
+        __syncthreads();
+        for (int g = wave; g < dv.groups && n; g += kWaves) {
+            const int64_t f = c * dv.chunk + g * dv.group;
+            double sum = 0.0;
+            for (int i = lane; i < int(n); i += 64) {
+                const unsigned long long k = key[i];
+                const int64_t at = int64_t(~uint32_t(k));
+                if (k >= last && at >= f && at < f + dv.group) sum += r.drawn(value_of(uint32_t(k >> 32)));
             }
-            run += chunk_sum[c];
+#pragma unroll
+            for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
+            if (lane == 0) group_sum[g] += sum;
         }
+        __syncthreads();
+        const double mine = group_sum[threadIdx.x];
+        const int g = pick_group(s, mine, run, target);
+        run = s.d.wave[0];
+        const int64_t f = c * dv.chunk + max(g, 0) * dv.group;
+        if (g >= 0) pick = walk_group(s, r, x, f, min(p.N, f + dv.group), last, run, target);
     }
     if (threadIdx.x == 0) p.idx[row] = pick < p.N ? int32_t(pick) : r.top_idx;
 }
@@ -706,24 +865,23 @@ __global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p)
 
 size_t sample_workspace_bytes(int64_t m, int64_t N)
 {
-    return N <= kSmallRow || m == 0 ? 256 : size_t(m) * sizeof(RowSpace);
+    if (m == 0) return 256;
+    const Division d = division(m, N);
+    if (d.chunks == 1) return 256;
+    return size_t(m) * (sizeof(RowSpace) + size_t(d.chunks) * size_t(d.groups) * 8);
 }
 
 hipError_t launch_sample(const SampleParams& p, hipStream_t s)
 {
-    if (p.N <= kSmallRow) {
-        hipLaunchKernelGGL(sample_small, dim3(unsigned(p.m)), dim3(kThreads), 0, s, p);
+    const Division d = division(p.m, p.N);
+    const dim3 grid{unsigned(d.chunks), unsigned(p.m), 1};
+    if (d.chunks == 1) {
+        hipLaunchKernelGGL(sample_draw<true>, grid, dim3(kThreads), 0, s, p, d);
         return hipGetLastError();
     }
-    // about as many chunks as the chip holds work-groups, of at least 4096 logits
-    int64_t chunks = (p.N + 4095) / 4096;
-    const int64_t fit = (kResident + p.m - 1) / p.m;
-    if (chunks > fit) chunks = fit;
-    if (chunks > kMaxChunks) chunks = kMaxChunks;
-    const dim3 grid{unsigned(chunks), unsigned(p.m), 1};
-    hipLaunchKernelGGL(sample_top, grid, dim3(kThreads), 0, s, p);
-    if (p.top_k || p.top_p) hipLaunchKernelGGL(sample_histogram, grid, dim3(kThreads), 0, s, p);
-    hipLaunchKernelGGL(sample_draw, grid, dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL(sample_top, grid, dim3(kThreads), 0, s, p, d);
+    if (p.top_k || p.top_p) hipLaunchKernelGGL(sample_histogram, grid, dim3(kThreads), 0, s, p, d);
+    hipLaunchKernelGGL(sample_draw<false>, grid, dim3(kThreads), 0, s, p, d);
     return hipGetLastError();
 }
 
