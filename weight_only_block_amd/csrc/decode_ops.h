@@ -8,6 +8,28 @@
 
 namespace qg {
 
+#ifdef __HIP_DEVICE_COMPILE__
+// Reads a word of each 64-byte line of the kernel's first BYTES argument bytes
+// at once.  A line's first read misses every cache (about 1 us); without this
+// each line's miss comes where its first argument is used, one after another.
+template <int BYTES>
+__device__ __forceinline__ void fetch_arguments()
+{
+    typedef const __attribute__((address_space(4))) uint32_t* words;
+    words a = (words)__builtin_amdgcn_kernarg_segment_ptr();
+    uint32_t v[(BYTES + 63) / 64];
+#pragma unroll
+    for (int i = 0; i < (BYTES + 63) / 64; ++i) v[i] = a[16 * i];
+#pragma unroll
+    for (int i = 0; i < (BYTES + 63) / 64; ++i) asm volatile("" ::"s"(v[i]));
+}
+#else
+template <int BYTES>
+__device__ inline void fetch_arguments()
+{
+}
+#endif
+
 constexpr int kMaxHeadDim = 256;
 constexpr int kMaxRotPairs = kMaxHeadDim / 2;
 

@@ -45,7 +45,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.0f;             // log2 by which a score may pass the reference
 constexpr int kListPages = 1024;           // page ids of a run's segment, in LDS
-constexpr int kMaxWorkers = 512;
+constexpr int kListSeqs = 128;             // sequences whose lengths are kept in LDS
+constexpr int kComputeUnits = 256;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -109,7 +110,9 @@ template <int DP_, bool E4M3_, bool SHARED_>
 struct Shape {
     static constexpr int DP = DP_;
     static constexpr bool E4M3 = E4M3_, SHARED = SHARED_;
-    static constexpr int W = (!SHARED && DP == 256 && !E4M3) ? 2 : 4;   // waves
+    // Waves.  Split: two, so that two to four work-groups share a compute
+    // unit and one streams while another begins or ends a unit.
+    static constexpr int W = SHARED ? 4 : DP == 256 && !E4M3 ? 1 : 2;
     static constexpr int THREADS = 64 * W;
     static constexpr int WAVES_PER_SIMD = DP <= 128 ? 2 : 1;
     static constexpr int M = SHARED ? 32 * W : 32;                      // rows of a unit
@@ -127,7 +130,15 @@ struct Shape {
     static constexpr int OS = DP + 4;                                   // floats of a row in the joining buffer
     static constexpr int JOIN = SHARED ? 0 : W * M * OS * 4;
     static constexpr int BUFFER = RING > JOIN ? RING : JOIN;
-    static constexpr int LDS = BUFFER + kListPages * 4 + 2 * W * 32 * 4 + 64;
+    static constexpr int LDS = BUFFER + kListPages * 4 + 2 * W * 32 * 4 + 64 + kListSeqs * 12;
+    // work-groups that a compute unit holds (160 KB of LDS, two waves of up to
+    // 256 registers a SIMD or one of 512)
+    static constexpr int BY_LDS = 160 * 1024 / LDS, BY_WAVES = 4 * WAVES_PER_SIMD / W;
+    static constexpr int PER_CU = BY_LDS < BY_WAVES ? BY_LDS : BY_WAVES;
+    // Steps that a run has at least: a shorter one costs more in joining its
+    // part than it saves.
+    static constexpr int LEAST = SHARED ? 8 : 4;
+    static constexpr int EXTRA = SHARED ? 4 : 3;
     static constexpr int SLOT = M * DP + 2 * M;                         // floats of a partial result
     static constexpr int STEPS = DP / 16;                               // products along the dimension
     static constexpr int DB = DP / 32;
@@ -158,6 +169,12 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b)
     return s;
 }
 
+// From LDS where all sequences fit.
+__device__ __forceinline__ Seq get_seq(const AttnParams& p, const Seq* seqs, int b)
+{
+    return p.seqs <= kListSeqs ? seqs[b] : load_seq(p, b);
+}
+
 struct Range {
     int lo, hi, base;   // keys [lo, hi) that some row sees; the first tile starts at base
 };
@@ -180,6 +197,14 @@ __device__ __forceinline__ int unit_steps(const AttnParams& p, const Seq& s, int
 {
     const Range g = unit_range<S>(p, s, tile);
     return g.hi > g.lo ? (g.hi - g.base + S::STEP - 1) / S::STEP : 1;   // a unit without keys still writes its rows
+}
+
+// A unit's length in the line: its steps and what beginning and ending it
+// costs, in steps.
+template <class S>
+__device__ __forceinline__ int unit_cost(const AttnParams& p, const Seq& s, int tile)
+{
+    return unit_steps<S>(p, s, tile) + S::EXTRA;
 }
 
 template <class S>
@@ -452,8 +477,11 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
     int32_t* list = reinterpret_cast<int32_t*>(lds + S::BUFFER);
     float* ml = reinterpret_cast<float*>(list + kListPages);      // [2][W][32]
     int64_t* plan = reinterpret_cast<int64_t*>(ml + 2 * S::W * 32);   // 8 values
+    Seq* seqs = reinterpret_cast<Seq*>(plan + 8);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 31, h = lane >> 5, dim = p.cache.head_dim;
+
+    fetch_arguments<sizeof(AttnParams)>();
 
     // ---- the line of work: this run's part of it
     int64_t mine = 0;
@@ -462,9 +490,10 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
     const int b0 = min(int(threadIdx.x) * per, p.seqs), b1 = min(b0 + per, p.seqs);
     for (int b = b0; b < b1; ++b) {
         const Seq s = load_seq(p, b);
+        if (p.seqs <= kListSeqs) seqs[b] = s;
         const int tiles = seq_tiles<S>(p, s);
         mine_units += tiles;
-        for (int t = 0; t < tiles; ++t) mine += unit_steps<S>(p, s, t);
+        for (int t = 0; t < tiles; ++t) mine += unit_cost<S>(p, s, t);
     }
     int64_t upto = mine;
     int upto_units = mine_units;
@@ -488,26 +517,34 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
     const int64_t total = head_steps * p.cache.kv_heads;
     // starts that are not ascending claim more rows than there are
     if (int64_t(head_units) * p.cache.kv_heads > counters) return;
-    const int64_t runs = min(int64_t(gridDim.x), total);
+    const int64_t runs = max(int64_t(1), min(int64_t(gridDim.x), total / S::LEAST));
     // consecutive work-groups go to different XCDs: give each XCD one stretch
     // of the line, so that its L2 holds few heads' keys
     const int xcds = gridDim.x % 8 == 0 ? 8 : 1;
     const int64_t run = runs < int64_t(gridDim.x) ? int64_t(blockIdx.x)   // few: over all XCDs
                                                   : int64_t(blockIdx.x % xcds) * (gridDim.x / xcds) + blockIdx.x / xcds;
-    if (run >= runs) return;
-    int64_t at = run * total / runs;
-    const int64_t end = (run + 1) * total / runs;
+    if (run >= runs || total == 0) return;
+    // the first `longer` runs have base + 1 steps, the others base
+    const int64_t base = total / runs, longer = total - base * runs;
+    const auto run_start = [&](int64_t w) { return w * base + min(w, longer); };
+    const auto run_of = [&](int64_t x) {
+        const int64_t split = longer * (base + 1);
+        return x < split ? x / (base + 1) : longer + (x - split) / base;
+    };
+    int64_t at = run_start(run);
+    const int64_t end = run_start(run + 1);
+    int kvh = int(at / head_steps);
     {
-        const int64_t r = at % head_steps;
+        const int64_t r = at - kvh * head_steps;
         if (r >= upto - mine && r < upto) {
             int64_t left = r - (upto - mine);
             int unit = upto_units - mine_units;
             for (int b = b0; b < b1; ++b) {
-                const Seq s = load_seq(p, b);
+                const Seq s = get_seq(p, seqs, b);
                 const int tiles = seq_tiles<S>(p, s);
                 bool found = false;
                 for (int t = 0; t < tiles && !found; ++t) {
-                    const int n = unit_steps<S>(p, s, t);
+                    const int n = unit_cost<S>(p, s, t);
                     if (left < n) {
                         plan[0] = b, plan[1] = t, plan[2] = left, plan[3] = unit;
                         found = true;
@@ -521,24 +558,45 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
         }
     }
     __syncthreads();
-    int kvh = int(at / head_steps), b = int(plan[0]), tile = int(plan[1]), off = int(plan[2]), unit = int(plan[3]);
-    b = __builtin_amdgcn_readfirstlane(b);
-    tile = __builtin_amdgcn_readfirstlane(tile);
-    off = __builtin_amdgcn_readfirstlane(off);
-    unit = __builtin_amdgcn_readfirstlane(unit);
+    int b = __builtin_amdgcn_readfirstlane(int(plan[0])), tile = __builtin_amdgcn_readfirstlane(int(plan[1]));
+    int off = __builtin_amdgcn_readfirstlane(int(plan[2])), unit = __builtin_amdgcn_readfirstlane(int(plan[3]));
 
     // dimensions past the head's end stay zero in every tile
-    for (int i = threadIdx.x; i < S::BUFFER / 16; i += S::THREADS) reinterpret_cast<u32x4*>(lds)[i] = u32x4{0, 0, 0, 0};
+    const auto clear = [&] {
+        if (dim < S::DP)
+            for (int i = threadIdx.x; i < S::BUFFER / 16; i += S::THREADS) reinterpret_cast<u32x4*>(lds)[i] = u32x4{0, 0, 0, 0};
+    };
+    clear();
 
     uint32_t* arrived = static_cast<uint32_t*>(p.workspace);
     float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + (size_t(counters) * 4 + 255) / 256 * 256);
 
+    // Goes on to the next unit of the line.
+    const auto advance = [&](int cost) {
+        at += cost;
+        off = 0;
+        if (at >= end) return;
+        ++tile;
+        ++unit;
+        Seq q = get_seq(p, seqs, b);
+        while (tile >= seq_tiles<S>(p, q)) {
+            tile = 0;
+            if (++b == p.seqs) b = 0, unit = 0, ++kvh;
+            q = get_seq(p, seqs, b);
+        }
+    };
+
     while (at < end) {
-        const Seq s = load_seq(p, b);
+        const Seq s = get_seq(p, seqs, b);
         const int rows = min(S::M, s.n * p.group - tile * S::M);
         const Range g = unit_range<S>(p, s, tile);
         const int steps = unit_steps<S>(p, s, tile);
-        const int count = int(min(int64_t(steps - off), end - at));
+        const int take = int(min(int64_t(steps + S::EXTRA - off), end - at));
+        const int from = max(0, off - S::EXTRA), count = max(0, off + take - S::EXTRA) - from;
+        if (count == 0) {       // only what stands for the unit's beginning
+            advance(take);
+            continue;
+        }
         const float ks = S::E4M3 ? p.cache.k_scale[kvh] : 1.0f;
         float c = p.scale * ks * kLog2e;
         const bool neg = c < 0.0f;
@@ -601,7 +659,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
 
         // ---- segments of the run whose page ids fit the list
         for (int done = 0; done < count && g.hi > g.lo;) {
-            const int start = g.base + (off + done) * S::STEP;
+            const int start = g.base + (from + done) * S::STEP;
             ld.first_page = start >> p.cache.page_shift;
             // steps whose last key's page is in the list
             const int64_t span = (int64_t(ld.first_page + kListPages) << p.cache.page_shift) - start;
@@ -653,7 +711,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
         }
         st.l += other_half(st.l);
         __syncthreads();
-        if (plan[5]) restore(st, p, ld, g.base + off * S::STEP, g.base + (off + count) * S::STEP);
+        if (plan[5]) restore(st, p, ld, g.base + from * S::STEP, g.base + (from + count) * S::STEP);
 
         // ---- results: whole units to the output, parts to the workspace
         const bool whole = count == steps;
@@ -738,6 +796,48 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
             }
         }
 
+        // The unit's parts, run by run.  Each part's share, exp2(its reference
+        // less the largest), is worked out once a row, then every thread adds
+        // up places of its own, eight parts' loads at a time.
+        const auto join = [&](int64_t unit_start, int steps, int rows) {
+            const int64_t wf = run_of(unit_start + S::EXTRA), wl = run_of(unit_start + S::EXTRA + steps - 1);
+            const auto part = [&](int64_t w) { return slots + (w * 2 + (run_start(w) > unit_start ? 0 : 1)) * S::SLOT; };
+            const int parts = int(wl - wf + 1), quads = dim / 4;
+            for (int i = threadIdx.x; i < rows * quads; i += S::THREADS) {
+                const int rw = i / quads, d = (i % quads) * 4;
+                float m = -INFINITY, l = 0.0f, a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int x = 0; x < parts; x += 8) {
+                    float pm[8], pl[8], v[8][4];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        // past the last part: the last again, with no share
+                        const float* src = part(wf + min(x + e, parts - 1));
+                        get2(src + S::M * S::DP + 2 * rw, &pm[e], &pl[e]);
+                        get2(src + rw * S::DP + d, &v[e][0], &v[e][1]);
+                        get2(src + rw * S::DP + d + 2, &v[e][2], &v[e][3]);
+                    }
+                    float mn = m;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) mn = fmaxf(mn, pm[e]);
+                    const float ref = mn == -INFINITY ? 0.0f : mn, keep = __builtin_amdgcn_exp2f(m - ref);
+                    m = mn;
+                    l *= keep;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) a[j] *= keep;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if (x + e >= parts) break;
+                        const float share = __builtin_amdgcn_exp2f(pm[e] - ref);
+                        l += pl[e] * share;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) a[j] += v[e][j] * share;
+                    }
+                }
+                put_out(rw, d, a[0], a[1], a[2], a[3], inverse(l));
+                if (d == 0 && p.lse) put_lse(rw, m, l);
+            }
+        };
+
         if (!whole) {
             // The partial stores have reached the device-wide level before
             // this work-group counts its steps; whoever completes the count
@@ -754,59 +854,23 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
             }
             __syncthreads();
             if (plan[4]) {
-                const int64_t wf = ((unit_start + 1) * runs - 1) / total, wl = ((unit_start + steps) * runs - 1) / total;
-                const int quads = dim / 4;
-                for (int i = threadIdx.x; i < rows * quads; i += S::THREADS) {
-                    const int rw = i / quads, d = (i % quads) * 4;
-                    float m = -INFINITY, l = 0.0f, a0 = 0.0f, a1 = 0.0f, a2 = 0.0f, a3 = 0.0f;
-                    for (int64_t w = wf; w <= wl; ++w) {
-                        const float* part = slots + (w * 2 + (w * total / runs > unit_start ? 0 : 1)) * S::SLOT;
-                        float pm, pl, v0, v1, v2, v3;
-                        get2(part + S::M * S::DP + 2 * rw, &pm, &pl);
-                        get2(part + rw * S::DP + d, &v0, &v1);
-                        get2(part + rw * S::DP + d + 2, &v2, &v3);
-                        const float mn = fmaxf(m, pm), ref = mn == -INFINITY ? 0.0f : mn;
-                        const float e0 = __builtin_amdgcn_exp2f(m - ref), e1 = __builtin_amdgcn_exp2f(pm - ref);
-                        m = mn;
-                        l = l * e0 + pl * e1;
-                        a0 = a0 * e0 + v0 * e1;
-                        a1 = a1 * e0 + v1 * e1;
-                        a2 = a2 * e0 + v2 * e1;
-                        a3 = a3 * e0 + v3 * e1;
-                    }
-                    put_out(rw, d, a0, a1, a2, a3, inverse(l));
-                    if (d == 0 && p.lse) put_lse(rw, m, l);
-                }
+                join(unit_start, steps, rows);
             }
         }
 
-        // ---- next unit
-        at += count;
-        off = 0;
         __syncthreads();
-        if (at < end) {
-            ++tile;
-            ++unit;
-            Seq q = s;
-            while (tile >= seq_tiles<S>(p, q)) {
-                tile = 0;
-                if (++b == p.seqs) b = 0, unit = 0, ++kvh;
-                q = load_seq(p, b);
-            }
-            // the joining buffer wrote over the tiles' empty dimensions
-            if (!S::SHARED && dim < S::DP)
-                for (int i = threadIdx.x; i < S::BUFFER / 16; i += S::THREADS) reinterpret_cast<u32x4*>(lds)[i] = u32x4{0, 0, 0, 0};
-        }
+        // the joining buffer wrote over the tiles' empty dimensions
+        if (!S::SHARED) clear();
+        advance(take);
     }
 }
 
 template <class S>
 int64_t workers(int64_t tokens, int group, int kv_heads, int seqs, int64_t max_kv)
 {
-    const int64_t units = tokens * group / S::M + seqs;
+    const int64_t units = (tokens * group / S::M + seqs) * kv_heads;
     const int64_t steps = (max_kv + 15 + S::STEP - 1) / S::STEP + 1;
-    const int64_t most = S::LDS > 80 * 1024 ? kMaxWorkers / 2 : kMaxWorkers;
-    const int64_t need = units * kv_heads * steps;
+    const int64_t most = kComputeUnits * S::PER_CU, need = units * steps / S::LEAST + 1;
     return need < most ? (need + 7) / 8 * 8 : most;
 }
 

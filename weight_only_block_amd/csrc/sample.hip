@@ -475,6 +475,7 @@ __device__ __forceinline__ void add_to_bins(Shared& s, const Row& r, const float
 
 __global__ __launch_bounds__(kThreads) void sample_top(SampleParams p, Division dv)
 {
+    fetch_arguments<sizeof(SampleParams) + sizeof(Division)>();
     __shared__ Shared s;
     const int64_t row = blockIdx.y;
     RowSpace& ws = static_cast<RowSpace*>(p.workspace)[row];
@@ -498,6 +499,7 @@ __device__ __forceinline__ uint64_t row_best(const RowSpace& ws)
 
 __global__ __launch_bounds__(kThreads) void sample_histogram(SampleParams p, Division dv)
 {
+    fetch_arguments<sizeof(SampleParams) + sizeof(Division)>();
     __shared__ Shared s;
     const int64_t row = blockIdx.y;
     RowSpace& ws = static_cast<RowSpace*>(p.workspace)[row];
@@ -690,6 +692,7 @@ __device__ uint64_t cut_of_candidates(Shared& s, const Row& r, const Bins& b, un
 template <bool ONE>
 __global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p, Division dv)
 {
+    fetch_arguments<sizeof(SampleParams) + sizeof(Division)>();
     __shared__ Shared s;
     __shared__ unsigned long long key[kCandidates];
     __shared__ double chunk_sum[kMaxChunks];
