@@ -47,6 +47,7 @@ constexpr float kRaise = 8.0f;             // log2 by which a score may pass the
 constexpr int kListPages = 1024;           // page ids of a run's segment, in LDS
 constexpr int kListSeqs = 128;             // sequences whose lengths are kept in LDS
 constexpr int kComputeUnits = 256;
+constexpr int32_t kMaxWindow = 1 << 30;    // no shorter than the longest sequence
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -105,11 +106,66 @@ __device__ __forceinline__ void get2(const float* p, float* a, float* b)
     *b = __uint_as_float(uint32_t(v >> 32));
 }
 
-// One kernel shape.  DP: head dimension padded to a matrix-core multiple.
-template <int DP_, bool E4M3_, bool SHARED_>
+// A value the compiler knows nothing of.  Lane numbers pass through it where a
+// part of the kernel begins: what depends on them is then worked out there,
+// not all together ahead of the loop over units, where hundreds of
+// instructions, each fetched from a cold cache, stood before the first load.
+__device__ __forceinline__ int opaque(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// a / b for a below 2^52, b > 0.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b)
+{
+    int64_t q = int64_t(double(a) * __builtin_amdgcn_rcp(double(b)));   // off by a little
+    while (q * b > a) --q;
+    while ((q + 1) * b <= a) ++q;
+    return q;
+}
+
+// The same value in every lane, in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t x)
+{
+    const uint32_t lo = uint32_t(__builtin_amdgcn_readfirstlane(int(x)));
+    const uint32_t hi = uint32_t(__builtin_amdgcn_readfirstlane(int(x >> 32)));
+    return int64_t(uint64_t(hi) << 32 | lo);
+}
+
+// The kernel's arguments, strides and sizes in 32 bits (few scalar registers).
+struct Args {
+    const uint8_t* k;
+    const uint8_t* v;
+    const float* k_scale;
+    const float* v_scale;
+    const uint16_t* q;
+    uint16_t* out;
+    float* lse;
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    const int32_t* table;
+    uint8_t* workspace;
+    uint32_t page16, head16, slot16;          // cache strides in 16 bytes
+    uint32_t q_token, q_head, o_token, o_head, lse_token, table_stride;
+    int32_t pages, kv_heads, page_shift, dim;
+    int32_t tokens, max_q, cap, window, seqs; // cap: keys a sequence may have; window 0: none
+    int32_t group;
+    uint32_t by_group;                        // ceil(2^31 / group)
+    int32_t counters;
+    float scale;
+};
+
+// x / group, exact while x * group is below 2^30: x is a row of a unit beside
+// the heads before its first, below 127 + group, and group below 2^15.
+__device__ __forceinline__ uint32_t by_group(const Args& p, uint32_t x) { return __umulhi(2 * x, p.by_group); }
+
+// One kernel shape.  DP: head dimension padded to a matrix-core multiple;
+// FULL: the head has all of it.
+template <int DP_, bool E4M3_, bool SHARED_, bool FULL_>
 struct Shape {
     static constexpr int DP = DP_;
-    static constexpr bool E4M3 = E4M3_, SHARED = SHARED_;
+    static constexpr bool E4M3 = E4M3_, SHARED = SHARED_, FULL = FULL_;
     // Waves.  Split: two, so that two to four work-groups share a compute
     // unit and one streams while another begins or ends a unit.
     static constexpr int W = SHARED ? 4 : DP == 256 && !E4M3 ? 1 : 2;
@@ -136,7 +192,7 @@ struct Shape {
     static constexpr int BY_LDS = 160 * 1024 / LDS, BY_WAVES = 4 * WAVES_PER_SIMD / W;
     static constexpr int PER_CU = BY_LDS < BY_WAVES ? BY_LDS : BY_WAVES;
     // Steps that a run has at least: a shorter one costs more in joining its
-    // part than it saves.
+    // part than it saves.  What beginning and ending a unit costs, in steps.
     static constexpr int LEAST = SHARED ? 8 : 4;
     static constexpr int EXTRA = SHARED ? 4 : 3;
     static constexpr int SLOT = M * DP + 2 * M;                         // floats of a partial result
@@ -157,60 +213,53 @@ struct Seq {
     int q0, n, kv;
 };
 
-__device__ __forceinline__ Seq load_seq(const AttnParams& p, int b)
+__device__ __forceinline__ Seq load_seq(const Args& p, int b)
 {
+    const int a0 = p.q_start[b], a1 = p.q_start[b + 1], kv = p.kv_len[b];
     Seq s;
-    const int64_t q0 = max(int64_t(0), min(int64_t(p.q_start[b]), p.tokens));
-    const int64_t q1 = max(q0, min(min(int64_t(p.q_start[b + 1]), p.tokens), q0 + p.max_q));
-    const int64_t cap = min(p.max_kv, p.table_cols << p.cache.page_shift);
-    s.q0 = int(q0);
-    s.n = int(q1 - q0);
-    s.kv = int(max(int64_t(0), min(int64_t(p.kv_len[b]), cap)));
+    s.q0 = max(0, min(a0, p.tokens));
+    s.n = max(0, min(min(a1, p.tokens) - s.q0, p.max_q));
+    s.kv = max(0, min(kv, p.cap));
     return s;
 }
 
 // From LDS where all sequences fit.
-__device__ __forceinline__ Seq get_seq(const AttnParams& p, const Seq* seqs, int b)
+__device__ __forceinline__ Seq get_seq(const Args& p, const Seq* seqs, int b)
 {
     return p.seqs <= kListSeqs ? seqs[b] : load_seq(p, b);
 }
 
-struct Range {
-    int lo, hi, base;   // keys [lo, hi) that some row sees; the first tile starts at base
+// A unit: rows [row0, row0 + rows) of a sequence's tokens x group.
+struct Unit {
+    int rows, token0, lane0;   // token and head of its first row
+    int first, last;           // positions of the first and last row's tokens
+    int lo, hi, base;          // keys [lo, hi) that some row sees; the first tile starts at base
+    int steps;
 };
 
 template <class S>
-__device__ __forceinline__ Range unit_range(const AttnParams& p, const Seq& s, int tile)
+__device__ __forceinline__ Unit make_unit(const Args& p, const Seq& s, int tile)
 {
-    const int rows = s.n * p.group, r0 = tile * S::M, r1 = min(r0 + S::M, rows) - 1;
-    const int first = s.kv - s.n + r0 / p.group, last = s.kv - s.n + r1 / p.group;
-    Range g;
-    g.hi = max(0, last + 1);
-    g.lo = p.window > 0 ? int(max(int64_t(0), int64_t(first) - p.window + 1)) : 0;
-    if (g.lo > g.hi) g.lo = g.hi;
-    g.base = g.lo & ~15;
-    return g;
+    Unit u;
+    const uint32_t row0 = uint32_t(tile) * S::M;
+    u.rows = int(min(uint32_t(S::M), uint32_t(s.n) * uint32_t(p.group) - row0));
+    u.token0 = int(row0 / uint32_t(p.group));
+    u.lane0 = int(row0 - uint32_t(u.token0) * uint32_t(p.group));
+    u.first = s.kv - s.n + u.token0;
+    u.last = u.first + int(by_group(p, uint32_t(u.lane0 + u.rows - 1)));
+    u.hi = max(0, u.last + 1);
+    u.lo = p.window > 0 ? max(0, u.first - p.window + 1) : 0;
+    if (u.lo > u.hi) u.lo = u.hi;
+    u.base = u.lo & ~15;
+    // a unit without keys still writes its rows
+    u.steps = u.hi > u.lo ? int(uint32_t(u.hi - u.base + S::STEP - 1) / S::STEP) : 1;
+    return u;
 }
 
 template <class S>
-__device__ __forceinline__ int unit_steps(const AttnParams& p, const Seq& s, int tile)
+__device__ __forceinline__ int seq_tiles(const Args& p, const Seq& s)
 {
-    const Range g = unit_range<S>(p, s, tile);
-    return g.hi > g.lo ? (g.hi - g.base + S::STEP - 1) / S::STEP : 1;   // a unit without keys still writes its rows
-}
-
-// A unit's length in the line: its steps and what beginning and ending it
-// costs, in steps.
-template <class S>
-__device__ __forceinline__ int unit_cost(const AttnParams& p, const Seq& s, int tile)
-{
-    return unit_steps<S>(p, s, tile) + S::EXTRA;
-}
-
-template <class S>
-__device__ __forceinline__ int seq_tiles(const AttnParams& p, const Seq& s)
-{
-    return int((int64_t(s.n) * p.group + S::M - 1) / S::M);
+    return int((uint32_t(s.n) * uint32_t(p.group) + S::M - 1) / S::M);
 }
 
 // What a wave accumulates: its 32 rows are the lanes' columns.
@@ -225,9 +274,10 @@ struct State {
 // A key tile (K and V, 32 or 64 keys from k0) against the wave's rows.
 // `masked`: some row does not see some key.
 template <class S>
-__device__ __forceinline__ void compute(State<S>& st, const uint8_t* kt, const uint8_t* vt, int k0, float c, bool masked)
+__device__ __forceinline__ void compute(State<S>& st, const uint8_t* kt, const uint8_t* vt, int k0, float c, bool masked,
+                                        int lane)
 {
-    const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5, i16 = lane & 15, dh = (lane >> 4) & 1;
+    const int col = lane & 31, h = lane >> 5, i16 = lane & 15, dh = (lane >> 4) & 1;
     f32x16 s[S::BLOCKS];
 #pragma unroll
     for (int b = 0; b < S::BLOCKS; ++b)
@@ -337,7 +387,7 @@ __device__ __forceinline__ void compute(State<S>& st, const uint8_t* kt, const u
 // The loads of one tile, and what the tile needs before use.
 template <class S>
 struct Loader {
-    const AttnParams& p;
+    const Args& p;
     const int32_t* list;      // LDS: page ids from page `first_page` on, -1 outside the sequence or the cache
     int first_page;
     const int32_t* table;     // the sequence's row of the page table
@@ -346,48 +396,43 @@ struct Loader {
     int lo, hi;               // keys that some row of the unit sees
     int all_lo, all_hi;       // and that every row sees
     int64_t* poisoned;        // LDS
+    int lane;
 
-    // Rows [0, ROWS) of the wave's part, the first being key k0 + row0 of the tile at LDS kt, vt.
-    __device__ __forceinline__ bool issue(uint8_t* kt, uint8_t* vt, int k0, int row0) const
+    // Rows [row0, row0 + ROWS) of the tile, the wave's part; its K and V at
+    // LDS offsets kt and vt, its first key k0.
+    __device__ __forceinline__ bool issue(uint32_t kt, uint32_t vt, int k0, int row0) const
     {
-        const int lane = threadIdx.x & 63, lr = lane / S::CPR, lc = lane % S::CPR;
-        const int chunks = p.cache.head_dim * S::ES / 16;
-        const uint64_t slot_bytes = uint64_t(p.cache.slot_stride) * S::ES, page_bytes = uint64_t(p.cache.page_stride) * S::ES;
-        const int mask = (1 << p.cache.page_shift) - 1;
+        const int lr = lane / S::CPR, lc = lane % S::CPR;
+        const int chunks = S::FULL ? S::CPR : p.dim * S::ES / 16;
+        const int mask = (1 << p.page_shift) - 1;
         bool dirty = k0 + row0 < all_lo || k0 + row0 + S::ROWS > all_hi;
-        int ids[S::LOADS];
-        if (p.cache.page_shift >= 4 && slot_bytes < (1u << 24)) {
-            // all rows of one load lie in one page
-            const uint32_t row_off = uint32_t(lr) * uint32_t(slot_bytes);
-#pragma unroll
-            for (int j = 0; j < S::LOADS; ++j) ids[j] = list[((k0 + row0 + j * S::RPI) >> p.cache.page_shift) - first_page];
+        kt += row0 * S::RB;
+        vt += row0 * S::RB;
+        if (p.page_shift >= 4 && p.slot16 < (1u << 20)) {
+            // all rows of one load lie in one page; lane j looks up load j's
+            const int mine = list[((k0 + row0 + min(lane, S::LOADS - 1) * S::RPI) >> p.page_shift) - first_page];
+            if (__any(mine < 0)) dirty = true;
+            const uint32_t row_off = uint32_t(lr) * (p.slot16 * 16);
 #pragma unroll
             for (int j = 0; j < S::LOADS; ++j) {
-                const int row = row0 + j * S::RPI, key = k0 + row;
-                int id = __builtin_amdgcn_readfirstlane(ids[j]);
-                if (id < 0) dirty = true, id = 0;
-                const uint64_t off = uint64_t(id) * page_bytes + uint64_t(key & mask) * slot_bytes;
-                const int ck = lc ^ S::k_swizzle(row + lr), cv = lc ^ S::v_swizzle(row + lr);
-                const uint32_t dk = __builtin_amdgcn_readfirstlane(lds_offset(kt + row * S::RB));
-                const uint32_t dv = __builtin_amdgcn_readfirstlane(lds_offset(vt + row * S::RB));
-                if (ck < chunks) load_lds_uniform(dk, kbase + off, row_off + 16 * ck);
-                if (cv < chunks) load_lds_uniform(dv, vbase + off, row_off + 16 * cv);
+                const uint32_t id = uint32_t(max(0, __builtin_amdgcn_readlane(mine, j)));
+                const uint32_t slot = uint32_t((k0 + row0 + j * S::RPI) & mask);
+                const uint64_t off = (uint64_t(id) * p.page16 + uint64_t(slot) * p.slot16) << 4;
+                const int ck = lc ^ S::k_swizzle(row0 + j * S::RPI + lr), cv = lc ^ S::v_swizzle(row0 + j * S::RPI + lr);
+                if (S::FULL || ck < chunks) load_lds_uniform(kt + j * 1024, kbase + off, row_off + 16 * ck);
+                if (S::FULL || cv < chunks) load_lds_uniform(vt + j * 1024, vbase + off, row_off + 16 * cv);
             }
         } else {
-#pragma unroll
-            for (int j = 0; j < S::LOADS; ++j) ids[j] = list[((k0 + row0 + j * S::RPI + lr) >> p.cache.page_shift) - first_page];
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < S::LOADS; ++j) {
-                const int row = row0 + j * S::RPI, key = k0 + row + lr;
-                int id = ids[j];
+                const int row = row0 + j * S::RPI + lr, key = k0 + row;
+                int id = list[(key >> p.page_shift) - first_page];
                 if (__any(id < 0)) dirty = true;
-                if (id < 0) id = 0;
-                const uint64_t off = uint64_t(id) * page_bytes + uint64_t(key & mask) * slot_bytes;
-                const int ck = lc ^ S::k_swizzle(row + lr), cv = lc ^ S::v_swizzle(row + lr);
-                const uint32_t dk = __builtin_amdgcn_readfirstlane(lds_offset(kt + row * S::RB));
-                const uint32_t dv = __builtin_amdgcn_readfirstlane(lds_offset(vt + row * S::RB));
-                if (ck < chunks) load_lds(dk, kbase + off + 16 * ck);
-                if (cv < chunks) load_lds(dv, vbase + off + 16 * cv);
+                id = max(0, id);
+                const uint64_t off = (uint64_t(uint32_t(id)) * p.page16 + uint64_t(uint32_t(key & mask)) * p.slot16) << 4;
+                const int ck = lc ^ S::k_swizzle(row), cv = lc ^ S::v_swizzle(row);
+                if (S::FULL || ck < chunks) load_lds(kt + j * 1024, kbase + off + 16 * ck);
+                if (S::FULL || cv < chunks) load_lds(vt + j * 1024, vbase + off + 16 * cv);
             }
         }
         return dirty;
@@ -400,17 +445,17 @@ struct Loader {
     // back at the end (restore).
     __device__ __forceinline__ void patch(uint8_t* kt, uint8_t* vt, int k0, int row0) const
     {
-        const int lane = threadIdx.x & 63, lr = lane / S::CPR, lc = lane % S::CPR;
-        const int chunks = p.cache.head_dim * S::ES / 16;   // those past the dimension stay zero
+        const int lane = opaque(this->lane), lr = lane / S::CPR, lc = lane % S::CPR;
+        const int chunks = S::FULL ? S::CPR : p.dim * S::ES / 16;   // those past the dimension stay zero
         const uint32_t nan = S::E4M3 ? 0x7f7f7f7fu : 0x7fc07fc0u;
 #pragma unroll 1
         for (int j = 0; j < S::LOADS; ++j) {
             const int row = row0 + j * S::RPI + lr, key = k0 + row;
             const bool outside = key < lo || key >= hi;
-            const int page = key >> p.cache.page_shift;
-            int64_t id = -1;
+            const int page = key >> p.page_shift;
+            int id = -1;
             if (!outside && page < pages) id = table[page];
-            const bool lost = !outside && (id < 0 || id >= p.cache.pages);
+            const bool lost = !outside && (id < 0 || id >= p.pages);
             u32x4* v = reinterpret_cast<u32x4*>(vt + row * S::RB + 16 * lc);
             if (outside || lost) {
                 *v = u32x4{0, 0, 0, 0};
@@ -444,24 +489,24 @@ struct Loader {
 
 // Gives the lane's row the values that patch() took out, of keys [from, to).
 template <class S>
-__device__ __forceinline__ void restore(State<S>& st, const AttnParams& p, const Loader<S>& ld, int from, int to)
+__device__ __forceinline__ void restore(State<S>& st, const Args& p, const Loader<S>& ld, int from, int to)
 {
-    const int h = (threadIdx.x & 63) >> 5;
-    const int mask = (1 << p.cache.page_shift) - 1;
+    const int h = opaque(threadIdx.x & 63) >> 5;
+    const int mask = (1 << p.page_shift) - 1;
 #pragma unroll 1
     for (int key = max(from, ld.lo); key < min(to, ld.hi); ++key) {
         if (key >= ld.all_lo && key < ld.all_hi) continue;
-        const int64_t id = ld.table[key >> p.cache.page_shift];
-        if (id < 0 || id >= p.cache.pages) continue;
+        const int id = ld.table[key >> p.page_shift];
+        if (id < 0 || id >= p.pages) continue;
         const uint8_t* row = reinterpret_cast<const uint8_t*>(ld.vbase) +
-                             (id * p.cache.page_stride + int64_t(key & mask) * p.cache.slot_stride) * S::ES;
+                             ((uint64_t(uint32_t(id)) * p.page16 + uint64_t(uint32_t(key & mask)) * p.slot16) << 4);
         const bool sees = key >= st.rlo && key < st.rhi;
 #pragma unroll
         for (int d = 0; d < S::DB; ++d)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int dim = 32 * d + 8 * (i / 4) + 4 * h + i % 4;
-                if (dim >= p.cache.head_dim) continue;
+                if (!S::FULL && dim >= p.dim) continue;
                 float v;
                 if (!S::E4M3) v = __uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(row)[dim]) << 16);
                 else v = __builtin_amdgcn_cvt_f32_fp8(int(row[dim]), 0);
@@ -471,7 +516,7 @@ __device__ __forceinline__ void restore(State<S>& st, const AttnParams& p, const
 }
 
 template <class S>
-__global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kernel(AttnParams p, int64_t counters)
+__global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kernel(Args p)
 {
     extern __shared__ __align__(1024) uint8_t lds[];
     int32_t* list = reinterpret_cast<int32_t*>(lds + S::BUFFER);
@@ -479,9 +524,8 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
     int64_t* plan = reinterpret_cast<int64_t*>(ml + 2 * S::W * 32);   // 8 values
     Seq* seqs = reinterpret_cast<Seq*>(plan + 8);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int col = lane & 31, h = lane >> 5, dim = p.cache.head_dim;
 
-    fetch_arguments<sizeof(AttnParams)>();
+    fetch_arguments<sizeof(Args)>();
 
     // ---- the line of work: this run's part of it
     int64_t mine = 0;
@@ -493,7 +537,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
         if (p.seqs <= kListSeqs) seqs[b] = s;
         const int tiles = seq_tiles<S>(p, s);
         mine_units += tiles;
-        for (int t = 0; t < tiles; ++t) mine += unit_cost<S>(p, s, t);
+        for (int t = 0; t < tiles; ++t) mine += make_unit<S>(p, s, t).steps + S::EXTRA;
     }
     int64_t upto = mine;
     int upto_units = mine_units;
@@ -507,6 +551,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
     __syncthreads();
     int64_t head_steps = 0, before = 0;
     int head_units = 0, before_units = 0;
+#pragma unroll
     for (int w = 0; w < S::W; ++w) {
         if (w == wave) before = head_steps, before_units = head_units;
         head_steps += sums[w];
@@ -514,26 +559,27 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
     }
     upto += before;
     upto_units += before_units;
-    const int64_t total = head_steps * p.cache.kv_heads;
+    head_steps = uniform(head_steps);
+    const int64_t total = head_steps * p.kv_heads;
     // starts that are not ascending claim more rows than there are
-    if (int64_t(head_units) * p.cache.kv_heads > counters) return;
-    const int64_t runs = max(int64_t(1), min(int64_t(gridDim.x), total / S::LEAST));
+    if (total == 0 || int64_t(head_units) * p.kv_heads > p.counters) return;
+    const int runs = int(max(int64_t(1), min(int64_t(gridDim.x), total / S::LEAST)));
     // consecutive work-groups go to different XCDs: give each XCD one stretch
-    // of the line, so that its L2 holds few heads' keys
+    // of the line, so that its L2 holds few heads' keys; few go over all XCDs
     const int xcds = gridDim.x % 8 == 0 ? 8 : 1;
-    const int64_t run = runs < int64_t(gridDim.x) ? int64_t(blockIdx.x)   // few: over all XCDs
-                                                  : int64_t(blockIdx.x % xcds) * (gridDim.x / xcds) + blockIdx.x / xcds;
-    if (run >= runs || total == 0) return;
+    const int run = runs < int(gridDim.x) ? int(blockIdx.x) : int(blockIdx.x % xcds) * int(gridDim.x / xcds) + int(blockIdx.x / xcds);
+    if (run >= runs) return;
     // the first `longer` runs have base + 1 steps, the others base
-    const int64_t base = total / runs, longer = total - base * runs;
-    const auto run_start = [&](int64_t w) { return w * base + min(w, longer); };
+    const int64_t base = uniform(divide(total, runs));
+    const int longer = int(total - base * runs);
+    const auto run_start = [&](int w) { return w * base + min(w, longer); };
     const auto run_of = [&](int64_t x) {
         const int64_t split = longer * (base + 1);
-        return x < split ? x / (base + 1) : longer + (x - split) / base;
+        return int(x < split ? divide(x, base + 1) : longer + divide(x - split, base));
     };
     int64_t at = run_start(run);
     const int64_t end = run_start(run + 1);
-    int kvh = int(at / head_steps);
+    int kvh = int(uniform(divide(at, head_steps)));
     {
         const int64_t r = at - kvh * head_steps;
         if (r >= upto - mine && r < upto) {
@@ -544,7 +590,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
                 const int tiles = seq_tiles<S>(p, s);
                 bool found = false;
                 for (int t = 0; t < tiles && !found; ++t) {
-                    const int n = unit_cost<S>(p, s, t);
+                    const int n = make_unit<S>(p, s, t).steps + S::EXTRA;
                     if (left < n) {
                         plan[0] = b, plan[1] = t, plan[2] = left, plan[3] = unit;
                         found = true;
@@ -560,16 +606,14 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
     __syncthreads();
     int b = __builtin_amdgcn_readfirstlane(int(plan[0])), tile = __builtin_amdgcn_readfirstlane(int(plan[1]));
     int off = __builtin_amdgcn_readfirstlane(int(plan[2])), unit = __builtin_amdgcn_readfirstlane(int(plan[3]));
+    Seq s = get_seq(p, seqs, b);
 
     // dimensions past the head's end stay zero in every tile
     const auto clear = [&] {
-        if (dim < S::DP)
+        if (!S::FULL)
             for (int i = threadIdx.x; i < S::BUFFER / 16; i += S::THREADS) reinterpret_cast<u32x4*>(lds)[i] = u32x4{0, 0, 0, 0};
     };
     clear();
-
-    uint32_t* arrived = static_cast<uint32_t*>(p.workspace);
-    float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + (size_t(counters) * 4 + 255) / 256 * 256);
 
     // Goes on to the next unit of the line.
     const auto advance = [&](int cost) {
@@ -578,132 +622,141 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
         if (at >= end) return;
         ++tile;
         ++unit;
-        Seq q = get_seq(p, seqs, b);
-        while (tile >= seq_tiles<S>(p, q)) {
+        while (tile >= seq_tiles<S>(p, s)) {
             tile = 0;
             if (++b == p.seqs) b = 0, unit = 0, ++kvh;
-            q = get_seq(p, seqs, b);
+            s = get_seq(p, seqs, b);
         }
     };
 
+    const uint32_t lds0 = lds_offset(lds);
     while (at < end) {
-        const Seq s = get_seq(p, seqs, b);
-        const int rows = min(S::M, s.n * p.group - tile * S::M);
-        const Range g = unit_range<S>(p, s, tile);
-        const int steps = unit_steps<S>(p, s, tile);
-        const int take = int(min(int64_t(steps + S::EXTRA - off), end - at));
+        s.q0 = __builtin_amdgcn_readfirstlane(s.q0);
+        s.n = __builtin_amdgcn_readfirstlane(s.n);
+        s.kv = __builtin_amdgcn_readfirstlane(s.kv);
+        const Unit u = make_unit<S>(p, s, tile);
+        const int take = int(min(int64_t(u.steps + S::EXTRA - off), end - at));
         const int from = max(0, off - S::EXTRA), count = max(0, off + take - S::EXTRA) - from;
         if (count == 0) {       // only what stands for the unit's beginning
             advance(take);
             continue;
         }
-        const float ks = S::E4M3 ? p.cache.k_scale[kvh] : 1.0f;
-        float c = p.scale * ks * kLog2e;
-        const bool neg = c < 0.0f;
-        const bool none = c == 0.0f;
-        c = none ? 1.0f : fabsf(c);
+        const float ks = S::E4M3 ? p.k_scale[kvh] : 1.0f;
 
         // ---- the wave's rows
+        const int ulane = opaque(lane), col = ulane & 31, h = ulane >> 5;
         State<S> st;
         const int row = S::SHARED ? wave * 32 + col : col;
-        const bool live = row < rows;
-        const int r = tile * S::M + row;
-        const int token = r / p.group, head = kvh * p.group + r % p.group;
-        const int pos = s.kv - s.n + token;
-        st.rhi = live ? max(0, pos + 1) : 0;
-        st.rlo = live && p.window > 0 ? int(min(int64_t(st.rhi), max(int64_t(0), int64_t(pos) - p.window + 1))) : 0;
+        // rows past the last repeat it and are never written
+        const uint32_t r = uint32_t(u.lane0 + min(row, u.rows - 1)), step = by_group(p, r);
+        const uint32_t head = uint32_t(kvh) * uint32_t(p.group) + (r - step * uint32_t(p.group));
+        const uint16_t* qrow = p.q + uint64_t(uint32_t(s.q0 + u.token0) + step) * p.q_token + uint64_t(head) * p.q_head;
+        const int pos = u.first + int(step);
+        st.rhi = max(0, pos + 1);
+        st.rlo = p.window > 0 ? min(st.rhi, max(0, pos - p.window + 1)) : 0;
         st.m = -INFINITY;
         st.l = 0.0f;
-#pragma unroll
-        for (int d = 0; d < S::DB; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) st.o[d][i] = 0.0f;
 #pragma unroll
         for (int t = 0; t < S::STEPS; ++t) {
             const int d = S::E4M3 ? 32 * (t / 2) + 16 * h + 8 * (t % 2) : 16 * t + 8 * h;
             u32x4 x = {0, 0, 0, 0};
-            if (live && d < dim)
-                x = *reinterpret_cast<const u32x4*>(p.q + (s.q0 + token) * p.q_token + head * p.q_head + d);
-            // the scale's sign goes into the queries, so that the largest
-            // score stays the largest; a scale of zero leaves equal scores
-            if (neg) x ^= 0x80008000u;
-            if (none) x = u32x4{0, 0, 0, 0};
+            if (S::FULL || d < p.dim) x = *reinterpret_cast<const u32x4*>(qrow + d);
             st.q[t] = __builtin_bit_cast(bf16x8, x);
         }
+#pragma unroll
+        for (int d = 0; d < S::DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) st.o[d][i] = 0.0f;
         // keys that every row of this wave sees, and that any does
-        const int wr0 = S::SHARED ? wave * 32 : 0, wr1 = min(wr0 + 32, rows) - 1;
-        const bool busy = wr0 < rows;
+        const int wr0 = S::SHARED ? wave * 32 : 0;
+        const bool busy = wr0 < u.rows;
         int all_lo = 0, all_hi = 0, any_lo = 0, any_hi = 0;
         if (busy) {
-            const int f = s.kv - s.n + (tile * S::M + wr0) / p.group, l = s.kv - s.n + (tile * S::M + wr1) / p.group;
+            const int wr1 = min(wr0 + 32, u.rows) - 1;
+            const int f = u.first + int(by_group(p, uint32_t(u.lane0 + wr0)));
+            const int l = u.first + int(by_group(p, uint32_t(u.lane0 + wr1)));
             all_hi = f + 1;
             any_hi = max(0, l + 1);
             if (p.window > 0) {
-                all_lo = int(max(int64_t(0), int64_t(l) - p.window + 1));
-                any_lo = int(max(int64_t(0), int64_t(f) - p.window + 1));
+                all_lo = max(0, l - p.window + 1);
+                any_lo = max(0, f - p.window + 1);
             }
         }
 
-        Loader<S> ld{p, list, 0, p.table + int64_t(b) * p.table_stride, 0, 0, 0, g.lo, g.hi, 0, 0, plan + 5};
-        ld.all_hi = s.kv - s.n + tile * S::M / p.group + 1;
-        ld.all_lo = p.window > 0 ? int(max(int64_t(0), int64_t(s.kv - s.n + (tile * S::M + rows - 1) / p.group) - p.window + 1)) : 0;
+        Loader<S> ld{p, list, 0, p.table + uint64_t(uint32_t(b)) * p.table_stride, 0, 0, 0, u.lo, u.hi, 0, u.first + 1, plan + 5, ulane};
+        if (p.window > 0) ld.all_lo = max(0, u.last - p.window + 1);
+        ld.pages = int((uint32_t(s.kv) + (1u << p.page_shift) - 1) >> p.page_shift);
+        const uint64_t head_bytes = uint64_t(uniform(int64_t(uint64_t(uint32_t(kvh)) * p.head16 << 4)));
+        ld.kbase = reinterpret_cast<uint64_t>(p.k) + head_bytes;
+        ld.vbase = reinterpret_cast<uint64_t>(p.v) + head_bytes;
         if (threadIdx.x == 0) plan[5] = 0;
-        ld.pages = int((int64_t(s.kv) + (int64_t(1) << p.cache.page_shift) - 1) >> p.cache.page_shift);
-        ld.kbase = reinterpret_cast<uint64_t>(p.cache.k) + uint64_t(kvh) * p.cache.head_stride * S::ES;
-        ld.vbase = reinterpret_cast<uint64_t>(p.cache.v) + uint64_t(kvh) * p.cache.head_stride * S::ES;
 
-        auto run_tile = [&](const uint8_t* kt, const uint8_t* vt, int k0) {
+        // The scale's sign goes into the queries, so that the largest score
+        // stays the largest; a scale of zero becomes one that leaves scores
+        // equal.
+        float c = p.scale * ks * kLog2e;
+        if (c < 0.0f) {
+            c = -c;
+#pragma unroll
+            for (int t = 0; t < S::STEPS; ++t) st.q[t] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, st.q[t]) ^ 0x80008000u);
+        }
+        if (c < 1e-37f) c = 1e-37f;
+
+        const auto run_tile = [&](uint32_t at_lds, int k0) {
             if (!busy || k0 >= any_hi || k0 + S::KT <= any_lo) return;
-            compute<S>(st, kt, vt, k0, c, k0 < all_lo || k0 + S::KT > all_hi);
+            const uint8_t* kt = lds + (at_lds - lds0);
+            compute<S>(st, kt, kt + S::TILE, k0, c, k0 < all_lo || k0 + S::KT > all_hi, ulane);
         };
 
         // ---- segments of the run whose page ids fit the list
-        for (int done = 0; done < count && g.hi > g.lo;) {
-            const int start = g.base + (from + done) * S::STEP;
-            ld.first_page = start >> p.cache.page_shift;
+        for (int done = 0; done < count && u.hi > u.lo;) {
+            const int start = __builtin_amdgcn_readfirstlane(u.base + (from + done) * S::STEP);
+            ld.first_page = start >> p.page_shift;
             // steps whose last key's page is in the list
-            const int64_t span = (int64_t(ld.first_page + kListPages) << p.cache.page_shift) - start;
+            const int64_t span = (int64_t(ld.first_page + kListPages) << p.page_shift) - start;
             const int n = int(min(int64_t(count - done), span / S::STEP));
-            const int want = int(min(int64_t(kListPages), (int64_t(start) + int64_t(n) * S::STEP - 1 >> p.cache.page_shift) - ld.first_page + 1));
+            const int want = int((uint32_t(start + n * S::STEP - 1) >> p.page_shift) - ld.first_page + 1);
             __syncthreads();
             for (int i = threadIdx.x; i < want; i += S::THREADS) {
                 int id = -1;
                 if (ld.first_page + i < ld.pages) id = ld.table[ld.first_page + i];
-                list[i] = id >= p.cache.pages ? -1 : id;
+                list[i] = id >= p.pages ? -1 : id;
             }
             __syncthreads();
+            bool dirty = false, next = false;
             if (S::SHARED) {
                 const int row0 = wave * S::ROWS;
-                bool dirty = ld.issue(lds, lds + S::TILE, start, row0);
-                for (int i = 0; i < n; ++i) {
-                    uint8_t* kt = lds + (i & 1) * 2 * S::TILE;
+                for (int i = -1; i < n; ++i) {
+                    const uint32_t kt = lds0 + (i & 1) * 2 * S::TILE;
                     const int k0 = start + i * S::STEP;
-                    wait_loads<0>();
-                    if (dirty) ld.patch(kt, kt + S::TILE, k0, row0);
-                    __syncthreads();
+                    if (i >= 0) {
+                        wait_loads<0>();
+                        if (dirty) ld.patch(lds + (kt - lds0), lds + (kt - lds0) + S::TILE, k0, row0);
+                        __syncthreads();
+                    }
                     if (i + 1 < n) {
-                        uint8_t* nt = lds + ((i + 1) & 1) * 2 * S::TILE;
+                        const uint32_t nt = lds0 + ((i + 1) & 1) * 2 * S::TILE;
                         dirty = ld.issue(nt, nt + S::TILE, k0 + S::STEP, row0);
                     }
-                    run_tile(kt, kt + S::TILE, k0);
+                    if (i >= 0) run_tile(kt, k0);
                 }
             } else {
-                uint8_t* ring = lds + wave * 4 * S::TILE;
+                const uint32_t ring = lds0 + wave * 4 * S::TILE;
                 const int k1 = start + wave * S::KT;
-                bool dirty = ld.issue(ring, ring + S::TILE, k1, 0), next = false;
-                for (int i = 0; i < n; ++i) {
-                    uint8_t* kt = ring + (i & 1) * 2 * S::TILE;
+                for (int i = -1; i < n; ++i) {
+                    const uint32_t kt = ring + (i & 1) * 2 * S::TILE;
                     const int k0 = k1 + i * S::STEP;
                     if (i + 1 < n) {
-                        uint8_t* nt = ring + ((i + 1) & 1) * 2 * S::TILE;
+                        const uint32_t nt = ring + ((i + 1) & 1) * 2 * S::TILE;
                         wait_lds();
                         next = ld.issue(nt, nt + S::TILE, k0 + S::STEP, 0);
-                        wait_loads<2 * S::LOADS>();
-                    } else {
-                        wait_loads<0>();
                     }
-                    if (dirty) ld.patch(kt, kt + S::TILE, k0, 0);
-                    run_tile(kt, kt + S::TILE, k0);
+                    if (i >= 0) {
+                        if (i + 1 < n) wait_loads<2 * S::LOADS>();
+                        else wait_loads<0>();
+                        if (dirty) ld.patch(lds + (kt - lds0), lds + (kt - lds0) + S::TILE, k0, 0);
+                        run_tile(kt, k0);
+                    }
                     dirty = next;
                 }
             }
@@ -711,33 +764,38 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
         }
         st.l += other_half(st.l);
         __syncthreads();
-        if (plan[5]) restore(st, p, ld, g.base + from * S::STEP, g.base + (from + count) * S::STEP);
+        if (plan[5]) restore(st, p, ld, u.base + from * S::STEP, u.base + (from + count) * S::STEP);
 
         // ---- results: whole units to the output, parts to the workspace
-        const bool whole = count == steps;
-        const float vs = S::E4M3 ? p.cache.v_scale[kvh] : 1.0f;
-        float* slot = slots + (run * 2 + (off > 0 ? 0 : 1)) * S::SLOT;
-        auto put_out = [&](int row, int d, float a0, float a1, float a2, float a3, float inv) {
-            const int rr = tile * S::M + row;
-            uint16_t* o = p.out + (s.q0 + rr / p.group) * p.o_token + (kvh * p.group + rr % p.group) * p.o_head + d;
+        const bool whole = count == u.steps;
+        const int tid = opaque(threadIdx.x), lane2 = tid & 63, col2 = lane2 & 31, h2 = lane2 >> 5;
+        const float vs = S::E4M3 ? p.v_scale[kvh] : 1.0f;
+        float* slots = reinterpret_cast<float*>(p.workspace + (size_t(p.counters) * 4 + 255) / 256 * 256);
+        float* slot = slots + uint64_t(run * 2 + (off > 0 ? 0 : 1)) * S::SLOT;
+        const auto put_out = [&](int row, int d, float a0, float a1, float a2, float a3, float inv) {
+            const uint32_t r = uint32_t(u.lane0 + row), step = by_group(p, r);
+            const uint32_t head = uint32_t(kvh) * uint32_t(p.group) + (r - step * uint32_t(p.group));
+            uint16_t* o = p.out + uint64_t(uint32_t(s.q0 + u.token0) + step) * p.o_token + uint64_t(head) * p.o_head + d;
             *reinterpret_cast<u32x2*>(o) = u32x2{pack_bf16(a0 * inv, a1 * inv), pack_bf16(a2 * inv, a3 * inv)};
         };
-        auto put_lse = [&](int row, float m, float l) {
-            const int rr = tile * S::M + row;
-            p.lse[(s.q0 + rr / p.group) * p.lse_token + kvh * p.group + rr % p.group] =
+        const auto put_lse = [&](int row, float m, float l) {
+            const uint32_t r = uint32_t(u.lane0 + row), step = by_group(p, r);
+            const uint32_t head = uint32_t(kvh) * uint32_t(p.group) + (r - step * uint32_t(p.group));
+            p.lse[uint64_t(uint32_t(s.q0 + u.token0) + step) * p.lse_token + head] =
                 m == -INFINITY && l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
         };
         // rows that see nothing have l = 0 and o = 0
-        auto inverse = [&](float l) { return l == 0.0f ? 0.0f : vs / l; };
+        const auto inverse = [&](float l) { return l == 0.0f ? 0.0f : vs / l; };
         if (S::SHARED) {
-            if (live) {
+            const int row = wave * 32 + col2;
+            if (row < u.rows) {
                 const float inv = inverse(st.l);
 #pragma unroll
                 for (int d = 0; d < S::DB; ++d)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const int at_d = 32 * d + 8 * x + 4 * h;
-                        if (at_d >= dim) continue;
+                        const int at_d = 32 * d + 8 * x + 4 * h2;
+                        if (!S::FULL && at_d >= p.dim) continue;
                         if (whole) {
                             put_out(row, at_d, st.o[d][4 * x], st.o[d][4 * x + 1], st.o[d][4 * x + 2], st.o[d][4 * x + 3], inv);
                         } else {
@@ -746,49 +804,57 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
                             put2(o + 2, st.o[d][4 * x + 2], st.o[d][4 * x + 3]);
                         }
                     }
-                if (h == 0) {
+                if (h2 == 0) {
                     if (!whole) put2(slot + S::M * S::DP + 2 * row, st.m, st.l);
                     else if (p.lse) put_lse(row, st.m, st.l);
                 }
             }
         } else {
             // the waves' sums meet in LDS
-            __syncthreads();
-            if (h == 0) ml[wave * 32 + col] = st.m, ml[(S::W + wave) * 32 + col] = st.l;
+            if (h2 == 0) ml[wave * 32 + col2] = st.m, ml[(S::W + wave) * 32 + col2] = st.l;
             __syncthreads();
             float m = -INFINITY, l = 0.0f;
-            for (int w = 0; w < S::W; ++w) m = fmaxf(m, ml[w * 32 + col]);
+#pragma unroll
+            for (int w = 0; w < S::W; ++w) m = fmaxf(m, ml[w * 32 + col2]);
             const float ref = m == -INFINITY ? 0.0f : m;
-            for (int w = 0; w < S::W; ++w) l += ml[(S::W + w) * 32 + col] * __builtin_amdgcn_exp2f(ml[w * 32 + col] - ref);
+#pragma unroll
+            for (int w = 0; w < S::W; ++w) l += ml[(S::W + w) * 32 + col2] * __builtin_amdgcn_exp2f(ml[w * 32 + col2] - ref);
             const float keep = __builtin_amdgcn_exp2f(st.m - ref);
-            float* buf = reinterpret_cast<float*>(lds) + wave * S::M * S::OS;
-            if (live) {
+            float* buf = reinterpret_cast<float*>(lds) + wave * S::M * S::OS + col2 * S::OS + 4 * h2;
+            if (col2 < u.rows) {
 #pragma unroll
                 for (int d = 0; d < S::DB; ++d)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         float4 v = {st.o[d][4 * x] * keep, st.o[d][4 * x + 1] * keep, st.o[d][4 * x + 2] * keep, st.o[d][4 * x + 3] * keep};
-                        *reinterpret_cast<float4*>(buf + col * S::OS + 32 * d + 8 * x + 4 * h) = v;
+                        *reinterpret_cast<float4*>(buf + 32 * d + 8 * x) = v;
                     }
+                if (wave == 0 && h2 == 0) {
+                    if (!whole) put2(slot + S::M * S::DP + 2 * col2, m, l);
+                    else if (p.lse) put_lse(col2, m, l);
+                }
             }
             __syncthreads();
-            if (wave == 0 && h == 0) ml[col] = m, ml[S::W * 32 + col] = l;
-            if (wave == 0 && h == 0 && live) {
-                if (!whole) put2(slot + S::M * S::DP + 2 * row, m, l);
-                else if (p.lse) put_lse(row, m, l);
-            }
-            __syncthreads();
-            const int quads = dim / 4;
-            for (int i = threadIdx.x; i < rows * quads; i += S::THREADS) {
-                const int rw = i / quads, d = (i % quads) * 4;
+            // (references and sums of the rows stay in ml)
+            constexpr int QUADS = S::DP / 4;
+            for (int i = tid; i < u.rows * QUADS; i += S::THREADS) {
+                const int rw = i / QUADS, d = (i % QUADS) * 4;
+                if (!S::FULL && d >= p.dim) continue;
                 const float* src = reinterpret_cast<const float*>(lds) + rw * S::OS + d;
                 float4 a = *reinterpret_cast<const float4*>(src);
+#pragma unroll
                 for (int w = 1; w < S::W; ++w) {
                     const float4 v = *reinterpret_cast<const float4*>(src + w * S::M * S::OS);
                     a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
                 }
                 if (whole) {
-                    put_out(rw, d, a.x, a.y, a.z, a.w, inverse(ml[S::W * 32 + rw]));
+                    float m = -INFINITY, l = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < S::W; ++w) m = fmaxf(m, ml[w * 32 + rw]);
+                    const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                    for (int w = 0; w < S::W; ++w) l += ml[(S::W + w) * 32 + rw] * __builtin_amdgcn_exp2f(ml[w * 32 + rw] - ref);
+                    put_out(rw, d, a.x, a.y, a.z, a.w, inverse(l));
                 } else {
                     put2(slot + rw * S::DP + d, a.x, a.y);
                     put2(slot + rw * S::DP + d + 2, a.z, a.w);
@@ -796,68 +862,63 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
             }
         }
 
-        // The unit's parts, run by run.  Each part's share, exp2(its reference
-        // less the largest), is worked out once a row, then every thread adds
-        // up places of its own, eight parts' loads at a time.
-        const auto join = [&](int64_t unit_start, int steps, int rows) {
-            const int64_t wf = run_of(unit_start + S::EXTRA), wl = run_of(unit_start + S::EXTRA + steps - 1);
-            const auto part = [&](int64_t w) { return slots + (w * 2 + (run_start(w) > unit_start ? 0 : 1)) * S::SLOT; };
-            const int parts = int(wl - wf + 1), quads = dim / 4;
-            for (int i = threadIdx.x; i < rows * quads; i += S::THREADS) {
-                const int rw = i / quads, d = (i % quads) * 4;
-                float m = -INFINITY, l = 0.0f, a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                for (int x = 0; x < parts; x += 8) {
-                    float pm[8], pl[8], v[8][4];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        // past the last part: the last again, with no share
-                        const float* src = part(wf + min(x + e, parts - 1));
-                        get2(src + S::M * S::DP + 2 * rw, &pm[e], &pl[e]);
-                        get2(src + rw * S::DP + d, &v[e][0], &v[e][1]);
-                        get2(src + rw * S::DP + d + 2, &v[e][2], &v[e][3]);
-                    }
-                    float mn = m;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) mn = fmaxf(mn, pm[e]);
-                    const float ref = mn == -INFINITY ? 0.0f : mn, keep = __builtin_amdgcn_exp2f(m - ref);
-                    m = mn;
-                    l *= keep;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) a[j] *= keep;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        if (x + e >= parts) break;
-                        const float share = __builtin_amdgcn_exp2f(pm[e] - ref);
-                        l += pl[e] * share;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) a[j] += v[e][j] * share;
-                    }
-                }
-                put_out(rw, d, a[0], a[1], a[2], a[3], inverse(l));
-                if (d == 0 && p.lse) put_lse(rw, m, l);
-            }
-        };
-
         if (!whole) {
             // The partial stores have reached the device-wide level before
             // this work-group counts its steps; whoever completes the count
             // finds every part there.
             wait_loads<0>();
             __syncthreads();
-            const int64_t unit_start = at - off;
             if (threadIdx.x == 0) {
-                uint32_t* cnt = arrived + int64_t(kvh) * head_units + unit;
+                uint32_t* cnt = reinterpret_cast<uint32_t*>(p.workspace) + int64_t(kvh) * head_units + unit;
                 const uint32_t old = __hip_atomic_fetch_add(cnt, uint32_t(count), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                const bool last = old + uint32_t(count) == uint32_t(steps);
+                const bool last = old + uint32_t(count) == uint32_t(u.steps);
                 if (last) __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
                 plan[4] = last;
             }
             __syncthreads();
             if (plan[4]) {
-                join(unit_start, steps, rows);
+                // The unit's parts in run order, eight parts' loads at a time.
+                const int64_t begin = at - off;
+                const int wf = run_of(begin + S::EXTRA), parts = run_of(begin + S::EXTRA + u.steps - 1) - wf + 1;
+                // only the first can have begun in its run, all others continue one
+                const int slot0 = wf * 2 + (run_start(wf) > begin ? 0 : 1);
+                constexpr int QUADS = S::DP / 4;
+                for (int i = opaque(threadIdx.x); i < u.rows * QUADS; i += S::THREADS) {
+                    const int rw = i / QUADS, d = (i % QUADS) * 4;
+                    if (!S::FULL && d >= p.dim) continue;
+                    float m = -INFINITY, l = 0.0f, a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int x = 0; x < parts; x += 8) {
+                        float pm[8], pl[8], v[8][4];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            pm[e] = -INFINITY, pl[e] = v[e][0] = v[e][1] = v[e][2] = v[e][3] = 0.0f;
+                            if (x + e >= parts) continue;
+                            const float* src = slots + uint64_t(x + e ? 2 * (wf + x + e) : slot0) * S::SLOT;
+                            get2(src + S::M * S::DP + 2 * rw, &pm[e], &pl[e]);
+                            get2(src + rw * S::DP + d, &v[e][0], &v[e][1]);
+                            get2(src + rw * S::DP + d + 2, &v[e][2], &v[e][3]);
+                        }
+                        float mn = m;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) mn = fmaxf(mn, pm[e]);
+                        const float ref = mn == -INFINITY ? 0.0f : mn, keep = __builtin_amdgcn_exp2f(m - ref);
+                        m = mn;
+                        l *= keep;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) a[j] *= keep;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float share = __builtin_amdgcn_exp2f(pm[e] - ref);
+                            l += pl[e] * share;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) a[j] += v[e][j] * share;
+                        }
+                    }
+                    put_out(rw, d, a[0], a[1], a[2], a[3], inverse(l));
+                    if (d == 0 && p.lse) put_lse(rw, m, l);
+                }
             }
         }
-
         __syncthreads();
         // the joining buffer wrote over the tiles' empty dimensions
         if (!S::SHARED) clear();
@@ -869,7 +930,7 @@ template <class S>
 int64_t workers(int64_t tokens, int group, int kv_heads, int seqs, int64_t max_kv)
 {
     const int64_t units = (tokens * group / S::M + seqs) * kv_heads;
-    const int64_t steps = (max_kv + 15 + S::STEP - 1) / S::STEP + 1;
+    const int64_t steps = (max_kv + 15 + S::STEP - 1) / S::STEP + 1 + S::EXTRA;
     const int64_t most = kComputeUnits * S::PER_CU, need = units * steps / S::LEAST + 1;
     return need < most ? (need + 7) / 8 * 8 : most;
 }
@@ -888,10 +949,10 @@ size_t bytes(int64_t tokens, int group, int kv_heads, int seqs, int64_t max_kv)
 }
 
 template <class S>
-hipError_t run(const AttnParams& p, hipStream_t s)
+hipError_t run(const AttnParams& a, Args p, hipStream_t s)
 {
-    const int64_t grid = workers<S>(p.tokens, p.group, p.cache.kv_heads, p.seqs, p.max_kv);
-    const int64_t counters = unit_bound<S>(p.tokens, p.group, p.cache.kv_heads, p.seqs);
+    const int64_t grid = workers<S>(a.tokens, a.group, a.cache.kv_heads, a.seqs, a.max_kv);
+    p.counters = int32_t(unit_bound<S>(a.tokens, a.group, a.cache.kv_heads, a.seqs));
     static const hipError_t attr = [] {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(attention_kernel<S>),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS);
@@ -899,7 +960,7 @@ hipError_t run(const AttnParams& p, hipStream_t s)
         return e;
     }();
     if (attr != hipSuccess && S::LDS > 64 * 1024) return attr;
-    hipLaunchKernelGGL((attention_kernel<S>), dim3(unsigned(grid)), dim3(S::THREADS), S::LDS, s, p, counters);
+    hipLaunchKernelGGL((attention_kernel<S>), dim3(unsigned(grid)), dim3(S::THREADS), S::LDS, s, p);
     return hipGetLastError();
 }
 
@@ -909,10 +970,13 @@ auto with_shape(bool e4m3, int dim, bool shared, F f)
 {
     const auto by_dim = [&](auto e, auto sh) {
         constexpr bool E = decltype(e)::value, SH = decltype(sh)::value;
-        if (dim <= 64) return f(Shape<64, E, SH>());
-        if (dim <= 96) return f(Shape<96, E, SH>());
-        if (dim <= 128) return f(Shape<128, E, SH>());
-        return f(Shape<256, E, SH>());
+        if (dim == 64) return f(Shape<64, E, SH, true>());
+        if (dim == 128) return f(Shape<128, E, SH, true>());
+        if (dim == 256) return f(Shape<256, E, SH, true>());
+        if (dim <= 64) return f(Shape<64, E, SH, false>());
+        if (dim <= 96) return f(Shape<96, E, SH, false>());
+        if (dim <= 128) return f(Shape<128, E, SH, false>());
+        return f(Shape<256, E, SH, false>());
     };
     if (e4m3) return shared ? by_dim(std::true_type(), std::true_type()) : by_dim(std::true_type(), std::false_type());
     return shared ? by_dim(std::false_type(), std::true_type()) : by_dim(std::false_type(), std::false_type());
@@ -932,10 +996,45 @@ size_t attention_workspace_bytes(bool e4m3, int64_t tokens, int q_heads, int kv_
     });
 }
 
-hipError_t launch_attention(const AttnParams& p, hipStream_t s)
+hipError_t launch_attention(const AttnParams& a, hipStream_t s)
 {
-    return with_shape(p.cache.e4m3, p.cache.head_dim, is_shared(p.max_q, p.group),
-                      [&](auto shape) { return run<decltype(shape)>(p, s); });
+    const int unit = a.cache.e4m3 ? 16 : 8;   // elements in 16 bytes
+    const int64_t cap = a.table_cols << a.cache.page_shift;
+    Args p;
+    p.k = a.cache.k;
+    p.v = a.cache.v;
+    p.k_scale = a.cache.k_scale;
+    p.v_scale = a.cache.v_scale;
+    p.q = a.q;
+    p.out = a.out;
+    p.lse = a.lse;
+    p.q_start = a.q_start;
+    p.kv_len = a.kv_len;
+    p.table = a.table;
+    p.workspace = static_cast<uint8_t*>(a.workspace);
+    p.page16 = uint32_t(a.cache.page_stride / unit);
+    p.head16 = uint32_t(a.cache.head_stride / unit);
+    p.slot16 = uint32_t(a.cache.slot_stride / unit);
+    p.q_token = uint32_t(a.q_token);
+    p.q_head = uint32_t(a.q_head);
+    p.o_token = uint32_t(a.o_token);
+    p.o_head = uint32_t(a.o_head);
+    p.lse_token = uint32_t(a.lse_token);
+    p.table_stride = uint32_t(a.table_stride);
+    p.pages = int32_t(a.cache.pages);
+    p.kv_heads = a.cache.kv_heads;
+    p.page_shift = a.cache.page_shift;
+    p.dim = a.cache.head_dim;
+    p.tokens = int32_t(a.tokens);
+    p.max_q = int32_t(a.max_q);
+    p.cap = int32_t(cap < a.max_kv ? cap : a.max_kv);
+    p.window = a.window > kMaxWindow ? kMaxWindow : int32_t(a.window);
+    p.seqs = a.seqs;
+    p.group = a.group;
+    p.by_group = uint32_t(((uint64_t(1) << 31) + a.group - 1) / a.group);
+    p.scale = a.scale;
+    return with_shape(a.cache.e4m3, a.cache.head_dim, is_shared(a.max_q, a.group),
+                      [&](auto shape) { return run<decltype(shape)>(a, p, s); });
 }
 
 }  // namespace qg
