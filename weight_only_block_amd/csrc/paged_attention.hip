@@ -527,18 +527,51 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
 
     fetch_arguments<sizeof(Args)>();
 
-    // ---- the line of work: this run's part of it
-    int64_t mine = 0;
-    int mine_units = 0;
-    const int per = (p.seqs + S::THREADS - 1) / S::THREADS;
-    const int b0 = min(int(threadIdx.x) * per, p.seqs), b1 = min(b0 + per, p.seqs);
-    for (int b = b0; b < b1; ++b) {
-        const Seq s = load_seq(p, b);
-        if (p.seqs <= kListSeqs) seqs[b] = s;
-        const int tiles = seq_tiles<S>(p, s);
-        mine_units += tiles;
-        for (int t = 0; t < tiles; ++t) mine += make_unit<S>(p, s, t).steps + S::EXTRA;
+    // ---- the line of work: this run's part of it.  Each thread sums a run of
+    // units: those of some sequences, or where sequences have many tiles and
+    // fit the list, its share of all units.
+    int b0, t0 = 0, mine_units = 0;
+    if (S::SHARED && p.seqs <= kListSeqs) {
+        for (int b = threadIdx.x; b < p.seqs; b += S::THREADS) seqs[b] = load_seq(p, b);
+        __syncthreads();
+        int units = 0;
+        for (int b = 0; b < p.seqs; ++b) units += seq_tiles<S>(p, seqs[b]);
+        const int per = (units + S::THREADS - 1) / S::THREADS, u0 = min(int(threadIdx.x) * per, units);
+        mine_units = min(per, units - u0);
+        int before = 0;
+        for (b0 = 0; b0 < p.seqs; ++b0) {
+            const int tiles = seq_tiles<S>(p, seqs[b0]);
+            if (u0 < before + tiles) break;
+            before += tiles;
+        }
+        t0 = u0 - before;
+    } else {
+        const int per = (p.seqs + S::THREADS - 1) / S::THREADS;
+        b0 = min(int(threadIdx.x) * per, p.seqs);
+        for (int b = b0; b < min(b0 + per, p.seqs); ++b) {
+            const Seq s = load_seq(p, b);
+            if (p.seqs <= kListSeqs) seqs[b] = s;
+            mine_units += seq_tiles<S>(p, s);
+        }
     }
+    // The units of this thread one after another, until `f` says so.
+    const auto walk = [&](auto f) {
+        int b = b0, t = t0;
+        for (int k = 0; k < mine_units; ++k) {
+            Seq s = get_seq(p, seqs, b);
+            while (t >= seq_tiles<S>(p, s)) {
+                t = 0;
+                s = get_seq(p, seqs, ++b);
+            }
+            if (f(b, t, k, make_unit<S>(p, s, t).steps + S::EXTRA)) break;
+            ++t;
+        }
+    };
+    int64_t mine = 0;
+    walk([&](int, int, int, int cost) {
+        mine += cost;
+        return false;
+    });
     int64_t upto = mine;
     int upto_units = mine_units;
     for (int off = 1; off < 64; off <<= 1) {
@@ -584,23 +617,14 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
         const int64_t r = at - kvh * head_steps;
         if (r >= upto - mine && r < upto) {
             int64_t left = r - (upto - mine);
-            int unit = upto_units - mine_units;
-            for (int b = b0; b < b1; ++b) {
-                const Seq s = get_seq(p, seqs, b);
-                const int tiles = seq_tiles<S>(p, s);
-                bool found = false;
-                for (int t = 0; t < tiles && !found; ++t) {
-                    const int n = make_unit<S>(p, s, t).steps + S::EXTRA;
-                    if (left < n) {
-                        plan[0] = b, plan[1] = t, plan[2] = left, plan[3] = unit;
-                        found = true;
-                    } else {
-                        left -= n;
-                        ++unit;
-                    }
+            walk([&](int b, int t, int k, int cost) {
+                if (left < cost) {
+                    plan[0] = b, plan[1] = t, plan[2] = left, plan[3] = upto_units - mine_units + k;
+                    return true;
                 }
-                if (found) break;
-            }
+                left -= cost;
+                return false;
+            });
         }
     }
     __syncthreads();
