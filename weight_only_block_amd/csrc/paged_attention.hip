@@ -193,9 +193,10 @@ struct Shape {
     static constexpr int PER_CU = BY_LDS < BY_WAVES ? BY_LDS : BY_WAVES;
     // Steps that a run has at least: a shorter one costs more in joining its
     // part than it saves.  What beginning and ending a unit costs, in steps.
-    static constexpr int LEAST = SHARED ? 8 : 4;
-    static constexpr int EXTRA = SHARED ? 4 : 3;
-    static constexpr int SLOT = M * DP + 2 * M;                         // floats of a partial result
+    static constexpr int LEAST = SHARED ? 4 : 2;
+    static constexpr int EXTRA = SHARED ? 5 : 3;
+    static constexpr float JOINED = SHARED ? 1.0f : 0.25f;               // what joining a part costs
+    static constexpr int SLOT = SHARED ? W * (DP * 32 + 128) : M * DP + 2 * M;   // floats of a partial result
     static constexpr int STEPS = DP / 16;                               // products along the dimension
     static constexpr int DB = DP / 32;
 
@@ -568,8 +569,10 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
         }
     };
     int64_t mine = 0;
+    int longest = 0;
     walk([&](int, int, int, int cost) {
         mine += cost;
+        longest = max(longest, cost);
         return false;
     });
     int64_t upto = mine;
@@ -578,9 +581,10 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
         const int64_t a = __shfl_up((long long)upto, off, 64);
         const int u = __shfl_up(upto_units, off, 64);
         if (lane >= off) upto += a, upto_units += u;
+        longest = max(longest, __shfl_xor(longest, off, 64));
     }
-    int64_t* sums = reinterpret_cast<int64_t*>(lds);              // [W] steps, [W] units
-    if (lane == 63) sums[wave] = upto, sums[S::W + wave] = upto_units;
+    int64_t* sums = reinterpret_cast<int64_t*>(lds);              // [W] each: steps, units, longest unit
+    if (lane == 63) sums[wave] = upto, sums[S::W + wave] = upto_units, sums[2 * S::W + wave] = longest;
     __syncthreads();
     int64_t head_steps = 0, before = 0;
     int head_units = 0, before_units = 0;
@@ -589,6 +593,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
         if (w == wave) before = head_steps, before_units = head_units;
         head_steps += sums[w];
         head_units += int(sums[S::W + w]);
+        longest = max(longest, int(sums[2 * S::W + w]));
     }
     upto += before;
     upto_units += before_units;
@@ -596,7 +601,10 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
     const int64_t total = head_steps * p.kv_heads;
     // starts that are not ascending claim more rows than there are
     if (total == 0 || int64_t(head_units) * p.kv_heads > p.counters) return;
-    const int runs = int(max(int64_t(1), min(int64_t(gridDim.x), total / S::LEAST)));
+    // A unit of n steps in runs of x takes about x + JOINED n / x steps: no
+    // shorter runs than where that is least, and no more runs than work-groups.
+    const float least = fmaxf(float(S::LEAST), __builtin_amdgcn_sqrtf(float(longest) * S::JOINED));
+    const int runs = __builtin_amdgcn_readfirstlane(int(fmaxf(1.0f, fminf(float(gridDim.x), float(total) / least))));
     // consecutive work-groups go to different XCDs: give each XCD one stretch
     // of the line, so that its L2 holds few heads' keys; few go over all XCDs
     const int xcds = gridDim.x % 8 == 0 ? 8 : 1;
@@ -810,28 +818,31 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
         };
         // rows that see nothing have l = 0 and o = 0
         const auto inverse = [&](float l) { return l == 0.0f ? 0.0f : vs / l; };
-        if (S::SHARED) {
+        // A part of a Shared unit is what the waves' lanes hold, register pair
+        // by register pair, so that its stores and loads are contiguous.
+        const uint32_t lane_at = uint32_t(wave) * (S::DB * 8 + 1) * 128 + 2 * lane2;
+        const auto write_rows = [&] {
             const int row = wave * 32 + col2;
-            if (row < u.rows) {
-                const float inv = inverse(st.l);
+            if (row >= u.rows) return;
+            const float inv = inverse(st.l);
+#pragma unroll
+            for (int d = 0; d < S::DB; ++d)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int at_d = 32 * d + 8 * x + 4 * h2;
+                    if (!S::FULL && at_d >= p.dim) continue;
+                    put_out(row, at_d, st.o[d][4 * x], st.o[d][4 * x + 1], st.o[d][4 * x + 2], st.o[d][4 * x + 3], inv);
+                }
+            if (p.lse && h2 == 0) put_lse(row, st.m, st.l);
+        };
+        if (S::SHARED) {
+            if (!whole && busy) {
+                float* o = slot + lane_at;
 #pragma unroll
                 for (int d = 0; d < S::DB; ++d)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int at_d = 32 * d + 8 * x + 4 * h2;
-                        if (!S::FULL && at_d >= p.dim) continue;
-                        if (whole) {
-                            put_out(row, at_d, st.o[d][4 * x], st.o[d][4 * x + 1], st.o[d][4 * x + 2], st.o[d][4 * x + 3], inv);
-                        } else {
-                            float* o = slot + row * S::DP + at_d;
-                            put2(o, st.o[d][4 * x], st.o[d][4 * x + 1]);
-                            put2(o + 2, st.o[d][4 * x + 2], st.o[d][4 * x + 3]);
-                        }
-                    }
-                if (h2 == 0) {
-                    if (!whole) put2(slot + S::M * S::DP + 2 * row, st.m, st.l);
-                    else if (p.lse) put_lse(row, st.m, st.l);
-                }
+                    for (int i = 0; i < 8; ++i) put2(o + (8 * d + i) * 128, st.o[d][2 * i], st.o[d][2 * i + 1]);
+                put2(o + S::DB * 8 * 128, st.m, st.l);
             }
         } else {
             // the waves' sums meet in LDS
@@ -886,6 +897,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
             }
         }
 
+        bool ready = whole;     // the unit's sums are complete
         if (!whole) {
             // The partial stores have reached the device-wide level before
             // this work-group counts its steps; whoever completes the count
@@ -901,13 +913,46 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
             }
             __syncthreads();
             if (plan[4]) {
-                // The unit's parts in run order, eight parts' loads at a time.
+                // The unit's parts in run order; Split: eight parts' loads at a time.
                 const int64_t begin = at - off;
                 const int wf = run_of(begin + S::EXTRA), parts = run_of(begin + S::EXTRA + u.steps - 1) - wf + 1;
                 // only the first can have begun in its run, all others continue one
                 const int slot0 = wf * 2 + (run_start(wf) > begin ? 0 : 1);
+                if constexpr (S::SHARED) if (busy) {
+                    st.m = -INFINITY;
+                    st.l = 0.0f;
+#pragma unroll
+                    for (int d = 0; d < S::DB; ++d)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) st.o[d][i] = 0.0f;
+#pragma unroll 1
+                    for (int x = 0; x < parts; ++x) {
+                        const float* src = slots + uint64_t(x ? 2 * (wf + x) : slot0) * S::SLOT + lane_at;
+                        float pm, pl;
+                        get2(src + S::DB * 8 * 128, &pm, &pl);
+                        const float m = fmaxf(st.m, pm), ref = m == -INFINITY ? 0.0f : m;
+                        const float keep = __builtin_amdgcn_exp2f(st.m - ref), share = __builtin_amdgcn_exp2f(pm - ref);
+                        st.m = m;
+                        st.l = st.l * keep + pl * share;
+#pragma unroll
+                        for (int d0 = 0; d0 < S::DB; d0 += 4) {
+                            float v[4][16];          // four blocks' loads at a time
+#pragma unroll
+                            for (int d = 0; d < 4 && d0 + d < S::DB; ++d)
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    get2(src + (8 * (d0 + d) + i) * 128, &v[d][2 * i], &v[d][2 * i + 1]);
+                            asm volatile("" ::: "memory");
+#pragma unroll
+                            for (int d = 0; d < 4 && d0 + d < S::DB; ++d)
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) st.o[d0 + d][i] = st.o[d0 + d][i] * keep + v[d][i] * share;
+                        }
+                    }
+                }
+                ready = true;
                 constexpr int QUADS = S::DP / 4;
-                for (int i = opaque(threadIdx.x); i < u.rows * QUADS; i += S::THREADS) {
+                for (int i = opaque(threadIdx.x); !S::SHARED && i < u.rows * QUADS; i += S::THREADS) {
                     const int rw = i / QUADS, d = (i % QUADS) * 4;
                     if (!S::FULL && d >= p.dim) continue;
                     float m = -INFINITY, l = 0.0f, a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -943,6 +988,8 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
                 }
             }
         }
+        if constexpr (S::SHARED)
+            if (ready && busy) write_rows();
         __syncthreads();
         // the joining buffer wrote over the tiles' empty dimensions
         if (!S::SHARED) clear();
