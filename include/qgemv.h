@@ -429,7 +429,7 @@ qg_status qg_rope_init(qg_rope *rope, int32_t rot_dim, int32_t interleaved, doub
  * +-448 and rounded to nearest even, NaN kept.
  * QG_ERR_INVALID_ARG: null pointer, tokens < 0, q_heads < 1, rot_dim above
  * head_dim, a stride out of 0..2^31, overlapping q_out rows; tokens = 0 does
- * nothing.  Pointers need their element's alignment; 16-byte aligned rows are
+ * nothing, and the stride of a dimension of one entry is ignored.  Pointers need their element's alignment; 16-byte aligned rows are
  * read and written in wide accesses. */
 #define QG_SRC_F32 0
 #define QG_SRC_BF16 1

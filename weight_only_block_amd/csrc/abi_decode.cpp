@@ -118,6 +118,10 @@ qg_status qg_rope_append(const qg_kv_cache* cache, const qg_rope* rope, const vo
     qg::RopeParams p;
     const qg_status st = check_cache(cache, &p.cache);
     if (st != QG_OK) return st;
+    // a dimension of one entry has no stride that matters
+    if (tokens <= 1) q_token_stride = k_token_stride = v_token_stride = out_token_stride = 0;
+    if (q_heads == 1) q_head_stride = out_head_stride = 0;
+    if (p.cache.kv_heads == 1) k_head_stride = v_head_stride = 0;
     if (rope->rot_dim < 2 || rope->rot_dim % 2 != 0 || rope->rot_dim > p.cache.head_dim) return QG_ERR_INVALID_ARG;
     const int64_t strides[] = {q_token_stride, q_head_stride, k_token_stride, k_head_stride,
                                v_token_stride, v_head_stride, out_token_stride, out_head_stride};
@@ -194,6 +198,10 @@ qg_status qg_paged_attention(const qg_kv_cache* cache, const uint16_t* q_bf16, i
     qg::AttnParams p;
     const qg_status st = check_attention_shape(cache, tokens, q_heads, seqs, max_q, max_kv, &p.cache);
     if (st != QG_OK) return st;
+    // a dimension of one entry has no stride that matters
+    if (tokens <= 1) q_token_stride = out_token_stride = lse_token_stride = 0;
+    if (q_heads == 1) q_head_stride = out_head_stride = 0;
+    if (seqs <= 1) table_stride = 0;
     if (table_cols < 0 || table_cols > kMaxCount || !stride_ok(table_stride) || window < 0 || !std::isfinite(scale))
         return QG_ERR_INVALID_ARG;
     if (!stride_ok(q_token_stride) || !stride_ok(q_head_stride) || !stride_ok(out_token_stride) ||

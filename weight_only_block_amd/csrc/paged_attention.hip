@@ -913,7 +913,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
             }
             __syncthreads();
             if (plan[4]) {
-                // The unit's parts in run order; Split: eight parts' loads at a time.
+                // The unit's parts in run order; Split: sixteen parts' loads at a time.
                 const int64_t begin = at - off;
                 const int wf = run_of(begin + S::EXTRA), parts = run_of(begin + S::EXTRA + u.steps - 1) - wf + 1;
                 // only the first can have begun in its run, all others continue one
@@ -956,10 +956,10 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
                     const int rw = i / QUADS, d = (i % QUADS) * 4;
                     if (!S::FULL && d >= p.dim) continue;
                     float m = -INFINITY, l = 0.0f, a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    for (int x = 0; x < parts; x += 8) {
-                        float pm[8], pl[8], v[8][4];
+                    for (int x = 0; x < parts; x += 16) {
+                        float pm[16], pl[16], v[16][4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
+                        for (int e = 0; e < 16; ++e) {
                             pm[e] = -INFINITY, pl[e] = v[e][0] = v[e][1] = v[e][2] = v[e][3] = 0.0f;
                             if (x + e >= parts) continue;
                             const float* src = slots + uint64_t(x + e ? 2 * (wf + x + e) : slot0) * S::SLOT;
@@ -969,14 +969,14 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
                         }
                         float mn = m;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) mn = fmaxf(mn, pm[e]);
+                        for (int e = 0; e < 16; ++e) mn = fmaxf(mn, pm[e]);
                         const float ref = mn == -INFINITY ? 0.0f : mn, keep = __builtin_amdgcn_exp2f(m - ref);
                         m = mn;
                         l *= keep;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) a[j] *= keep;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
+                        for (int e = 0; e < 16; ++e) {
                             const float share = __builtin_amdgcn_exp2f(pm[e] - ref);
                             l += pl[e] * share;
 #pragma unroll

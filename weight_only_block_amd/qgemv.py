@@ -837,10 +837,8 @@ def rope_append(cache: KVCache, rope: Rope, q, k, v, pos, slots, q_out, stream=N
     so = _fits(q_out, where, "q_out", dt.bf16, shape, dev)
     _fits(pos, where, "pos", dt.i32, (tokens,), dev)
     _fits(slots, where, "slots", dt.i64, (tokens,), dev)
-    if tokens <= 1 or heads == 1 or kv[1] == 1:
-        if tokens == 0:
-            return QG_OK
-        sq, sk, sv, so = [(_step(t, 0), _step(t, 1)) for t in (q, k, v, q_out)]
+    if tokens == 0:
+        return QG_OK
     st = lib().qg_rope_append(cache._ref, rope._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                               SRC_F32 if kind == dt.f32 else SRC_BF16, sq[0], sq[1], sk[0], sk[1],
                               sv[0], sv[1], pos.data_ptr(), slots.data_ptr(), q_out.data_ptr(), so[0], so[1], tokens,
@@ -888,15 +886,12 @@ def paged_attention(cache: KVCache, q, out, q_start, kv_len, page_table, workspa
     _fits(q_start, where, "q_start", dt.i32, (seqs + 1,), dev)
     _fits(kv_len, where, "kv_len", dt.i32, (seqs,), dev)
     row = _fits(page_table, where, "page_table", dt.i32, table_shape, dev)[0]
-    if lse is not None:
-        _fits(lse, where, "lse", dt.f32, (tokens, heads), dev)
+    lse_row = 0 if lse is None else _fits(lse, where, "lse", dt.f32, (tokens, heads), dev)[0]
     room = _space(workspace, where, dev)
-    if tokens <= 1 or heads == 1 or seqs <= 1:
-        if tokens == 0 or seqs == 0:
-            return QG_OK
-        sq, so, row = (_step(q, 0), _step(q, 1)), (_step(out, 0), _step(out, 1)), _step(page_table, 0)
+    if tokens == 0 or seqs == 0:
+        return QG_OK
     st = lib().qg_paged_attention(cache._ref, q.data_ptr(), sq[0], sq[1], out.data_ptr(), so[0], so[1], _ptr(lse),
-                                  0 if lse is None else _step(lse, 0), q_start.data_ptr(), kv_len.data_ptr(),
+                                  lse_row, q_start.data_ptr(), kv_len.data_ptr(),
                                   page_table.data_ptr(), row, cols, tokens, heads, seqs, max_q, max_kv,
                                   dim ** -0.5 if scale is None else scale, window, workspace.data_ptr(), room,
                                   _stream_of(stream, dev))
