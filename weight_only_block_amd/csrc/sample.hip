@@ -79,7 +79,7 @@ struct RowSpace {
 __device__ __forceinline__ int weight_bits(int64_t N)
 {
     const int b = 62 - (64 - __clzll((long long)N));
-    return b > 52 ? 52 : b;
+    return b > 50 ? 50 : b;
 }
 
 __device__ __forceinline__ uint32_t order_of(float v) { return uint32_t(argmax_key(v, 0) >> 32); }
@@ -95,7 +95,8 @@ struct Row {
     double rate;          // log2(e) / temperature
     int64_t N, k;
     double top_p, floor;
-    int bits;
+    double unit;          // fixed-point steps of a weight of 1
+    const double* powers; // LDS: 2^(i / 128)
     bool greedy;
     int32_t top_idx;
 
@@ -107,31 +108,26 @@ struct Row {
     // out of the ranks behind every token that can be.
     static __device__ __forceinline__ bool nothing(double y) { return !(y >= -1100.0); }
 
-    // 2^y for y <= 0: 2^round(y) times the Taylor series of 2^f, |f| <= 1/2,
-    // whose 13th term is below 2^-52.
-    static __device__ __forceinline__ double weight(double y)
+    // 2^y for y <= 0 as 2^(n / 128) 2^f: the first factor from a table of 128
+    // and the exponent, the second by its Taylor series, |f ln 2| < 0.0028,
+    // whose sixth term is below 2^-60.
+    __device__ __forceinline__ double weight(double y) const
     {
         if (nothing(y)) return 0.0;
-        const double n = __builtin_rint(y);
-        const double f = (y - n) * 0.69314718055994530942;
-        double p = 1.0 / 479001600.0;
-        p = __builtin_fma(p, f, 1.0 / 39916800.0);
-        p = __builtin_fma(p, f, 1.0 / 3628800.0);
-        p = __builtin_fma(p, f, 1.0 / 362880.0);
-        p = __builtin_fma(p, f, 1.0 / 40320.0);
-        p = __builtin_fma(p, f, 1.0 / 5040.0);
-        p = __builtin_fma(p, f, 1.0 / 720.0);
-        p = __builtin_fma(p, f, 1.0 / 120.0);
-        p = __builtin_fma(p, f, 1.0 / 24.0);
-        p = __builtin_fma(p, f, 1.0 / 6.0);
-        p = __builtin_fma(p, f, 0.5);
-        p = __builtin_fma(p, f, 1.0);
-        p = __builtin_fma(p, f, 1.0);
-        return ldexp(p, int(n));
+        const double n = __builtin_rint(y * 128.0);
+        const double z = __builtin_fma(n, -1.0 / 128.0, y) * 0.69314718055994530942;
+        double p = __builtin_fma(z, 1.0 / 120.0, 1.0 / 24.0);
+        p = __builtin_fma(p, z, 1.0 / 6.0);
+        p = __builtin_fma(p, z, 0.5);
+        p = __builtin_fma(p, z, 1.0);
+        p = __builtin_fma(p, z, 1.0);
+        const int i = int(n);
+        return ldexp(p * powers[i & 127], i >> 7);
     }
+    // Rounded to an integer by adding 2^52: what is below the point leaves the mantissa.
     __device__ __forceinline__ unsigned long long fixed(double w) const
     {
-        return (unsigned long long)(ldexp(w, bits) + 0.5);
+        return (unsigned long long)__double_as_longlong(__builtin_fma(w, unit, 0x1p52)) & 0xfffffffffffffull;
     }
     // Weight of a kept token in the draw.
     __device__ __forceinline__ double drawn(float v) const
@@ -142,9 +138,21 @@ struct Row {
     __device__ __forceinline__ bool cut() const { return k < N || top_p < 1.0; }
 };
 
-__device__ __forceinline__ Row row_of(const SampleParams& p, int64_t row, uint64_t best)
+// 2^(i / 128) for i < 128: the Taylor series of exp(i ln 2 / 128), whose 18th
+// term is below 2^-58.
+__device__ __forceinline__ void fill_powers(double* powers)
+{
+    if (threadIdx.x >= 128) return;
+    const double z = double(threadIdx.x) * (0.69314718055994530942 / 128.0);
+    double p = 1.0;
+    for (int k = 17; k >= 1; --k) p = __builtin_fma(p, z / k, 1.0);
+    powers[threadIdx.x] = p;
+}
+
+__device__ __forceinline__ Row row_of(const SampleParams& p, int64_t row, uint64_t best, const double* powers)
 {
     Row r;
+    r.powers = powers;
     r.top_idx = key_index(best);
     r.top = value_of(uint32_t(best >> 32));
     const float t = p.temperature ? p.temperature[row] : 1.0f;
@@ -156,7 +164,7 @@ __device__ __forceinline__ Row row_of(const SampleParams& p, int64_t row, uint64
     const float tp = p.top_p ? p.top_p[row] : 1.0f, mp = p.min_p ? p.min_p[row] : 0.0f;
     r.top_p = tp < 1.0f ? double(tp) : 1.0;          // NaN: none
     r.floor = mp != mp ? 0.0 : fmin(double(mp), 1.0);
-    r.bits = weight_bits(p.N);
+    r.unit = ldexp(1.0, weight_bits(p.N));
     return r;
 }
 
@@ -207,6 +215,7 @@ __device__ __forceinline__ void wave_max(int* at, int v)
 }
 
 struct Shared {
+    double powers[128];
     unsigned long long weight[kBins];
     unsigned int count[kBins];
     ScanSpace<double> d;
@@ -252,7 +261,7 @@ __device__ void select(Shared& s, const Row& r, const float* x, bool by_count, u
             if ((o & known) != prefix) continue;
             const int bin = int((o >> shift) & ((1u << width) - 1));
             atomicAdd(&s.count[bin], 1u);
-            atomicAdd(&s.weight[bin], r.fixed(Row::weight(r.exponent(v))));
+            atomicAdd(&s.weight[bin], r.fixed(r.weight(r.exponent(v))));
         }
         __syncthreads();
         // thread t holds bins kBins - 1 - 2 t and the one below: descending
@@ -296,12 +305,12 @@ __device__ uint64_t cut_by_selection(Shared& s, const Row& r, const float* x)
         uint64_t ac, aw;
         select(s, r, x, true, uint64_t(r.k), 0.0, &cut, &ac, &aw, &ties);
         kept = uint64_t(r.k) - ac;
-        sum = aw + kept * r.fixed(Row::weight(r.exponent(value_of(cut))));
+        sum = aw + kept * r.fixed(r.weight(r.exponent(value_of(cut))));
     }
     if (r.top_p < 1.0) {
         if (r.k >= r.N) {
             unsigned long long mine = 0, all;
-            for (int64_t i = threadIdx.x; i < r.N; i += kThreads) mine += r.fixed(Row::weight(r.exponent(x[i])));
+            for (int64_t i = threadIdx.x; i < r.N; i += kThreads) mine += r.fixed(r.weight(r.exponent(x[i])));
             scan(s.u, mine, &all);
             sum = all;
         }
@@ -309,7 +318,7 @@ __device__ uint64_t cut_by_selection(Shared& s, const Row& r, const float* x)
         uint64_t ac, aw, pties;
         const double limit = r.top_p * double(sum);
         select(s, r, x, false, 0, limit, &pcut, &ac, &aw, &pties);
-        const uint64_t w = r.fixed(Row::weight(r.exponent(value_of(pcut))));
+        const uint64_t w = r.fixed(r.weight(r.exponent(value_of(pcut))));
         // ties j = 0, 1, ... are kept while the weight before them is below the limit
         uint64_t lo = 1, hi = pties;
         while (lo < hi) {
@@ -355,34 +364,42 @@ __device__ int pick_group(Shared& s, double mine, double run, double target)
 }
 
 // The token of [from, to) where the running sum of kept weights passes
-// `target`, else the last kept one: the first wave takes 64 at a time.
+// `target`, else the last kept one, r.N without any; by one wave, 256 tokens
+// at a time.
+__device__ int64_t walk_wave(const Row& r, const float* x, int64_t from, int64_t to, uint64_t cut, double run, double target)
+{
+    const int lane = threadIdx.x & 63;
+    int64_t last = r.N, found = r.N;
+    for (int64_t base = from; base < to && found == r.N; base += 256) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = base + 64 * e + lane < to ? x[base + 64 * e + lane] : -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t i = base + 64 * e + lane;
+            const double w = i < to && argmax_key(v[e], uint32_t(i)) >= cut ? r.drawn(v[e]) : 0.0;
+            double upto = w;
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                const double o = __shfl_up(upto, off, 64);
+                if (lane >= off) upto += o;
+            }
+            const uint64_t past = __ballot(w > 0.0 && run + upto > target), some = __ballot(w > 0.0);
+            if (past && found == r.N) found = base + 64 * e + __ffsll((unsigned long long)past) - 1;
+            if (some) last = base + 64 * e + 63 - __clzll((long long)some);
+            run += __shfl(upto, 63, 64);
+        }
+    }
+    return found < r.N ? found : last;
+}
+
+// The same for a work-group, whose first wave walks.
 __device__ int64_t walk_group(Shared& s, const Row& r, const float* x, int64_t from, int64_t to, uint64_t cut, double run,
                               double target)
 {
-    const int lane = threadIdx.x & 63;
     if (threadIdx.x < 64) {
-        int64_t last = r.N, found = r.N;
-        for (int64_t base = from; base < to && found == r.N; base += 256) {
-            float v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = base + 64 * e + lane < to ? x[base + 64 * e + lane] : -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int64_t i = base + 64 * e + lane;
-                const double w = i < to && argmax_key(v[e], uint32_t(i)) >= cut ? r.drawn(v[e]) : 0.0;
-                double upto = w;
-#pragma unroll
-                for (int off = 1; off < 64; off <<= 1) {
-                    const double o = __shfl_up(upto, off, 64);
-                    if (lane >= off) upto += o;
-                }
-                const uint64_t past = __ballot(w > 0.0 && run + upto > target), some = __ballot(w > 0.0);
-                if (past && found == r.N) found = base + 64 * e + __ffsll((unsigned long long)past) - 1;
-                if (some) last = base + 64 * e + 63 - __clzll((long long)some);
-                run += __shfl(upto, 63, 64);
-            }
-        }
-        if (lane == 0) s.pick = (unsigned long long)(found < r.N ? found : last);
+        const int64_t pick = walk_wave(r, x, from, to, cut, run, target);
+        if (threadIdx.x == 0) s.pick = (unsigned long long)pick;
     }
     __syncthreads();
     return int64_t(s.pick);
@@ -467,7 +484,7 @@ __device__ __forceinline__ void add_to_bins(Shared& s, const Row& r, const float
             if (Row::nothing(y)) continue;
             const int bin = bin_of(r.top, v[e]);
             if (rank) atomicAdd(&s.count[bin], 1u);
-            if (weigh) atomicAdd(&s.weight[bin], r.fixed(Row::weight(y)));
+            if (weigh) atomicAdd(&s.weight[bin], r.fixed(r.weight(y)));
         }
     }
     __syncthreads();
@@ -503,7 +520,8 @@ __global__ __launch_bounds__(kThreads) void sample_histogram(SampleParams p, Div
     __shared__ Shared s;
     const int64_t row = blockIdx.y;
     RowSpace& ws = static_cast<RowSpace*>(p.workspace)[row];
-    const Row r = row_of(p, row, row_best(ws));
+    fill_powers(s.powers);
+    const Row r = row_of(p, row, row_best(ws), s.powers);
     if (r.greedy || !r.cut()) return;
     const int64_t from = blockIdx.x * dv.chunk, to = min(p.N, from + dv.chunk);
     add_to_bins(s, r, p.x + row * p.ldx, from, to);
@@ -656,7 +674,7 @@ __device__ uint64_t cut_of_candidates(Shared& s, const Row& r, const Bins& b, un
         if (at + e >= n) continue;
         const float v = value_of(uint32_t(key[at + e] >> 32));
         const int bin = bin_of(r.top, v);
-        w[e] = r.fixed(Row::weight(r.exponent(v)));
+        w[e] = r.fixed(r.weight(r.exponent(v)));
         in_k[e] = bin == b.kbin;
         in_p[e] = bin >= b.first && bin <= b.second;
         if (in_p[e]) range = at + e + 1;
@@ -688,6 +706,109 @@ __device__ uint64_t cut_of_candidates(Shared& s, const Row& r, const Bins& b, un
     return s.bin2 ? key[s.bin2 - 1] : ~0ull;
 }
 
+__device__ __forceinline__ unsigned long long lane_value(unsigned long long v, int lane)
+{
+    const uint32_t lo = uint32_t(__builtin_amdgcn_readlane(int(v), lane)), hi = uint32_t(__builtin_amdgcn_readlane(int(v >> 32), lane));
+    return (unsigned long long)(hi) << 32 | lo;
+}
+
+// The value of the lane that sends to this one; `to` is a permutation of the lanes.
+__device__ __forceinline__ unsigned long long send(unsigned long long v, int to)
+{
+    const uint32_t lo = uint32_t(__builtin_amdgcn_ds_permute(4 * to, int(v)));
+    const uint32_t hi = uint32_t(__builtin_amdgcn_ds_permute(4 * to, int(v >> 32)));
+    return (unsigned long long)(hi) << 32 | lo;
+}
+
+// The end of a row with at most 64 candidates (the usual one), by one wave:
+// lane i holds candidate i (`key`, 0 past the n-th) and chunk i's sum (`own`).
+// `sums` gives the sum of a group of a chunk, group_sum is space for them.
+template <class F>
+__device__ int64_t finish_wave(const SampleParams& p, const Division& dv, const Row& r, const Bins& b, const float* x,
+                               unsigned long long key, int n, double own, double u, double* group_sum, F sums)
+{
+    const int lane = threadIdx.x & 63;
+    const bool is = lane < n;
+    const float v = value_of(uint32_t(key >> 32));
+    const int bin = is ? bin_of(r.top, v) : -1;
+    const unsigned long long w = is ? r.fixed(r.weight(r.exponent(v))) : 0;
+    // rank among the candidates and the weight before it
+    int rank = is ? 0 : lane;
+    unsigned long long before = 0;
+    for (int j = 0; j < n; ++j) {
+        const unsigned long long o = lane_value(key, j), ow = lane_value(w, j);
+        if (is && o > key) {
+            ++rank;
+            before += ow;
+        }
+    }
+    const bool in_k = is && bin == b.kbin, in_p = is && bin >= b.first && bin <= b.second;
+    const int in_range = __popcll(__ballot(in_p));
+    const uint64_t place = in_p ? b.first_count + rank : b.k_count + rank - in_range;
+    unsigned long long sum_k = in_k && place < uint64_t(r.k) ? w : 0;
+#pragma unroll
+    for (int off = 32; off; off >>= 1) sum_k += __shfl_xor(sum_k, off, 64);
+    sum_k = b.by_k ? b.k_weight + sum_k : b.total_weight;
+    const double limit = r.top_p * double(sum_k);
+    const bool keep = in_p && place < uint64_t(r.k) &&
+                      (r.top_p >= 1.0 || place == 0 || double(b.first_weight + before) < limit);
+    const int kept = __popcll(__ballot(keep));       // the first ones in order
+    // in order from here on
+    key = send(key, rank);
+    const uint64_t cut = n == 0 ? 0 : kept ? lane_value(key, kept - 1) : ~0ull;
+    const double mine = lane < kept ? r.drawn(value_of(uint32_t(key >> 32))) : 0.0;
+    const uint32_t index = ~uint32_t(key);
+    const int chunk = int(int64_t(index) / dv.chunk);
+    for (int j = 0; j < kept; ++j) {
+        const double add = __longlong_as_double((long long)lane_value((unsigned long long)__double_as_longlong(mine), j));
+        if (lane == __builtin_amdgcn_readlane(chunk, j)) own += add;
+    }
+    double upto = own;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const double o = __shfl_up(upto, off, 64);
+        if (lane >= off) upto += o;
+    }
+    const double target = u * __shfl(upto, 63, 64);
+    const uint64_t past = __ballot(own > 0.0 && upto > target);
+    if (!(u < 1.0) || !past) return p.N;
+    const int c = __ffsll((unsigned long long)past) - 1;
+    double run = __shfl(upto - own, c, 64);
+    // the chunk's groups, its kept candidates among them; a lane takes q of them
+    for (int g = lane; g < dv.groups; g += 64) group_sum[g] = sums(c, g);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    for (int j = 0; j < kept; ++j) {
+        if (__builtin_amdgcn_readlane(chunk, j) != c) continue;
+        const uint32_t i = uint32_t(__builtin_amdgcn_readlane(int(index), j));
+        if (lane == j) group_sum[int((int64_t(i) - c * dv.chunk) / dv.group)] += mine;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    const int q = (dv.groups + 63) / 64;
+    double strip = 0.0;
+    for (int i = 0; i < q; ++i)
+        if (lane * q + i < dv.groups) strip += group_sum[lane * q + i];
+    double sum = strip;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const double o = __shfl_up(sum, off, 64);
+        if (lane >= off) sum += o;
+    }
+    const uint64_t over = __ballot(strip > 0.0 && run + sum > target), some = __ballot(strip > 0.0);
+    if (!some) return p.N;
+    // (rounding may leave the target past the end)
+    const int at = over ? __ffsll((unsigned long long)over) - 1 : 63 - __clzll((long long)some);
+    run += __shfl(sum - strip, at, 64);
+    int g = -1;
+    for (int i = at * q; i < min((at + 1) * q, dv.groups); ++i) {
+        if (!(group_sum[i] > 0.0)) continue;
+        if (g >= 0) run += group_sum[g];
+        g = i;
+        if (run + group_sum[i] > target) break;
+    }
+    const int64_t f = c * dv.chunk + g * dv.group;
+    return walk_wave(r, x, f, min(p.N, f + dv.group), cut, run, target);
+}
+
 // ONE: a work-group has the whole row and does the first two steps as well.
 template <bool ONE>
 __global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p, Division dv)
@@ -700,7 +821,8 @@ __global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p, Division
     RowSpace& ws = static_cast<RowSpace*>(p.workspace)[ONE ? 0 : row];
     const float* x = p.x + row * p.ldx;
     const int64_t from = blockIdx.x * dv.chunk, to = min(p.N, from + dv.chunk);
-    const Row r = row_of(p, row, ONE ? top_of(s, x, from, to) : row_best(ws));
+    fill_powers(s.powers);
+    const Row r = row_of(p, row, ONE ? top_of(s, x, from, to) : row_best(ws), s.powers);
     if (r.greedy) {
         if (blockIdx.x == 0 && threadIdx.x == 0) p.idx[row] = r.top_idx;
         return;
@@ -722,41 +844,45 @@ __global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p, Division
     __syncthreads();
     if (threadIdx.x == 0) s.flag = 0;
     __syncthreads();
-    // Four tokens a lane at a time, the next four on their way meanwhile.
+    // Rounds of 256 tokens, four a lane; the next two rounds are on their way
+    // meanwhile.
     const int rounds = int(dv.group / 256);
-    const auto load = [&](int g, int j, float* v) {
-        const int64_t at = from + g * dv.group + j * 256 + lane;
+    const int mine = (max(0, dv.groups - wave) + kWaves - 1) / kWaves * rounds;    // of this wave
+    const auto place = [&](int i) { return from + (wave + i / rounds * kWaves) * dv.group + (i % rounds) * 256 + lane; };
+    const auto load = [&](int i, float* v) {
+        const int64_t at = place(i);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = g < dv.groups && at + 64 * e < to ? x[at + 64 * e] : -INFINITY;
+        for (int e = 0; e < 4; ++e) v[e] = i < mine && at + 64 * e < to ? x[at + 64 * e] : -INFINITY;
     };
-    float next[4];
-    load(wave, 0, next);
-    for (int g = wave; g < dv.groups; g += kWaves) {
-        double w = 0.0;
-        for (int j = 0; j < rounds; ++j) {
-            const int64_t at = from + g * dv.group + j * 256 + lane;
-            float v[4];
+    float ahead[2][4];
+    load(0, ahead[0]);
+    load(1, ahead[1]);
+    double w = 0.0;
+    for (int i = 0; i < mine; ++i) {
+        const int64_t at = place(i);
+        float v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = next[e];
-            if (j + 1 < rounds) load(g, j + 1, next);
-            else load(g + kWaves, 0, next);
+        for (int e = 0; e < 4; ++e) v[e] = ahead[0][e], ahead[0][e] = ahead[1][e];
+        load(i + 2, ahead[1]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int bin = cut ? bin_of(r.top, v[e]) : 0;
-                if (bin < b.first) {
-                    w += r.drawn(v[e]);
-                } else if ((bin <= b.second || bin == b.kbin) && !Row::nothing(r.exponent(v[e]))) {
-                    const int c = atomicAdd(&s.flag, 1);
-                    if (c < kCandidates) key[c] = argmax_key(v[e], uint32_t(at + 64 * e));
-                }
+        for (int e = 0; e < 4; ++e) {
+            const int bin = cut ? bin_of(r.top, v[e]) : 0;
+            if (bin < b.first) {
+                w += r.drawn(v[e]);
+            } else if ((bin <= b.second || bin == b.kbin) && !Row::nothing(r.exponent(v[e]))) {
+                const int c = atomicAdd(&s.flag, 1);
+                if (c < kCandidates) key[c] = argmax_key(v[e], uint32_t(at + 64 * e));
             }
         }
+        if ((i + 1) % rounds) continue;
 #pragma unroll
         for (int off = 32; off; off >>= 1) w += __shfl_xor(w, off, 64);
         if (lane == 0) {
+            const int g = wave + i / rounds * kWaves;
             group_sum[g] = w;
             if (!ONE) put(&groups[g], (unsigned long long)__double_as_longlong(w));
         }
+        w = 0.0;
     }
     __syncthreads();
     // the work-group's candidates join the row's list
@@ -789,6 +915,18 @@ __global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p, Division
         draw_by_selection(s, p, row, r);
         return;
     }
+    const double u = p.u[row];
+    if (n <= 64) {
+        if (wave != 0) return;
+        const unsigned long long mine = lane >= int(n) ? 0 : ONE ? key[lane] : get(&ws.candidate[lane]);
+        const double own = lane >= int(gridDim.x) ? 0.0 : ONE ? all : __longlong_as_double((long long)get(&ws.sum[lane]));
+        const int64_t pick = finish_wave(p, dv, r, b, x, mine, int(n), own, u, group_sum, [&](int c, int g) {
+            return ONE ? group_sum[g]
+                       : __longlong_as_double((long long)get(groups + (c - int(blockIdx.x)) * int64_t(dv.groups) + g));
+        });
+        if (lane == 0) p.idx[row] = pick < p.N ? int32_t(pick) : r.top_idx;
+        return;
+    }
     if (!ONE) {
         for (int i = threadIdx.x; i < int(n); i += kThreads) key[i] = get(&ws.candidate[i]);
         if (threadIdx.x < gridDim.x)
@@ -797,9 +935,8 @@ __global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p, Division
         chunk_sum[0] = all;
     }
     __syncthreads();
-    const uint64_t last = n == 0           ? 0
-                          : n <= kThreads ? cut_of_candidates<1>(s, r, b, key, int(n))
-                                          : cut_of_candidates<kCandidates / kThreads>(s, r, b, key, int(n));
+    const uint64_t last = n <= kThreads ? cut_of_candidates<1>(s, r, b, key, int(n))
+                                        : cut_of_candidates<kCandidates / kThreads>(s, r, b, key, int(n));
     // kept candidates join their chunks' sums, a wave a chunk
     __syncthreads();
     double* kept = reinterpret_cast<double*>(s.weight);
@@ -822,7 +959,6 @@ __global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p, Division
         __syncthreads();
     }
     // the chunk in which the running sum passes the target: every wave finds it
-    const double u = p.u[row];
     const double own = lane < int(gridDim.x) ? chunk_sum[lane] : 0.0;
     double upto = own;
 #pragma unroll
@@ -855,8 +991,7 @@ __global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p, Division
             if (lane == 0) group_sum[g] += sum;
         }
         __syncthreads();
-        const double mine = group_sum[threadIdx.x];
-        const int g = pick_group(s, mine, run, target);
+        const int g = pick_group(s, group_sum[threadIdx.x], run, target);
         run = s.d.wave[0];
         const int64_t f = c * dv.chunk + max(g, 0) * dv.group;
         if (g >= 0) pick = walk_group(s, r, x, f, min(p.N, f + dv.group), last, run, target);
