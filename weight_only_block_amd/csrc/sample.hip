@@ -706,6 +706,83 @@ __device__ uint64_t cut_of_candidates(Shared& s, const Row& r, const Bins& b, un
     return s.bin2 ? key[s.bin2 - 1] : ~0ull;
 }
 
+// Where one range of bins holds the cut, by rank or by weight: a second
+// histogram, of the range's candidates over 1024 places of the order between
+// its ends, then those of the place that holds the cut against each other.
+// False where more than 64 lie there.
+__device__ bool cut_by_places(Shared& s, const Row& r, const Bins& b, const unsigned long long* key, int n, uint64_t* cut)
+{
+    const bool by_k = r.top_p >= 1.0;
+    if (b.by_k && !by_k) return false;
+    constexpr int kPlaces = 1024;
+    static_assert(kPlaces == kThreads, "a thread scans a place");
+    uint32_t lo = ~0u, hi = 0;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint32_t o = uint32_t(key[i] >> 32);
+        lo = min(lo, o), hi = max(hi, o);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) s.in_bin = ~0u, s.above_count = 0, s.flag = 0, s.bin = 0, s.cut = ~0ull;
+    s.weight[threadIdx.x] = 0, s.count[threadIdx.x] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int off = 32; off; off >>= 1) {
+        lo = min(lo, uint32_t(__shfl_xor(int(lo), off, 64)));
+        hi = max(hi, uint32_t(__shfl_xor(int(hi), off, 64)));
+    }
+    if ((threadIdx.x & 63) == 0) atomicMin(&s.in_bin, lo), atomicMax(&s.above_count, hi);
+    __syncthreads();
+    lo = s.in_bin, hi = s.above_count;
+    const float scale = float(kPlaces) / (float(hi - lo) + 1.0f);
+    const auto place = [&](unsigned long long k) { return min(kPlaces - 1, int(float(hi - uint32_t(k >> 32)) * scale)); };
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const int at = place(key[i]);
+        atomicAdd(&s.count[at], 1u);
+        atomicAdd(&s.weight[at], r.fixed(r.weight(r.exponent(value_of(uint32_t(key[i] >> 32))))));
+    }
+    __syncthreads();
+    const unsigned int c = s.count[threadIdx.x];
+    const unsigned long long w = s.weight[threadIdx.x];
+    unsigned int call;
+    unsigned long long wall;
+    const uint64_t cb = b.first_count + scan(s.n, c, &call) - c;
+    const uint64_t wb = b.first_weight + scan(s.u, w, &wall) - w;
+    const double limit = r.top_p * double(b.total_weight);
+    // the last place that begins inside the cut
+    const bool inside = c && (by_k ? cb < uint64_t(r.k) : cb == 0 || double(wb) < limit);
+    wave_max(&s.bin, inside ? int(threadIdx.x) + 1 : 0);
+    __syncthreads();
+    const int at = s.bin - 1;
+    if (int(threadIdx.x) == at) s.sum_k = cb, s.above_weight = wb;
+    __syncthreads();
+    const uint64_t before_count = s.sum_k, before_weight = s.above_weight;
+    unsigned long long* chosen = s.weight;      // that place's candidates
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreads)
+        if (place(key[i]) == at) {
+            const int j = atomicAdd(&s.flag, 1);
+            if (j < 64) chosen[j] = key[i];
+        }
+    __syncthreads();
+    const int m = s.flag;
+    if (m > 64) return false;
+    if (threadIdx.x < 64) {
+        const int lane = threadIdx.x;
+        const unsigned long long mine = lane < m ? chosen[lane] : 0;
+        const unsigned long long mw = lane < m ? r.fixed(r.weight(r.exponent(value_of(uint32_t(mine >> 32))))) : 0;
+        uint64_t rank = before_count, weight = before_weight;
+        for (int j = 0; j < m; ++j) {
+            const unsigned long long o = __shfl(mine, j, 64), ow = __shfl(mw, j, 64);
+            if (o > mine) ++rank, weight += ow;
+        }
+        const bool keep = lane < m && (by_k ? rank < uint64_t(r.k) : rank == 0 || double(weight) < limit);
+        if (keep) atomicMin(&s.cut, mine);
+    }
+    __syncthreads();
+    *cut = s.cut;
+    return true;
+}
+
 __device__ __forceinline__ unsigned long long lane_value(unsigned long long v, int lane)
 {
     const uint32_t lo = uint32_t(__builtin_amdgcn_readlane(int(v), lane)), hi = uint32_t(__builtin_amdgcn_readlane(int(v >> 32), lane));
@@ -935,29 +1012,25 @@ __global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p, Division
         chunk_sum[0] = all;
     }
     __syncthreads();
-    const uint64_t last = n <= kThreads ? cut_of_candidates<1>(s, r, b, key, int(n))
-                                        : cut_of_candidates<kCandidates / kThreads>(s, r, b, key, int(n));
-    // kept candidates join their chunks' sums, a wave a chunk
+    uint64_t last;
+    if (!cut_by_places(s, r, b, key, int(n), &last))
+        last = n <= kThreads ? cut_of_candidates<1>(s, r, b, key, int(n))
+                             : cut_of_candidates<kCandidates / kThreads>(s, r, b, key, int(n));
+    // Kept candidates join their chunks' sums, in fixed point, where the
+    // smallest kept weight still counts and the order does not.
+    unsigned long long* add = s.weight;
+    const auto kept = [&](int i) -> unsigned long long {
+        const double w = key[i] >= last ? r.drawn(value_of(uint32_t(key[i] >> 32))) : 0.0;
+        return w > 0.0 ? max(1ull, r.fixed(w)) : 0;
+    };
     __syncthreads();
-    double* kept = reinterpret_cast<double*>(s.weight);
-    int* chunk = reinterpret_cast<int*>(s.count);
-    for (int base = 0; base < int(n); base += kBins) {
-        const int m = min(kBins, int(n) - base);
-        for (int i = threadIdx.x; i < m; i += kThreads) {
-            const unsigned long long k = key[base + i];
-            kept[i] = k >= last ? r.drawn(value_of(uint32_t(k >> 32))) : 0.0;
-            chunk[i] = int(int64_t(~uint32_t(k)) / dv.chunk);
-        }
-        __syncthreads();
-        for (int c = wave; c < int(gridDim.x); c += kWaves) {
-            double sum = 0.0;
-            for (int i = lane; i < m; i += 64) sum += chunk[i] == c ? kept[i] : 0.0;
-#pragma unroll
-            for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
-            if (lane == 0) chunk_sum[c] += sum;
-        }
-        __syncthreads();
-    }
+    if (threadIdx.x < kMaxChunks) add[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < int(n); i += kThreads)
+        if (const unsigned long long w = kept(i)) atomicAdd(&add[int64_t(~uint32_t(key[i])) / dv.chunk], w);
+    __syncthreads();
+    if (threadIdx.x < gridDim.x) chunk_sum[threadIdx.x] += double(add[threadIdx.x]) / r.unit;
+    __syncthreads();
     // the chunk in which the running sum passes the target: every wave finds it
     const double own = lane < int(gridDim.x) ? chunk_sum[lane] : 0.0;
     double upto = own;
@@ -972,26 +1045,20 @@ __global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p, Division
     if (u < 1.0 && past) {
         const int c = __ffsll((unsigned long long)past) - 1;
         double run = __shfl(upto - own, c, 64);
-        // its groups: what the chunk's work-group summed, and the kept
-        // candidates, which lie in the list in the row's order
+        // its groups: what the chunk's work-group summed, and the kept candidates
+        add[threadIdx.x] = 0;
         __syncthreads();
-        group_sum[threadIdx.x] = ONE ? own_group : int(threadIdx.x) < dv.groups
-            ? __longlong_as_double((long long)get(groups + (c - int(blockIdx.x)) * int64_t(dv.groups) + threadIdx.x)) : 0.0;
-        __syncthreads();
-        for (int g = wave; g < dv.groups && n; g += kWaves) {
-            const int64_t f = c * dv.chunk + g * dv.group;
-            double sum = 0.0;
-            for (int i = lane; i < int(n); i += 64) {
-                const unsigned long long k = key[i];
-                const int64_t at = int64_t(~uint32_t(k));
-                if (k >= last && at >= f && at < f + dv.group) sum += r.drawn(value_of(uint32_t(k >> 32)));
-            }
-#pragma unroll
-            for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
-            if (lane == 0) group_sum[g] += sum;
+        const int64_t begin = c * dv.chunk;
+        for (int i = threadIdx.x; i < int(n); i += kThreads) {
+            const int64_t at = int64_t(~uint32_t(key[i])) - begin;
+            if (at < 0 || at >= dv.chunk) continue;
+            if (const unsigned long long w = kept(i)) atomicAdd(&add[at / dv.group], w);
         }
         __syncthreads();
-        const int g = pick_group(s, group_sum[threadIdx.x], run, target);
+        double sum = ONE ? own_group : int(threadIdx.x) < dv.groups
+            ? __longlong_as_double((long long)get(groups + (c - int(blockIdx.x)) * int64_t(dv.groups) + threadIdx.x)) : 0.0;
+        sum += double(add[threadIdx.x]) / r.unit;
+        const int g = pick_group(s, sum, run, target);
         run = s.d.wave[0];
         const int64_t f = c * dv.chunk + max(g, 0) * dv.group;
         if (g >= 0) pick = walk_group(s, r, x, f, min(p.N, f + dv.group), last, run, target);
