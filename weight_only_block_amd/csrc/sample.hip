@@ -19,7 +19,7 @@
 //      chunk that the uniform number falls into and the token in it.
 // Bound by reading the logits (64 rows of 151936: 39 MB) and, for few rows, by
 // the launches' latency.  Rows of up to 8192 logits, and rows of any length
-// where there are 512 and more, are a work-group's each, with all steps in one
+// where there are more than 128, are a work-group's each, with all steps in one
 // launch.  A row whose cut falls into bins of more than 4096 tokens (many
 // nearly equal logits) gets its key by a radix selection over the row.
 #include <hip/hip_runtime.h>
@@ -38,7 +38,9 @@ constexpr int kBins = 2048;
 constexpr int kCandidates = 4096;
 constexpr int kMaxChunks = 64;
 constexpr int64_t kSmallRow = 8192;        // one work-group at once
-constexpr int64_t kResident = 512;         // work-groups the chip holds at once
+// Work-groups of the last launch that the chip holds at once (112 registers a
+// thread leave room for one a compute unit; 64 of them spill and cost more).
+constexpr int64_t kResident = 256;
 
 // How a row is divided: chunks of a work-group each, groups of 256 q tokens,
 // at most 1024 a chunk, whose kept weight is remembered so that only one of
@@ -53,7 +55,7 @@ __host__ __device__ inline Division division(int64_t m, int64_t N)
     Division d;
     // about as many chunks as the chip holds work-groups, of at least 4096 logits
     int64_t chunks = (N + 4095) / 4096;
-    const int64_t fit = (kResident + m - 1) / m;
+    const int64_t fit = m < kResident ? kResident / m : 1;
     if (chunks > fit) chunks = fit;
     if (chunks > kMaxChunks) chunks = kMaxChunks;
     if (N <= kSmallRow) chunks = 1;
