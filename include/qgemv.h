@@ -470,11 +470,11 @@ qg_status qg_rope_append(const qg_kv_cache *cache, const qg_rope *rope, const vo
  * Scores, softmax statistics and sums are fp32; probabilities enter the
  * second product as bf16.  The split of a sequence over work-groups and the
  * order of every sum depend on the arguments alone: a result is the same bits
- * from run to run.  Starts that do not ascend write nothing or only some rows.
+ * from run to run.  Where starts do not ascend, which rows are written, and
+ * by which sequence, is not defined; nothing outside them is.
  * QG_ERR_INVALID_ARG also for q_heads no multiple of kv_heads and a scale that
  * is not finite; QG_ERR_UNSUPPORTED for tokens * q_heads above 2^31 - 1, max_kv
- * above 2^30, seqs above 65535, q_heads above 32767, seqs * kv_heads above
- * 2^30. */
+ * above 2^30, seqs above 65535, q_heads above 32767. */
 size_t    qg_paged_attention_workspace_size(const qg_kv_cache *cache, int64_t tokens, int32_t q_heads, int32_t seqs,
                                             int64_t max_q, int64_t max_kv);
 qg_status qg_paged_attention(const qg_kv_cache *cache, const uint16_t *q_bf16, int64_t q_token_stride,
@@ -504,9 +504,8 @@ qg_status qg_paged_attention(const qg_kv_cache *cache, const uint16_t *q_bf16, i
  *   temperature, top_p, min_p  device fp32[m], top_k device int32[m]; NULL for
  *               1, 1, 0 and none
  *   workspace   device, >= qg_sample_workspace_size(m, N) bytes, 16-byte
- *               aligned, all zero before the first call; a completed call
- *               leaves it ready for the next of any m and N that need no more.
- *               Calls that share one must not overlap in time.
+ *               aligned, of any contents.  Calls that share one must not
+ *               overlap in time.
  * Weights and sums are 64-bit; results do not depend on timing.
  * 1 <= N < 2^31, m <= 65535; m = 0 is a no-op. */
 size_t    qg_sample_workspace_size(int64_t m, int64_t N);

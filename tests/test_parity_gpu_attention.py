@@ -248,6 +248,22 @@ def test_same_bits_again_whatever_ran_before_in_the_workspace():
     small.check(small.run(max_q=9, max_kv=5000))
 
 
+def test_calls_of_many_shapes_share_a_workspace():
+    # what one shape leaves behind its counts must not be another's counts
+    problems = [Problem(10 + i, [q] * n, [kv] * n, hq, 2, dim, 16, kind) for i, (q, n, kv, hq, dim, kind) in enumerate([
+        (1, 2, 3000, 4, 128, "bf16"), (40, 3, 700, 4, 64, "e4m3"), (1, 70, 90, 2, 64, "bf16"), (3, 1, 4000, 8, 256, "e4m3"),
+        (200, 1, 900, 2, 128, "bf16"), (1, 1, 9000, 4, 80, "bf16")])]
+    want = [p.run() for p in problems]
+    size = max(Q.paged_attention_workspace_size(p.cache, p.q_start[-1], p.hq, len(p.q_lens), p.max_q, p.max_kv)
+               for p in problems)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    order = torch.Generator().manual_seed(0)
+    for _ in range(5):
+        for i in torch.randperm(len(problems), generator=order).tolist():
+            got = problems[i].run(workspace=ws)
+            assert torch.equal(got[0], want[i][0]) and torch.equal(got[1], want[i][1]), i
+
+
 def test_replays_in_a_graph():
     p = Problem(6, [1, 1, 1], [500, 33, 900], 8, 2, 128, 16, "bf16")
     tokens = 3

@@ -172,8 +172,7 @@ static qg_status check_attention_shape(const qg_kv_cache* cache, int64_t tokens,
     if (tokens < 0 || tokens > kMaxCount || seqs < 0 || max_q < 0 || max_q > kMaxCount || max_kv < 0 ||
         max_kv > kMaxCount || q_heads < 1 || q_heads % view->kv_heads != 0)
         return QG_ERR_INVALID_ARG;
-    if (seqs > 65535 || q_heads > 32767 || int64_t(seqs) * view->kv_heads > (int64_t(1) << 30) ||
-        max_kv > kMaxCachedTokens || tokens * q_heads > kMaxCount)
+    if (seqs > 65535 || q_heads > 32767 || max_kv > kMaxCachedTokens || tokens * q_heads > kMaxCount)
         return QG_ERR_UNSUPPORTED;
     return QG_OK;
 }

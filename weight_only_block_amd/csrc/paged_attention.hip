@@ -47,6 +47,9 @@ constexpr float kRaise = 8.0f;             // log2 by which a score may pass the
 constexpr int kListPages = 1024;           // page ids of a run's segment, in LDS
 constexpr int kListSeqs = 128;             // sequences whose lengths are kept in LDS
 constexpr int kComputeUnits = 256;
+// Counts of arrived parts come first in the workspace, in every shape as many
+// bytes: calls of other shapes leave them alone.
+constexpr size_t kCounterBytes = 4096;
 constexpr int32_t kMaxWindow = 1 << 30;    // no shorter than the longest sequence
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -152,7 +155,6 @@ struct Args {
     int32_t tokens, max_q, cap, window, seqs; // cap: keys a sequence may have; window 0: none
     int32_t group;
     uint32_t by_group;                        // ceil(2^31 / group)
-    int32_t counters;
     float scale;
 };
 
@@ -564,43 +566,37 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
                 t = 0;
                 s = get_seq(p, seqs, ++b);
             }
-            if (f(b, t, k, make_unit<S>(p, s, t).steps + S::EXTRA)) break;
+            if (f(b, t, make_unit<S>(p, s, t).steps + S::EXTRA)) break;
             ++t;
         }
     };
     int64_t mine = 0;
     int longest = 0;
-    walk([&](int, int, int, int cost) {
+    walk([&](int, int, int cost) {
         mine += cost;
         longest = max(longest, cost);
         return false;
     });
     int64_t upto = mine;
-    int upto_units = mine_units;
     for (int off = 1; off < 64; off <<= 1) {
         const int64_t a = __shfl_up((long long)upto, off, 64);
-        const int u = __shfl_up(upto_units, off, 64);
-        if (lane >= off) upto += a, upto_units += u;
+        if (lane >= off) upto += a;
         longest = max(longest, __shfl_xor(longest, off, 64));
     }
-    int64_t* sums = reinterpret_cast<int64_t*>(lds);              // [W] each: steps, units, longest unit
-    if (lane == 63) sums[wave] = upto, sums[S::W + wave] = upto_units, sums[2 * S::W + wave] = longest;
+    int64_t* sums = reinterpret_cast<int64_t*>(lds);              // [W] each: steps, longest unit
+    if (lane == 63) sums[wave] = upto, sums[S::W + wave] = longest;
     __syncthreads();
     int64_t head_steps = 0, before = 0;
-    int head_units = 0, before_units = 0;
 #pragma unroll
     for (int w = 0; w < S::W; ++w) {
-        if (w == wave) before = head_steps, before_units = head_units;
+        if (w == wave) before = head_steps;
         head_steps += sums[w];
-        head_units += int(sums[S::W + w]);
-        longest = max(longest, int(sums[2 * S::W + w]));
+        longest = max(longest, int(sums[S::W + w]));
     }
     upto += before;
-    upto_units += before_units;
     head_steps = uniform(head_steps);
     const int64_t total = head_steps * p.kv_heads;
-    // starts that are not ascending claim more rows than there are
-    if (total == 0 || int64_t(head_units) * p.kv_heads > p.counters) return;
+    if (total == 0) return;
     // A unit of n steps in runs of x takes about x + JOINED n / x steps: no
     // shorter runs than where that is least, and no more runs than work-groups.
     const float least = fmaxf(float(S::LEAST), __builtin_amdgcn_sqrtf(float(longest) * S::JOINED));
@@ -625,9 +621,9 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
         const int64_t r = at - kvh * head_steps;
         if (r >= upto - mine && r < upto) {
             int64_t left = r - (upto - mine);
-            walk([&](int b, int t, int k, int cost) {
+            walk([&](int b, int t, int cost) {
                 if (left < cost) {
-                    plan[0] = b, plan[1] = t, plan[2] = left, plan[3] = upto_units - mine_units + k;
+                    plan[0] = b, plan[1] = t, plan[2] = left;
                     return true;
                 }
                 left -= cost;
@@ -637,7 +633,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
     }
     __syncthreads();
     int b = __builtin_amdgcn_readfirstlane(int(plan[0])), tile = __builtin_amdgcn_readfirstlane(int(plan[1]));
-    int off = __builtin_amdgcn_readfirstlane(int(plan[2])), unit = __builtin_amdgcn_readfirstlane(int(plan[3]));
+    int off = __builtin_amdgcn_readfirstlane(int(plan[2]));
     Seq s = get_seq(p, seqs, b);
 
     // dimensions past the head's end stay zero in every tile
@@ -653,10 +649,9 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
         off = 0;
         if (at >= end) return;
         ++tile;
-        ++unit;
         while (tile >= seq_tiles<S>(p, s)) {
             tile = 0;
-            if (++b == p.seqs) b = 0, unit = 0, ++kvh;
+            if (++b == p.seqs) b = 0, ++kvh;
             s = get_seq(p, seqs, b);
         }
     };
@@ -802,7 +797,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
         const bool whole = count == u.steps;
         const int tid = opaque(threadIdx.x), lane2 = tid & 63, col2 = lane2 & 31, h2 = lane2 >> 5;
         const float vs = S::E4M3 ? p.v_scale[kvh] : 1.0f;
-        float* slots = reinterpret_cast<float*>(p.workspace + (size_t(p.counters) * 4 + 255) / 256 * 256);
+        float* slots = reinterpret_cast<float*>(p.workspace + kCounterBytes);
         float* slot = slots + uint64_t(run * 2 + (off > 0 ? 0 : 1)) * S::SLOT;
         const auto put_out = [&](int row, int d, float a0, float a1, float a2, float a3, float inv) {
             const uint32_t r = uint32_t(u.lane0 + row), step = by_group(p, r);
@@ -904,8 +899,12 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
             // finds every part there.
             wait_loads<0>();
             __syncthreads();
+            // a run begins at most one unit that it does not end: the run in
+            // which a unit's first step lies numbers its count
+            const int64_t begin = at - off;
+            const int wf = run_of(begin + S::EXTRA);
             if (threadIdx.x == 0) {
-                uint32_t* cnt = reinterpret_cast<uint32_t*>(p.workspace) + int64_t(kvh) * head_units + unit;
+                uint32_t* cnt = reinterpret_cast<uint32_t*>(p.workspace) + wf;
                 const uint32_t old = __hip_atomic_fetch_add(cnt, uint32_t(count), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
                 const bool last = old + uint32_t(count) == uint32_t(u.steps);
                 if (last) __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -914,8 +913,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
             __syncthreads();
             if (plan[4]) {
                 // The unit's parts in run order; Split: sixteen parts' loads at a time.
-                const int64_t begin = at - off;
-                const int wf = run_of(begin + S::EXTRA), parts = run_of(begin + S::EXTRA + u.steps - 1) - wf + 1;
+                const int parts = run_of(begin + S::EXTRA + u.steps - 1) - wf + 1;
                 // only the first can have begun in its run, all others continue one
                 const int slot0 = wf * 2 + (run_start(wf) > begin ? 0 : 1);
                 if constexpr (S::SHARED) if (busy) {
@@ -1007,23 +1005,16 @@ int64_t workers(int64_t tokens, int group, int kv_heads, int seqs, int64_t max_k
 }
 
 template <class S>
-int64_t unit_bound(int64_t tokens, int group, int kv_heads, int seqs)
-{
-    return (tokens * group / S::M + seqs) * kv_heads;
-}
-
-template <class S>
 size_t bytes(int64_t tokens, int group, int kv_heads, int seqs, int64_t max_kv)
 {
-    const size_t head = (size_t(unit_bound<S>(tokens, group, kv_heads, seqs)) * 4 + 255) / 256 * 256;
-    return head + size_t(workers<S>(tokens, group, kv_heads, seqs, max_kv)) * 2 * S::SLOT * 4;
+    static_assert(kComputeUnits * S::PER_CU * 4 <= kCounterBytes, "a count a run");
+    return kCounterBytes + size_t(workers<S>(tokens, group, kv_heads, seqs, max_kv)) * 2 * S::SLOT * 4;
 }
 
 template <class S>
 hipError_t run(const AttnParams& a, Args p, hipStream_t s)
 {
     const int64_t grid = workers<S>(a.tokens, a.group, a.cache.kv_heads, a.seqs, a.max_kv);
-    p.counters = int32_t(unit_bound<S>(a.tokens, a.group, a.cache.kv_heads, a.seqs));
     static const hipError_t attr = [] {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(attention_kernel<S>),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS);

@@ -911,8 +911,8 @@ def sample_f32(logits, u, idx_out, workspace, temperature=None, top_k=None, top_
 
     temperature, top_p, min_p: device float32 [m] or None (1, 1, 0); top_k:
     device int32 [m] or None; a temperature of 0 is the greedy choice.
-    workspace: device tensor of sample_workspace_size(m, N) bytes, zero before
-    the first call."""
+    workspace: device tensor of sample_workspace_size(m, N) bytes, of any
+    contents."""
     where = "qg_sample_f32"
     dt = _DT or _dtypes()
     if logits.dim() != 2:
