@@ -15,10 +15,13 @@
 //   3. from the histogram, the bins that the cuts fall into: tokens above are
 //      kept for sure and summed, tokens in those bins become candidates; the
 //      row's last work-group ranks the candidates against each other, which
-//      gives the key, adds the kept ones to their chunks' sums, finds the
-//      chunk that the uniform number falls into and the token in it.
-// Bound by reading the logits (64 rows of 151936: 39 MB) and, for few rows, by
-// the launches' latency.  Rows of up to 8192 logits, and rows of any length
+//      gives the key, adds the kept ones to the sums of their groups (256
+//      tokens, more in very long rows), finds the group that the uniform number
+//      falls into and the token in it.
+// Bound by fp64 weights (64 rows of 151936, 39 MB: 9 us for the largest logits,
+// 18 us for the histogram with its weights, 33 us for the draw) and, for few
+// rows, by latency (one row: 4 + 7 + 14 us, most of the last a chain of reads
+// and sums by the row's last work-group).  Rows of up to 8192 logits, and rows of any length
 // where there are more than 128, are a work-group's each, with all steps in one
 // launch.  A row whose cut falls into bins of more than 4096 tokens (many
 // nearly equal logits) gets its key by a radix selection over the row.
@@ -37,18 +40,25 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kBins = 2048;
 constexpr int kCandidates = 4096;
 constexpr int kMaxChunks = 64;
+constexpr int kAhead = 2;                  // rounds of loads in the last launch
+constexpr int kGroups = kThreads;          // of a row: a thread sums one up
 constexpr int64_t kSmallRow = 8192;        // one work-group at once
 // Work-groups of the last launch that the chip holds at once (112 registers a
 // thread leave room for one a compute unit; 64 of them spill and cost more).
 constexpr int64_t kResident = 256;
 
-// How a row is divided: chunks of a work-group each, groups of 256 q tokens,
-// at most 1024 a chunk, whose kept weight is remembered so that only one of
-// them is read again for the draw.
+// How a row is divided: at most 1024 groups of 256 q tokens, whose kept weight
+// is remembered so that only one of them is read again for the draw, and
+// chunks of whole groups, a work-group each.
 struct Division {
-    int64_t chunk, group;
-    int chunks, groups;       // groups of a chunk
+    int64_t chunk, group;     // tokens of a chunk, of a group
+    int chunks, groups;       // chunks of a row, groups of a chunk
 };
+
+__host__ __device__ inline int64_t group_size(int64_t N)
+{
+    return 256 * ((N + 256 * kGroups - 1) / (256 * kGroups));
+}
 
 __host__ __device__ inline Division division(int64_t m, int64_t N)
 {
@@ -59,20 +69,20 @@ __host__ __device__ inline Division division(int64_t m, int64_t N)
     if (chunks > fit) chunks = fit;
     if (chunks > kMaxChunks) chunks = kMaxChunks;
     if (N <= kSmallRow) chunks = 1;
-    const int64_t size = (N + chunks - 1) / chunks;
-    d.group = 256 * ((size + 256 * kThreads - 1) / (256 * kThreads));
-    d.groups = int((size + d.group - 1) / d.group);
+    d.group = group_size(N);
+    const int64_t groups = (N + d.group - 1) / d.group;
+    d.groups = int((groups + chunks - 1) / chunks);
     d.chunk = d.group * d.groups;
-    d.chunks = int((N + d.chunk - 1) / d.chunk);
+    d.chunks = int((groups + d.groups - 1) / d.groups);
     return d;
 }
 
-// Row r's part of the workspace; the groups' sums of all rows follow the last.
+// Row r's part of the workspace.
 struct RowSpace {
     unsigned long long weight[kBins];
     unsigned int count[kBins];
     unsigned long long key[kMaxChunks];
-    unsigned long long sum[kMaxChunks];    // fp64 bits
+    unsigned long long sum[kGroups];       // fp64 bits
     unsigned long long candidate[kCandidates];
     unsigned int candidates, arrived, pad[14];
 };
@@ -93,38 +103,42 @@ __device__ __forceinline__ float value_of(uint32_t order)
 
 // A row's settings; weights are 2^y with y = (x - top) log2(e) / temperature.
 struct Row {
-    float top;
+    float top, low;
     double rate;          // log2(e) / temperature
     int64_t N, k;
     double top_p, floor;
     double unit;          // fixed-point steps of a weight of 1
-    const double* powers; // LDS: 2^(i / 128)
+    const double* powers; // LDS: 2^(i / 256)
     bool greedy;
     int32_t top_idx;
 
+    // Tokens below `low` have a weight far under the smallest fp64 one (or are
+    // -infinity): never drawn, and left out of the ranks behind every token
+    // that can be.
+    __device__ __forceinline__ bool live(float v) const { return v >= low; }
+
+    // (equal infinities differ by NaN, which counts as 0)
     __device__ __forceinline__ double exponent(float v) const
     {
-        return v == top ? 0.0 : (double(v) - double(top)) * rate;
+        return fmax(fmin((double(v) - double(top)) * rate, 0.0), -1100.0);
     }
-    // Far below the smallest fp64 weight (or -infinity): never drawn, and left
-    // out of the ranks behind every token that can be.
-    static __device__ __forceinline__ bool nothing(double y) { return !(y >= -1100.0); }
 
-    // 2^y for y <= 0 as 2^(n / 128) 2^f: the first factor from a table of 128
-    // and the exponent, the second by its Taylor series, |f ln 2| < 0.0028,
-    // whose sixth term is below 2^-60.
+    // 2^y for -1100 <= y <= 0 as 2^(n / 256) 2^f: the first factor from a table
+    // of 256 and the exponent, the second by its Taylor series in f ln 2, below
+    // 0.0014, whose fifth term is below 2^-54 (without a table the series takes
+    // 13 terms: 29 us in place of 25 for 64 rows of 151936 without a cut).
+    // Adding 1.5 * 2^52 leaves n in the sum's low bits.
     __device__ __forceinline__ double weight(double y) const
     {
-        if (nothing(y)) return 0.0;
-        const double n = __builtin_rint(y * 128.0);
-        const double z = __builtin_fma(n, -1.0 / 128.0, y) * 0.69314718055994530942;
-        double p = __builtin_fma(z, 1.0 / 120.0, 1.0 / 24.0);
-        p = __builtin_fma(p, z, 1.0 / 6.0);
-        p = __builtin_fma(p, z, 0.5);
-        p = __builtin_fma(p, z, 1.0);
-        p = __builtin_fma(p, z, 1.0);
-        const int i = int(n);
-        return ldexp(p * powers[i & 127], i >> 7);
+        constexpr double kLn2 = 0.69314718055994530942;
+        const double t = __builtin_fma(y, 256.0, 0x1.8p52);
+        const int i = int(uint32_t(__double_as_longlong(t)));
+        const double f = __builtin_fma(t - 0x1.8p52, -1.0 / 256.0, y);
+        double p = __builtin_fma(f, kLn2 * kLn2 * kLn2 * kLn2 / 24.0, kLn2 * kLn2 * kLn2 / 6.0);
+        p = __builtin_fma(p, f, kLn2 * kLn2 / 2.0);
+        p = __builtin_fma(p, f, kLn2);
+        p = __builtin_fma(p, f, 1.0);
+        return ldexp(p * powers[i & 255], i >> 8);
     }
     // Rounded to an integer by adding 2^52: what is below the point leaves the mantissa.
     __device__ __forceinline__ unsigned long long fixed(double w) const
@@ -140,14 +154,15 @@ struct Row {
     __device__ __forceinline__ bool cut() const { return k < N || top_p < 1.0; }
 };
 
-// 2^(i / 128) for i < 128: the Taylor series of exp(i ln 2 / 128), whose 18th
+// 2^(i / 256) for i < 256: the Taylor series of exp(i ln 2 / 256), whose 18th
 // term is below 2^-58.
 __device__ __forceinline__ void fill_powers(double* powers)
 {
-    if (threadIdx.x >= 128) return;
-    const double z = double(threadIdx.x) * (0.69314718055994530942 / 128.0);
+    if (threadIdx.x >= 256) return;
+    const double z = double(threadIdx.x) * (0.69314718055994530942 / 256.0);
     double p = 1.0;
-    for (int k = 17; k >= 1; --k) p = __builtin_fma(p, z / k, 1.0);
+#pragma unroll
+    for (int k = 17; k >= 1; --k) p = __builtin_fma(p, z * (1.0 / k), 1.0);
     powers[threadIdx.x] = p;
 }
 
@@ -161,6 +176,7 @@ __device__ __forceinline__ Row row_of(const SampleParams& p, int64_t row, uint64
     // greedy, or nothing to weigh: a NaN wins, and a row of -infinity gives its first
     r.greedy = !(t > 0.0f) || r.top != r.top || r.top == -INFINITY;
     r.rate = 1.44269504088896340736 / double(t);
+    r.low = r.top == INFINITY ? INFINITY : float(fmax(double(r.top) - 1100.0 / r.rate, double(-__FLT_MAX__)));
     r.N = p.N;
     r.k = p.top_k && p.top_k[row] > 0 ? min(int64_t(p.top_k[row]), p.N) : p.N;
     const float tp = p.top_p ? p.top_p[row] : 1.0f, mp = p.min_p ? p.min_p[row] : 0.0f;
@@ -172,13 +188,24 @@ __device__ __forceinline__ Row row_of(const SampleParams& p, int64_t row, uint64
 
 // Bins of d = top - x, finest near the top in proportion (d < 1: 32 an octave
 // down to 2^-12), then 32 a unit to 33, then 32 an octave.
-__device__ __forceinline__ int bin_of(float top, float v)
+__device__ __forceinline__ float below_top(float top, float v) { return fmaxf(top - v, 0.0f); }
+
+__device__ __forceinline__ int bin_of(float d)
 {
-    if (v == top) return 0;
-    const float d = top - v;
-    if (d < 1.0f) return d < 0x1p-12f ? 0 : int((__float_as_uint(d) - 0x39800000u) >> 18);
-    if (d < 33.0f) return 384 + int((d - 1.0f) * 32.0f);
-    return min(1408 + int((__float_as_uint(d) - 0x42040000u) >> 18), kBins - 1);
+    const uint32_t bits = __float_as_uint(d);
+    const int near = int((max(bits, 0x39800000u) - 0x39800000u) >> 18), mid = 384 + int((d - 1.0f) * 32.0f);
+    const int far = min(1408 + int((bits - 0x42040000u) >> 18), kBins - 1);
+    return d < 1.0f ? near : d < 33.0f ? mid : far;
+}
+
+// The smallest d of a bin; no d is below that of bin 0, every d (infinity too)
+// is below the NaN of bin kBins.
+__device__ __forceinline__ float edge_of(int bin)
+{
+    if (bin <= 0) return 0.0f;
+    if (bin <= 384) return __uint_as_float(0x39800000u + (uint32_t(bin) << 18));
+    if (bin <= 1408) return 1.0f + float(bin - 384) * (1.0f / 32.0f);
+    return bin < kBins ? __uint_as_float(0x42040000u + (uint32_t(bin - 1408) << 18)) : __uint_as_float(0x7fc00000u);
 }
 
 template <class T>
@@ -217,8 +244,8 @@ __device__ __forceinline__ void wave_max(int* at, int v)
 }
 
 struct Shared {
-    double powers[128];
-    unsigned long long weight[kBins];
+    double powers[256];
+    unsigned long long weight[kBins];      // the histogram; then, by halves, groups' sums and what is added to them
     unsigned int count[kBins];
     ScanSpace<double> d;
     ScanSpace<unsigned long long> u;
@@ -239,6 +266,32 @@ __device__ __forceinline__ uint64_t block_max(Shared& s, uint64_t best)
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) best = max_key(best, s.best[w]);
     return best;
+}
+
+// Inclusive sums of two values at once, as scan.
+__device__ __forceinline__ void scan_both(Shared& s, unsigned int* c, unsigned long long* w, unsigned int* call,
+                                          unsigned long long* wall)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const unsigned int co = __shfl_up(*c, off, 64);
+        const unsigned long long wo = __shfl_up(*w, off, 64);
+        if (lane >= off) *c += co, *w += wo;
+    }
+    if (lane == 63) s.n.wave[wave] = *c, s.u.wave[wave] = *w;
+    __syncthreads();
+    *call = 0, *wall = 0;
+    unsigned int cb = 0;
+    unsigned long long wb = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        if (i == wave) cb = *call, wb = *wall;
+        *call += s.n.wave[i];
+        *wall += s.u.wave[i];
+    }
+    *c += cb;
+    *w += wb;
 }
 
 // ------------------------------------------------ one work-group for a row
@@ -346,82 +399,94 @@ __device__ uint64_t cut_by_selection(Shared& s, const Row& r, const float* x)
     return s.cut;
 }
 
-// The group (one a thread, `mine` its kept weight) in which the running sum
-// from `run` on passes `target`, the last one with a kept token if rounding
-// left the target past the end, -1 without any; the sum before it in
-// s.d.wave[0].
-__device__ int pick_group(Shared& s, double mine, double run, double target)
+// The token of [from, to) where the running sum of kept weights passes
+// `target`, else the last kept one, r.N without any; by one wave, 256 tokens
+// at a time, four neighbours a lane.
+__device__ int64_t walk_wave(const Row& r, const float* x, int64_t from, int64_t to, uint64_t cut, double run, double target)
+{
+    const int lane = threadIdx.x & 63;
+    int64_t last = r.N;
+#pragma unroll 1
+    for (int64_t base = from; base < to; base += 256) {
+        const int64_t i = base + 4 * lane;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = i + e < to ? x[i + e] : -INFINITY;
+        double w[4], strip = 0.0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            w[e] = i + e < to && argmax_key(v[e], uint32_t(i + e)) >= cut ? r.drawn(v[e]) : 0.0;
+            strip += w[e];
+        }
+        double upto = strip;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const double o = __shfl_up(upto, off, 64);
+            if (lane >= off) upto += o;
+        }
+        const uint64_t some = __ballot(strip > 0.0), past = __ballot(strip > 0.0 && run + upto > target);
+        // the last of a lane's kept tokens, or the first whose sum passes
+        double sum = run + (upto - strip);
+        int at = 0;
+        bool found = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (found || !(w[e] > 0.0)) continue;
+            at = e;
+            sum += w[e];
+            found = sum > target;
+        }
+        const int src = past ? __ffsll((unsigned long long)past) - 1 : some ? 63 - __clzll((long long)some) : 0;
+        if (some) last = base + 4 * src + __shfl(at, src, 64);
+        if (past) break;
+        run += __shfl(upto, 63, 64);
+    }
+    return last;
+}
+
+// The token in which the running sum of kept weights passes u times their
+// sum, r.N without any: thread t holds the kept weight of group t, one wave
+// walks the group that the token is in.
+__device__ int64_t draw_token(Shared& s, const Row& r, const float* x, uint64_t cut, double mine, int64_t size, double u)
 {
     if (threadIdx.x == 0) s.bin = kThreads, s.bin2 = 0;
     double all;
     const double upto = scan(s.d, mine, &all);
-    const uint64_t past = __ballot(mine > 0.0 && run + upto > target);
+    const double target = u * all;
+    const uint64_t past = __ballot(mine > 0.0 && upto > target);
     if (past && int(threadIdx.x & 63) == __ffsll((unsigned long long)past) - 1) atomicMin(&s.bin, int(threadIdx.x));
     wave_max(&s.bin2, mine > 0.0 ? int(threadIdx.x) + 1 : 0);
     __syncthreads();
+    // (rounding may leave the target past the end: then the last group with a kept token)
     const int g = s.bin < kThreads ? s.bin : s.bin2 - 1;
-    if (int(threadIdx.x) == g) s.d.wave[0] = run + (upto - mine);
+    if (g < 0 || !(u < 1.0)) return r.N;
+    if (int(threadIdx.x) == g) s.d.wave[0] = upto - mine;
     __syncthreads();
-    return g;
+    int64_t pick = r.N;
+    if (threadIdx.x < 64) pick = walk_wave(r, x, g * size, min(r.N, (g + 1) * size), cut, s.d.wave[0], target);
+    return pick;                               // (the first wave's)
 }
 
-// The token of [from, to) where the running sum of kept weights passes
-// `target`, else the last kept one, r.N without any; by one wave, 256 tokens
-// at a time.
-__device__ int64_t walk_wave(const Row& r, const float* x, int64_t from, int64_t to, uint64_t cut, double run, double target)
+// A wave's sum, in every lane.
+__device__ __forceinline__ double wave_sum(double w)
 {
-    const int lane = threadIdx.x & 63;
-    int64_t last = r.N, found = r.N;
-    for (int64_t base = from; base < to && found == r.N; base += 256) {
-        float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = base + 64 * e + lane < to ? x[base + 64 * e + lane] : -INFINITY;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int64_t i = base + 64 * e + lane;
-            const double w = i < to && argmax_key(v[e], uint32_t(i)) >= cut ? r.drawn(v[e]) : 0.0;
-            double upto = w;
-#pragma unroll
-            for (int off = 1; off < 64; off <<= 1) {
-                const double o = __shfl_up(upto, off, 64);
-                if (lane >= off) upto += o;
-            }
-            const uint64_t past = __ballot(w > 0.0 && run + upto > target), some = __ballot(w > 0.0);
-            if (past && found == r.N) found = base + 64 * e + __ffsll((unsigned long long)past) - 1;
-            if (some) last = base + 64 * e + 63 - __clzll((long long)some);
-            run += __shfl(upto, 63, 64);
-        }
-    }
-    return found < r.N ? found : last;
+    for (int off = 32; off; off >>= 1) w += __shfl_xor(w, off, 64);
+    return w;
 }
 
-// The same for a work-group, whose first wave walks.
-__device__ int64_t walk_group(Shared& s, const Row& r, const float* x, int64_t from, int64_t to, uint64_t cut, double run,
-                              double target)
+__device__ void draw_by_selection(Shared& s, const SampleParams& p, int64_t row, const Row& r)
 {
-    if (threadIdx.x < 64) {
-        const int64_t pick = walk_wave(r, x, from, to, cut, run, target);
-        if (threadIdx.x == 0) s.pick = (unsigned long long)pick;
-    }
-    __syncthreads();
-    return int64_t(s.pick);
-}
-
-// The token of a row in which the running sum of kept weights passes u times
-// their sum; r.N without any.  Groups of 256 q tokens are summed by a wave
-// each, then one wave walks the group that holds the token.
-__device__ int64_t draw_row(Shared& s, const Row& r, const float* x, uint64_t cut, double u)
-{
+    const float* x = p.x + row * p.ldx;
+    const uint64_t cut = r.cut() ? cut_by_selection(s, r, x) : 0;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    double* group_sum = reinterpret_cast<double*>(s.weight);      // kThreads of them
-    const int64_t size = 256 * ((r.N + 256 * kThreads - 1) / (256 * kThreads));
+    double* group_sum = reinterpret_cast<double*>(s.weight);
+    const int64_t size = group_size(r.N);
     const int groups = int((r.N + size - 1) / size);
     __syncthreads();
-    group_sum[threadIdx.x] = 0.0;
-    __syncthreads();
-    for (int g = wave; g < groups; g += kWaves) {
+    for (int g = wave; g < kGroups; g += kWaves) {
         double w = 0.0;
-        for (int64_t base = g * size; base < (g + 1) * size; base += 256) {
+        for (int64_t base = g * size; g < groups && base < (g + 1) * size; base += 256) {
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = base + 64 * e + lane < r.N ? x[base + 64 * e + lane] : -INFINITY;
@@ -429,44 +494,60 @@ __device__ int64_t draw_row(Shared& s, const Row& r, const float* x, uint64_t cu
             for (int e = 0; e < 4; ++e)
                 if (base + 64 * e + lane < r.N && argmax_key(v[e], uint32_t(base + 64 * e + lane)) >= cut) w += r.drawn(v[e]);
         }
-#pragma unroll
-        for (int off = 32; off; off >>= 1) w += __shfl_xor(w, off, 64);
+        w = wave_sum(w);
         if (lane == 0) group_sum[g] = w;
     }
     __syncthreads();
-    const double mine = group_sum[threadIdx.x];
-    double all;
-    scan(s.d, mine, &all);
-    const double target = u * all;
-    const int g = pick_group(s, mine, 0.0, target);
-    if (g < 0) return r.N;
-    return walk_group(s, r, x, g * size, min(r.N, (g + 1) * size), cut, s.d.wave[0], target);
-}
-
-__device__ void draw_by_selection(Shared& s, const SampleParams& p, int64_t row, const Row& r)
-{
-    const float* x = p.x + row * p.ldx;
-    const uint64_t cut = r.cut() ? cut_by_selection(s, r, x) : 0;
-    const double u = p.u[row];
-    int64_t pick = r.N;
-    if (u < 1.0) pick = draw_row(s, r, x, cut, u);
+    const int64_t pick = draw_token(s, r, x, cut, group_sum[threadIdx.x], size, p.u[row]);
     if (threadIdx.x == 0) p.idx[row] = pick < r.N ? int32_t(pick) : r.top_idx;
 }
 
 // ------------------------------------------------------------ three launches
 
+// Calls f(values, first token) for the tokens [from, to), eight a thread at a
+// time, the e-th of them kThreads * e past the first; the next eight are on
+// their way meanwhile.  Past the end f sees -infinity.
+template <class F>
+__device__ __forceinline__ void each_token(const float* x, int64_t from, int64_t to, F f)
+{
+    constexpr uint32_t kStep = 8 * kThreads;
+    const uint32_t n = uint32_t(to - from);        // below 2^31
+    x += from;
+    float next[8];
+    const auto load = [&](uint32_t base) {
+        const float* at = x + base;                // the same in every lane
+        if (base + kStep <= n) {
+#pragma unroll
+            for (uint32_t e = 0; e < 8; ++e) next[e] = at[e * kThreads + threadIdx.x];
+        } else {
+#pragma unroll
+            for (uint32_t e = 0; e < 8; ++e) next[e] = x[min(base + e * kThreads + threadIdx.x, n - 1)];
+        }
+    };
+    load(0);
+    for (uint32_t base = 0; base < n; base += kStep) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = next[e];
+        if (base + kStep < n) load(base + kStep);
+        if (base + kStep > n) {
+#pragma unroll
+            for (uint32_t e = 0; e < 8; ++e)
+                if (base + e * kThreads + threadIdx.x >= n) v[e] = -INFINITY;
+        }
+        f(v, from + base + threadIdx.x);
+    }
+}
+
 // The largest key of [from, to).
 __device__ __forceinline__ uint64_t top_of(Shared& s, const float* x, int64_t from, int64_t to)
 {
     uint64_t best = 0;
-    for (int64_t i = from + threadIdx.x; i < to; i += 8 * kThreads) {
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = i + e * kThreads < to ? x[i + e * kThreads] : -INFINITY;
+    each_token(x, from, to, [&](const float (&v)[8], int64_t i) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             if (i + e * kThreads < to) best = max_key(best, argmax_key(v[e], uint32_t(i + e * kThreads)));
-    }
+    });
     return block_max(s, best);
 }
 
@@ -476,19 +557,23 @@ __device__ __forceinline__ void add_to_bins(Shared& s, const Row& r, const float
     for (int i = threadIdx.x; i < kBins; i += kThreads) s.weight[i] = 0, s.count[i] = 0;
     __syncthreads();
     const bool weigh = r.top_p < 1.0, rank = r.k < r.N;
-    for (int64_t i = from + threadIdx.x; i < to; i += 8 * kThreads) {
-        float v[8];
+    // (eight weights side by side, as their operations wait on each other)
+    each_token(x, from, to, [&](const float (&v)[8], int64_t) {
+        int bin[8];
+        unsigned long long w[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = i + e * kThreads < to ? x[i + e * kThreads] : -INFINITY;
+        for (int e = 0; e < 8; ++e) bin[e] = bin_of(below_top(r.top, v[e]));
+        if (weigh) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = r.fixed(r.weight(r.exponent(v[e])));
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const double y = r.exponent(v[e]);
-            if (Row::nothing(y)) continue;
-            const int bin = bin_of(r.top, v[e]);
-            if (rank) atomicAdd(&s.count[bin], 1u);
-            if (weigh) atomicAdd(&s.weight[bin], r.fixed(r.weight(y)));
+            if (!r.live(v[e])) continue;
+            if (rank) atomicAdd(&s.count[bin[e]], 1u);
+            if (weigh) atomicAdd(&s.weight[bin[e]], w[e]);
         }
-    }
+    });
     __syncthreads();
 }
 
@@ -558,10 +643,10 @@ __device__ Bins find_bins(Shared& s, const Row& r, const unsigned int* count, co
     const int i0 = 2 * threadIdx.x;
     const unsigned int c0 = count[i0], c1 = count[i0 + 1];
     const unsigned long long w0 = weight[i0], w1 = weight[i0 + 1];
-    unsigned int call;
-    unsigned long long wall;
-    const unsigned int cb = scan(s.n, c0 + c1, &call) - (c0 + c1);
-    const unsigned long long wb = scan(s.u, w0 + w1, &wall) - (w0 + w1);
+    unsigned int call, cb = c0 + c1;
+    unsigned long long wall, wb = w0 + w1;
+    scan_both(s, &cb, &wb, &call, &wall);
+    cb -= c0 + c1, wb -= w0 + w1;
     b.total_weight = wall;
     b.by_k = r.k < r.N && uint64_t(r.k) < call;
     b.kbin = kBins;
@@ -675,7 +760,7 @@ __device__ uint64_t cut_of_candidates(Shared& s, const Row& r, const Bins& b, un
         in_k[e] = in_p[e] = false;
         if (at + e >= n) continue;
         const float v = value_of(uint32_t(key[at + e] >> 32));
-        const int bin = bin_of(r.top, v);
+        const int bin = bin_of(below_top(r.top, v));
         w[e] = r.fixed(r.weight(r.exponent(v)));
         in_k[e] = bin == b.kbin;
         in_p[e] = bin >= b.first && bin <= b.second;
@@ -785,107 +870,45 @@ __device__ bool cut_by_places(Shared& s, const Row& r, const Bins& b, const unsi
     return true;
 }
 
-__device__ __forceinline__ unsigned long long lane_value(unsigned long long v, int lane)
+// The cut's key where there are at most 64 candidates (the usual row): each
+// wave compares all of them with its share, the first wave then has their
+// ranks and the weights before them.
+__device__ uint64_t cut_of_few(Shared& s, const Row& r, const Bins& b, const unsigned long long* key, int n)
 {
-    const uint32_t lo = uint32_t(__builtin_amdgcn_readlane(int(v), lane)), hi = uint32_t(__builtin_amdgcn_readlane(int(v >> 32), lane));
-    return (unsigned long long)(hi) << 32 | lo;
-}
-
-// The value of the lane that sends to this one; `to` is a permutation of the lanes.
-__device__ __forceinline__ unsigned long long send(unsigned long long v, int to)
-{
-    const uint32_t lo = uint32_t(__builtin_amdgcn_ds_permute(4 * to, int(v)));
-    const uint32_t hi = uint32_t(__builtin_amdgcn_ds_permute(4 * to, int(v >> 32)));
-    return (unsigned long long)(hi) << 32 | lo;
-}
-
-// The end of a row with at most 64 candidates (the usual one), by one wave:
-// lane i holds candidate i (`key`, 0 past the n-th) and chunk i's sum (`own`).
-// `sums` gives the sum of a group of a chunk, group_sum is space for them.
-template <class F>
-__device__ int64_t finish_wave(const SampleParams& p, const Division& dv, const Row& r, const Bins& b, const float* x,
-                               unsigned long long key, int n, double own, double u, double* group_sum, F sums)
-{
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    unsigned long long* before = s.weight + kGroups;
+    unsigned long long* weight = before + 64;
+    unsigned int* rank = s.count;
     const bool is = lane < n;
-    const float v = value_of(uint32_t(key >> 32));
-    const int bin = is ? bin_of(r.top, v) : -1;
+    const unsigned long long mine = is ? key[lane] : 0;
+    const float v = value_of(uint32_t(mine >> 32));
     const unsigned long long w = is ? r.fixed(r.weight(r.exponent(v))) : 0;
-    // rank among the candidates and the weight before it
-    int rank = is ? 0 : lane;
-    unsigned long long before = 0;
-    for (int j = 0; j < n; ++j) {
-        const unsigned long long o = lane_value(key, j), ow = lane_value(w, j);
-        if (is && o > key) {
-            ++rank;
-            before += ow;
-        }
-    }
-    const bool in_k = is && bin == b.kbin, in_p = is && bin >= b.first && bin <= b.second;
-    const int in_range = __popcll(__ballot(in_p));
-    const uint64_t place = in_p ? b.first_count + rank : b.k_count + rank - in_range;
-    unsigned long long sum_k = in_k && place < uint64_t(r.k) ? w : 0;
+    if (wave == 0) before[lane] = 0, weight[lane] = w, rank[lane] = 0;
+    if (threadIdx.x == 0) s.cut = ~0ull;
+    __syncthreads();
+    unsigned int ahead = 0;
+    unsigned long long sum = 0;
+    for (int j = wave; j < n; j += kWaves)
+        if (key[j] > mine) ++ahead, sum += weight[j];
+    if (is && ahead) atomicAdd(&rank[lane], ahead), atomicAdd(&before[lane], sum);
+    __syncthreads();
+    if (wave == 0) {
+        const int bin = is ? bin_of(below_top(r.top, v)) : -1;
+        const bool in_k = is && bin == b.kbin, in_p = is && bin >= b.first && bin <= b.second;
+        const int in_range = __popcll(__ballot(in_p));      // the first ones in order
+        const uint64_t place = in_p ? b.first_count + rank[lane] : b.k_count + rank[lane] - in_range;
+        unsigned long long sum_k = in_k && place < uint64_t(r.k) ? w : 0;
 #pragma unroll
-    for (int off = 32; off; off >>= 1) sum_k += __shfl_xor(sum_k, off, 64);
-    sum_k = b.by_k ? b.k_weight + sum_k : b.total_weight;
-    const double limit = r.top_p * double(sum_k);
-    const bool keep = in_p && place < uint64_t(r.k) &&
-                      (r.top_p >= 1.0 || place == 0 || double(b.first_weight + before) < limit);
-    const int kept = __popcll(__ballot(keep));       // the first ones in order
-    // in order from here on
-    key = send(key, rank);
-    const uint64_t cut = n == 0 ? 0 : kept ? lane_value(key, kept - 1) : ~0ull;
-    const double mine = lane < kept ? r.drawn(value_of(uint32_t(key >> 32))) : 0.0;
-    const uint32_t index = ~uint32_t(key);
-    const int chunk = int(int64_t(index) / dv.chunk);
-    for (int j = 0; j < kept; ++j) {
-        const double add = __longlong_as_double((long long)lane_value((unsigned long long)__double_as_longlong(mine), j));
-        if (lane == __builtin_amdgcn_readlane(chunk, j)) own += add;
+        for (int off = 32; off; off >>= 1) sum_k += __shfl_xor(sum_k, off, 64);
+        sum_k = b.by_k ? b.k_weight + sum_k : b.total_weight;
+        const double limit = r.top_p * double(sum_k);
+        const bool keep = in_p && place < uint64_t(r.k) &&
+                          (r.top_p >= 1.0 || place == 0 || double(b.first_weight + before[lane]) < limit);
+        const int kept = __popcll(__ballot(keep));
+        if (keep && int(rank[lane]) == kept - 1) s.cut = mine;
     }
-    double upto = own;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const double o = __shfl_up(upto, off, 64);
-        if (lane >= off) upto += o;
-    }
-    const double target = u * __shfl(upto, 63, 64);
-    const uint64_t past = __ballot(own > 0.0 && upto > target);
-    if (!(u < 1.0) || !past) return p.N;
-    const int c = __ffsll((unsigned long long)past) - 1;
-    double run = __shfl(upto - own, c, 64);
-    // the chunk's groups, its kept candidates among them; a lane takes q of them
-    for (int g = lane; g < dv.groups; g += 64) group_sum[g] = sums(c, g);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    for (int j = 0; j < kept; ++j) {
-        if (__builtin_amdgcn_readlane(chunk, j) != c) continue;
-        const uint32_t i = uint32_t(__builtin_amdgcn_readlane(int(index), j));
-        if (lane == j) group_sum[int((int64_t(i) - c * dv.chunk) / dv.group)] += mine;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    }
-    const int q = (dv.groups + 63) / 64;
-    double strip = 0.0;
-    for (int i = 0; i < q; ++i)
-        if (lane * q + i < dv.groups) strip += group_sum[lane * q + i];
-    double sum = strip;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const double o = __shfl_up(sum, off, 64);
-        if (lane >= off) sum += o;
-    }
-    const uint64_t over = __ballot(strip > 0.0 && run + sum > target), some = __ballot(strip > 0.0);
-    if (!some) return p.N;
-    // (rounding may leave the target past the end)
-    const int at = over ? __ffsll((unsigned long long)over) - 1 : 63 - __clzll((long long)some);
-    run += __shfl(sum - strip, at, 64);
-    int g = -1;
-    for (int i = at * q; i < min((at + 1) * q, dv.groups); ++i) {
-        if (!(group_sum[i] > 0.0)) continue;
-        if (g >= 0) run += group_sum[g];
-        g = i;
-        if (run + group_sum[i] > target) break;
-    }
-    const int64_t f = c * dv.chunk + g * dv.group;
-    return walk_wave(r, x, f, min(p.N, f + dv.group), cut, run, target);
+    __syncthreads();
+    return s.cut;
 }
 
 // ONE: a work-group has the whole row and does the first two steps as well.
@@ -895,11 +918,37 @@ __global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p, Division
     fetch_arguments<sizeof(SampleParams) + sizeof(Division)>();
     __shared__ Shared s;
     __shared__ unsigned long long key[kCandidates];
-    __shared__ double chunk_sum[kMaxChunks];
     const int64_t row = blockIdx.y;
     RowSpace& ws = static_cast<RowSpace*>(p.workspace)[ONE ? 0 : row];
     const float* x = p.x + row * p.ldx;
     const int64_t from = blockIdx.x * dv.chunk, to = min(p.N, from + dv.chunk);
+    // A wave takes every 16th group of the chunk, 256 tokens a round, four a
+    // lane; kAhead rounds are on their way while as many are used.
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    // (a chunk is below 2^31 tokens, and steps past its end below 2^32)
+    const uint32_t group = uint32_t(dv.group), rounds = group / 256, count = uint32_t(to - from);
+    const float* chunk = x + from;
+    const auto step = [&](uint32_t& at, uint32_t& in_group) {
+        at += 256;
+        if (++in_group == rounds) in_group = 0, at += (kWaves - 1) * group;
+    };
+    const auto load = [&](uint32_t at, float* v) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (at + 256 <= count) v[e] = (chunk + at)[64 * e + lane];
+            else v[e] = chunk[min(at + 64 * e + lane, count - 1)];
+        }
+    };
+    uint32_t at = uint32_t(__builtin_amdgcn_readfirstlane(wave)) * group, in_group = 0, next = at, next_group = 0;
+    float ahead[kAhead][4];
+    const auto load_ahead = [&] {
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            load(next, ahead[a]);
+            step(next, next_group);
+        }
+    };
+    load_ahead();
     fill_powers(s.powers);
     const Row r = row_of(p, row, ONE ? top_of(s, x, from, to) : row_best(ws), s.powers);
     if (r.greedy) {
@@ -914,72 +963,74 @@ __global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p, Division
         if (ONE) add_to_bins(s, r, x, from, to);
         b = ONE ? find_bins(s, r, s.count, s.weight) : find_bins(s, r, ws.count, ws.weight);
     }
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    double* group_sum = reinterpret_cast<double*>(s.weight);      // kThreads of them
-    unsigned long long* groups = reinterpret_cast<unsigned long long*>(static_cast<RowSpace*>(p.workspace) + p.m) +
-                                 (row * gridDim.x + blockIdx.x) * dv.groups;
+    // d = top - x of the tokens kept for sure (below `sure`), and of the candidates
+    const float sure = edge_of(b.first), end = edge_of(b.second + 1), k_from = edge_of(b.kbin), k_to = edge_of(b.kbin + 1);
+    // No token below `least` counts: past the last candidate's bin, or in rows
+    // without a cut below min_p (the slack covers every rounding).
+    float least = r.low;
+    {
+        const float reach = fmaxf(end, b.kbin < kBins ? k_to : 0.0f), slack = fabsf(r.top) * 0x1p-20f;
+        if (cut && end == end && (b.kbin >= kBins || k_to == k_to)) least = fmaxf(least, r.top - reach * (1.0f + 0x1p-20f) - slack);
+        if (!cut && r.floor > 0.0)
+            least = fmaxf(least, float(double(r.top) + (double(__log2f(float(r.floor))) - 1e-3) / r.rate) - slack);
+    }
+    double* group_sum = reinterpret_cast<double*>(s.weight);
     __syncthreads();
     group_sum[threadIdx.x] = 0.0;
-    __syncthreads();
     if (threadIdx.x == 0) s.flag = 0;
     __syncthreads();
-    // Rounds of 256 tokens, four a lane; the next two rounds are on their way
-    // meanwhile.
-    const int rounds = int(dv.group / 256);
-    const int mine = (max(0, dv.groups - wave) + kWaves - 1) / kWaves * rounds;    // of this wave
-    const auto place = [&](int i) { return from + (wave + i / rounds * kWaves) * dv.group + (i % rounds) * 256 + lane; };
-    const auto load = [&](int i, float* v) {
-        const int64_t at = place(i);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = i < mine && at + 64 * e < to ? x[at + 64 * e] : -INFINITY;
-    };
-    float ahead[2][4];
-    load(0, ahead[0]);
-    load(1, ahead[1]);
     double w = 0.0;
-    for (int i = 0; i < mine; ++i) {
-        const int64_t at = place(i);
-        float v[4];
+    const auto round = [&](float* v) {
+        if (at >= count) return;
+        const uint32_t here = at, g = here / group;
+        step(at, in_group);
+        if (here + 256 > count) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = ahead[0][e], ahead[0][e] = ahead[1][e];
-        load(i + 2, ahead[1]);
+            for (int e = 0; e < 4; ++e)
+                if (here + 64 * e + lane >= count) v[e] = -INFINITY;
+        }
+        if (__any(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) >= least)) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int bin = cut ? bin_of(r.top, v[e]) : 0;
-            if (bin < b.first) {
-                w += r.drawn(v[e]);
-            } else if ((bin <= b.second || bin == b.kbin) && !Row::nothing(r.exponent(v[e]))) {
-                const int c = atomicAdd(&s.flag, 1);
-                if (c < kCandidates) key[c] = argmax_key(v[e], uint32_t(at + 64 * e));
+            for (int e = 0; e < 4; ++e) {
+                if (!(v[e] >= least)) continue;
+                const float d = below_top(r.top, v[e]);
+                if (!(d >= sure)) {
+                    w += r.drawn(v[e]);
+                } else if (!(d >= end) || (d >= k_from && !(d >= k_to))) {
+                    const int c = atomicAdd(&s.flag, 1);
+                    if (c < kCandidates) key[c] = argmax_key(v[e], uint32_t(from) + here + 64 * e + lane);
+                }
             }
         }
-        if ((i + 1) % rounds) continue;
-#pragma unroll
-        for (int off = 32; off; off >>= 1) w += __shfl_xor(w, off, 64);
+        if (in_group && at < count) return;
+        if (__any(w != 0.0)) w = wave_sum(w);
         if (lane == 0) {
-            const int g = wave + i / rounds * kWaves;
-            group_sum[g] = w;
-            if (!ONE) put(&groups[g], (unsigned long long)__double_as_longlong(w));
+            if (ONE) group_sum[g] = w;
+            else put(&ws.sum[blockIdx.x * dv.groups + g], (unsigned long long)__double_as_longlong(w));
         }
         w = 0.0;
+    };
+    while (at < count) {
+        float v[kAhead][4];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[a][e] = ahead[a][e];
+        load_ahead();
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) round(v[a]);
     }
     __syncthreads();
     // the work-group's candidates join the row's list
-    const int found = s.flag;
-    if (!ONE && found) {
-        if (threadIdx.x == 0) s.in_bin = atomicAdd(&ws.candidates, unsigned(found));
-        __syncthreads();
-        const unsigned int at = s.in_bin;
-        for (int i = threadIdx.x; i < min(found, kCandidates); i += kThreads)
-            if (at + i < unsigned(kCandidates)) put(&ws.candidate[at + i], key[i]);
-    }
-    __syncthreads();
-    double all;
-    const double own_group = group_sum[threadIdx.x];
-    scan(s.d, own_group, &all);
-    unsigned int n = unsigned(found);
+    unsigned int n = unsigned(s.flag);
     if (!ONE) {
-        if (threadIdx.x == 0) put(&ws.sum[blockIdx.x], (unsigned long long)__double_as_longlong(all));
+        if (n) {
+            if (threadIdx.x == 0) s.in_bin = atomicAdd(&ws.candidates, n);
+            __syncthreads();
+            const unsigned int at = s.in_bin;
+            for (int i = threadIdx.x; i < int(min(n, unsigned(kCandidates))); i += kThreads)
+                if (at + i < unsigned(kCandidates)) put(&ws.candidate[at + i], key[i]);
+        }
         // every store of the work-group is at the device-wide level before it counts itself
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
@@ -994,77 +1045,37 @@ __global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p, Division
         draw_by_selection(s, p, row, r);
         return;
     }
+    const int groups = int((p.N + dv.group - 1) / dv.group);
+    double own = 0.0;
+    if (int(threadIdx.x) < groups)
+        own = ONE ? group_sum[threadIdx.x] : __longlong_as_double((long long)get(&ws.sum[threadIdx.x]));
     const double u = p.u[row];
-    if (n <= 64) {
-        if (wave != 0) return;
-        const unsigned long long mine = lane >= int(n) ? 0 : ONE ? key[lane] : get(&ws.candidate[lane]);
-        const double own = lane >= int(gridDim.x) ? 0.0 : ONE ? all : __longlong_as_double((long long)get(&ws.sum[lane]));
-        const int64_t pick = finish_wave(p, dv, r, b, x, mine, int(n), own, u, group_sum, [&](int c, int g) {
-            return ONE ? group_sum[g]
-                       : __longlong_as_double((long long)get(groups + (c - int(blockIdx.x)) * int64_t(dv.groups) + g));
-        });
-        if (lane == 0) p.idx[row] = pick < p.N ? int32_t(pick) : r.top_idx;
-        return;
-    }
-    if (!ONE) {
-        for (int i = threadIdx.x; i < int(n); i += kThreads) key[i] = get(&ws.candidate[i]);
-        if (threadIdx.x < gridDim.x)
-            chunk_sum[threadIdx.x] = __longlong_as_double((long long)get(&ws.sum[threadIdx.x]));
-    } else if (threadIdx.x == 0) {
-        chunk_sum[0] = all;
-    }
-    __syncthreads();
-    uint64_t last;
-    if (!cut_by_places(s, r, b, key, int(n), &last))
-        last = n <= kThreads ? cut_of_candidates<1>(s, r, b, key, int(n))
-                             : cut_of_candidates<kCandidates / kThreads>(s, r, b, key, int(n));
-    // Kept candidates join their chunks' sums, in fixed point, where the
-    // smallest kept weight still counts and the order does not.
-    unsigned long long* add = s.weight;
-    const auto kept = [&](int i) -> unsigned long long {
-        const double w = key[i] >= last ? r.drawn(value_of(uint32_t(key[i] >> 32))) : 0.0;
-        return w > 0.0 ? max(1ull, r.fixed(w)) : 0;
-    };
-    __syncthreads();
-    if (threadIdx.x < kMaxChunks) add[threadIdx.x] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < int(n); i += kThreads)
-        if (const unsigned long long w = kept(i)) atomicAdd(&add[int64_t(~uint32_t(key[i])) / dv.chunk], w);
-    __syncthreads();
-    if (threadIdx.x < gridDim.x) chunk_sum[threadIdx.x] += double(add[threadIdx.x]) / r.unit;
-    __syncthreads();
-    // the chunk in which the running sum passes the target: every wave finds it
-    const double own = lane < int(gridDim.x) ? chunk_sum[lane] : 0.0;
-    double upto = own;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const double o = __shfl_up(upto, off, 64);
-        if (lane >= off) upto += o;
-    }
-    const double target = u * __shfl(upto, 63, 64);
-    const uint64_t past = __ballot(own > 0.0 && upto > target);
-    int64_t pick = p.N;
-    if (u < 1.0 && past) {
-        const int c = __ffsll((unsigned long long)past) - 1;
-        double run = __shfl(upto - own, c, 64);
-        // its groups: what the chunk's work-group summed, and the kept candidates
+    uint64_t last = 0;
+    if (n) {
+        if (!ONE) {
+            for (int i = threadIdx.x; i < int(n); i += kThreads) key[i] = get(&ws.candidate[i]);
+            __syncthreads();
+        }
+        if (n <= 64)
+            last = cut_of_few(s, r, b, key, int(n));
+        else if (!cut_by_places(s, r, b, key, int(n), &last))
+            last = n <= kThreads ? cut_of_candidates<1>(s, r, b, key, int(n))
+                                 : cut_of_candidates<kCandidates / kThreads>(s, r, b, key, int(n));
+        // Kept candidates join their groups' sums, in fixed point, where the
+        // smallest kept weight still counts and the order does not.
+        unsigned long long* add = s.weight + kGroups;
+        __syncthreads();
         add[threadIdx.x] = 0;
         __syncthreads();
-        const int64_t begin = c * dv.chunk;
         for (int i = threadIdx.x; i < int(n); i += kThreads) {
-            const int64_t at = int64_t(~uint32_t(key[i])) - begin;
-            if (at < 0 || at >= dv.chunk) continue;
-            if (const unsigned long long w = kept(i)) atomicAdd(&add[at / dv.group], w);
+            if (key[i] < last) continue;
+            const double x = r.drawn(value_of(uint32_t(key[i] >> 32)));
+            if (x > 0.0) atomicAdd(&add[int64_t(~uint32_t(key[i])) / dv.group], max(1ull, r.fixed(x)));
         }
         __syncthreads();
-        double sum = ONE ? own_group : int(threadIdx.x) < dv.groups
-            ? __longlong_as_double((long long)get(groups + (c - int(blockIdx.x)) * int64_t(dv.groups) + threadIdx.x)) : 0.0;
-        sum += double(add[threadIdx.x]) / r.unit;
-        const int g = pick_group(s, sum, run, target);
-        run = s.d.wave[0];
-        const int64_t f = c * dv.chunk + max(g, 0) * dv.group;
-        if (g >= 0) pick = walk_group(s, r, x, f, min(p.N, f + dv.group), last, run, target);
+        own += double(add[threadIdx.x]) / r.unit;
     }
+    const int64_t pick = draw_token(s, r, x, last, own, dv.group, u);
     if (threadIdx.x == 0) p.idx[row] = pick < p.N ? int32_t(pick) : r.top_idx;
 }
 
@@ -1075,7 +1086,7 @@ size_t sample_workspace_bytes(int64_t m, int64_t N)
     if (m == 0) return 256;
     const Division d = division(m, N);
     if (d.chunks == 1) return 256;
-    return size_t(m) * (sizeof(RowSpace) + size_t(d.chunks) * size_t(d.groups) * 8);
+    return size_t(m) * sizeof(RowSpace);
 }
 
 hipError_t launch_sample(const SampleParams& p, hipStream_t s)
