@@ -202,13 +202,18 @@ struct Shape {
     static constexpr int STEPS = DP / 16;                               // products along the dimension
     static constexpr int DB = DP / 32;
 
-    // Swizzles: the chunk of a row's 16 bytes is moved so that the rows of one
-    // LDS access lie in different banks.
-    static __device__ __forceinline__ int k_swizzle(int row) { return CPR == 4 ? (row >> 1) & 3 : row & 7; }
+    // Swizzles: the chunk of a row's 16 bytes is moved so that what 32 lanes of
+    // an LDS access read lies in different banks: 16 rows of one chunk (K), or
+    // of two halves of 32 dimensions four rows of 32 bytes or eight of 16 (V).
+    static __device__ __forceinline__ int k_swizzle(int row)
+    {
+        return CPR == 4 ? (row >> 2) & 3 : CPR == 8 ? (row >> 1) & 7 : row & 15;
+    }
     static __device__ __forceinline__ int v_swizzle(int row)
     {
-        if (!E4M3) return (row & 3) << 1;
-        return CPR == 4 ? ((row >> 1) & 1) | (((row >> 3) & 1) << 1) : (row & 3) | (((row >> 3) & 1) << 2);
+        if (!E4M3) return CPR == 8 ? ((row >> 1) & 1) << 2 : (row & 3) << 2;
+        return CPR == 4 ? ((row >> 3) & 1) << 1 : CPR == 8 ? (row & 2) | ((row >> 3) & 1) << 2
+                                                          : (row & 3) << 1 | ((row >> 3) & 1) << 3;
     }
 };
 
