@@ -43,6 +43,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kAhead = 4;                  // LDS reads ahead of their matrix products
 constexpr float kRaise = 8.0f;             // log2 by which a score may pass the reference
 constexpr int kListPages = 1024;           // page ids of a run's segment, in LDS
 constexpr int kListSeqs = 128;             // sequences whose lengths are kept in LDS
@@ -279,62 +280,90 @@ struct State {
     int rlo, rhi;        // keys the lane's row sees
 };
 
-// A key tile (K and V, 32 or 64 keys from k0) against the wave's rows.
-// `masked`: some row does not see some key.
 template <class S>
-__device__ __forceinline__ void compute(State<S>& st, const uint8_t* kt, const uint8_t* vt, int k0, float c, bool masked,
-                                        int lane)
-{
-    const int col = lane & 31, h = lane >> 5, i16 = lane & 15, dh = (lane >> 4) & 1;
+struct Scores {
     f32x16 s[S::BLOCKS];
+};
+template <class S>
+struct Probs {
+    u32x4 p[2 * S::BLOCKS];   // bf16, as the second product takes them
+};
+
+// Scores of a key tile (32 or 64 keys) for the wave's rows.
+template <class S>
+__device__ __forceinline__ void scores(const State<S>& st, Scores<S>& sc, const uint8_t* kt, int lane)
+{
+    const int col = lane & 31, h = lane >> 5;
 #pragma unroll
     for (int b = 0; b < S::BLOCKS; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
-    // scores
+        for (int i = 0; i < 16; ++i) sc.s[b][i] = 0.0f;
     const int ksw = S::k_swizzle(col);
+    const uint8_t* row = kt + col * S::RB;
+    // Blocks alternate, so that a product does not wait on the one before it.
+    // Reads run kAhead products ahead: left to itself the compiler puts each
+    // next to its product, which then waits for it.
+    constexpr int READS = S::E4M3 ? S::STEPS / 2 * S::BLOCKS : S::STEPS * S::BLOCKS;
+    u32x4 f[READS];
+    const auto read = [&](int i) {
+        const int t = i / S::BLOCKS, b = i % S::BLOCKS;
+        f[i] = *reinterpret_cast<const u32x4*>(row + b * 32 * S::RB + (((2 * t + h) ^ ksw) << 4));
+    };
 #pragma unroll
-    for (int b = 0; b < S::BLOCKS; ++b) {
-        const uint8_t* row = kt + (b * 32 + col) * S::RB;
+    for (int i = 0; i < (kAhead < READS ? kAhead : READS); ++i) read(i);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < READS; ++i) {
+        const int t = i / S::BLOCKS, b = i % S::BLOCKS;
+        if (i + kAhead < READS) read(i + kAhead);
         if (!S::E4M3) {
-#pragma unroll
-            for (int t = 0; t < S::STEPS; ++t) {
-                const bf16x8 a = *reinterpret_cast<const bf16x8*>(row + (((2 * t + h) ^ ksw) << 4));
-                s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, st.q[t], s[b], 0, 0, 0);
-            }
+            sc.s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, f[i]), st.q[t], sc.s[b], 0, 0, 0);
         } else {
             // one 16-byte read is two steps: step 2 t + e takes dimensions 32 t + 16 h + 8 e on
 #pragma unroll
-            for (int t = 0; t < S::STEPS / 2; ++t) {
-                const u32x4 raw = *reinterpret_cast<const u32x4*>(row + (((2 * t + h) ^ ksw) << 4));
+            for (int e = 0; e < 2; ++e) {
+                union { bf16x8 v; bf16x2 p[4]; } a;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    union { bf16x8 v; bf16x2 p[4]; } a;
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        a.p[2 * x] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[2 * e + x], 1.0f, false);
-                        a.p[2 * x + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[2 * e + x], 1.0f, true);
-                    }
-                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, st.q[2 * t + e], s[b], 0, 0, 0);
+                for (int x = 0; x < 2; ++x) {
+                    a.p[2 * x] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[i][2 * e + x], 1.0f, false);
+                    a.p[2 * x + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[i][2 * e + x], 1.0f, true);
                 }
+                sc.s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, st.q[2 * t + e], sc.s[b], 0, 0, 0);
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
     }
-    if (masked) {
-        const uint32_t width = uint32_t(st.rhi - st.rlo);
-        const int first = k0 + 4 * h - st.rlo;
-#pragma unroll
-        for (int b = 0; b < S::BLOCKS; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (uint32_t(first + 32 * b + 8 * (i / 4) + i % 4) >= width) s[b][i] = -INFINITY;
-    }
-    // reference
-    float top = s[0][0];
+}
+
+// Keys from k0 that the lane's row does not see.
+template <class S>
+__device__ __forceinline__ void mask(const State<S>& st, Scores<S>& sc, int k0, int lane)
+{
+    const uint32_t width = uint32_t(st.rhi - st.rlo);
+    const int first = k0 + 4 * (lane >> 5) - st.rlo;
 #pragma unroll
     for (int b = 0; b < S::BLOCKS; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+        for (int i = 0; i < 16; ++i)
+            if (uint32_t(first + 32 * b + 8 * (i / 4) + i % 4) >= width) sc.s[b][i] = -INFINITY;
+}
+
+// The largest score of the lane's half of the row.
+template <class S>
+__device__ __forceinline__ float largest(const Scores<S>& sc)
+{
+    float top = sc.s[0][0];
+#pragma unroll
+    for (int b = 0; b < S::BLOCKS; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, sc.s[b][i]);
+    return top;
+}
+
+// Raises the row's reference where a score passes it by too much.
+template <class S>
+__device__ __forceinline__ void raise(State<S>& st, float top, float c)
+{
     top = fmaxf(top, other_half(top)) * c;
     const bool raise = top > st.m + kRaise;
     if (__any(raise)) {
@@ -348,48 +377,110 @@ __device__ __forceinline__ void compute(State<S>& st, const uint8_t* kt, const u
 #pragma unroll
             for (int i = 0; i < 16; ++i) st.o[d][i] *= keep;
     }
+}
+
+// Probabilities, which become bf16 (half a step, 2^-9 of each on average
+// less: errors of many keys cancel) for the matrix cores, and their sum.
+template <class S>
+__device__ __forceinline__ void probs(State<S>& st, const Scores<S>& sc, Probs<S>& pb, float c)
+{
     const float ref = st.m == -INFINITY ? 0.0f : st.m;
     float sum = 0.0f;
 #pragma unroll
     for (int b = 0; b < S::BLOCKS; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            s[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], c, -ref));
-            sum += s[b][i];
+        for (int x = 0; x < 8; ++x) {
+            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc.s[b][2 * x], c, -ref));
+            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc.s[b][2 * x + 1], c, -ref));
+            sum += p0;
+            sum += p1;
+            pb.p[2 * b + x / 4][x % 4] = pack_bf16(p0, p1);
         }
     st.l += sum;
-    // Output.  Probabilities become bf16 (half a step, 2^-9 of each on
-    // average less: errors of many keys cancel) for the matrix cores.
+}
+
+// A tile's values as the second product takes them: fragment i is 16 keys
+// (i / DB) by 32 dimensions (i % DB).
+template <class S>
+struct Values {
+    static constexpr int COUNT = 2 * S::BLOCKS * S::DB;
+    s16x4 f[COUNT][2];
+    const uint8_t* vt;
+    int row, chunk, half;
+
+    __device__ __forceinline__ Values(const uint8_t* tile, int lane) : vt(tile)
+    {
+        const int h = lane >> 5, i16 = lane & 15, dh = (lane >> 4) & 1, rr = i16 / 2;
+        row = S::E4M3 ? 8 * (rr / 4) + 4 * h + rr % 4 : 4 * h + i16 / 4;
+        chunk = (S::E4M3 ? dh : 2 * dh + (i16 & 3) / 2) ^ S::v_swizzle(row);
+        half = (i16 & 1) * 8;
+    }
+    __device__ __forceinline__ void read(int i)
+    {
+        const int kb = i / S::DB, d = i % S::DB;
+        // (16 keys on have the same swizzle)
+        const uint8_t* at = vt + (16 * kb + row) * S::RB + ((chunk ^ (S::E4M3 ? 2 * d : 4 * d)) << 4) + half;
+        if (!S::E4M3) {
+            f[i][0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+            f[i][1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 8 * S::RB));
+        } else {
+            f[i][0] = __builtin_bit_cast(s16x4, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)at));
+        }
+    }
+    __device__ __forceinline__ void begin()
+    {
 #pragma unroll
-    for (int b = 0; b < S::BLOCKS; ++b)
+        for (int i = 0; i < (kAhead < COUNT ? kAhead : COUNT); ++i) read(i);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    __device__ __forceinline__ bf16x8 value(int i) const
+    {
+        union { bf16x8 v; s16x4 h[2]; bf16x2 p[4]; } a;
+        if (!S::E4M3) {
+            a.h[0] = f[i][0];
+            a.h[1] = f[i][1];
+        } else {
+            const i32x2 raw = __builtin_bit_cast(i32x2, f[i][0]);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            union { bf16x8 v; uint32_t u[4]; } pb;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) pb.u[x] = pack_bf16(s[b][8 * t + 2 * x], s[b][8 * t + 2 * x + 1]);
-#pragma unroll
-            for (int d = 0; d < S::DB; ++d) {
-                union { bf16x8 v; s16x4 h[2]; bf16x2 p[4]; } a;
-                if (!S::E4M3) {
-                    const int row = b * 32 + 16 * t + 4 * h + i16 / 4;
-                    const int chunk = (4 * d + 2 * dh + (i16 & 3) / 2) ^ S::v_swizzle(row);
-                    const uint8_t* at = vt + row * S::RB + (chunk << 4) + (i16 & 1) * 8;
-                    a.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
-                    a.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 8 * S::RB));
-                } else {
-                    const int rr = i16 / 2, row = b * 32 + 16 * t + 8 * (rr / 4) + 4 * h + rr % 4;
-                    const int chunk = (2 * d + dh) ^ S::v_swizzle(row);
-                    const i32x2 raw = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                        (lds_i32x2*)(vt + row * S::RB + (chunk << 4) + (i16 & 1) * 8));
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        a.p[2 * x] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[x], 1.0f, false);
-                        a.p[2 * x + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[x], 1.0f, true);
-                    }
-                }
-                st.o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, pb.v, st.o[d], 0, 0, 0);
+            for (int x = 0; x < 2; ++x) {
+                a.p[2 * x] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[x], 1.0f, false);
+                a.p[2 * x + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[x], 1.0f, true);
             }
         }
+        return a.v;
+    }
+};
+
+// Adds the tile's values, weighed by the probabilities; the first reads have
+// begun.
+template <class S>
+__device__ __forceinline__ void output(State<S>& st, const Probs<S>& pb, Values<S>& v)
+{
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < Values<S>::COUNT; ++i) {
+        if (i + kAhead < Values<S>::COUNT) v.read(i + kAhead);
+        st.o[i % S::DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v.value(i), __builtin_bit_cast(bf16x8, pb.p[i / S::DB]),
+                                                                 st.o[i % S::DB], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// A key tile (K and V, 32 or 64 keys from k0) against the wave's rows.
+// `masked`: some row does not see some key.
+template <class S>
+__device__ __forceinline__ void compute(State<S>& st, const uint8_t* kt, const uint8_t* vt, int k0, float c, bool masked,
+                                        int lane)
+{
+    Scores<S> sc;
+    Probs<S> pb;
+    scores<S>(st, sc, kt, lane);
+    Values<S> v(vt, lane);
+    v.begin();
+    if (masked) mask<S>(st, sc, k0, lane);
+    raise<S>(st, largest<S>(sc), c);
+    probs<S>(st, sc, pb, c);
+    output<S>(st, pb, v);
 }
 
 // The loads of one tile, and what the tile needs before use.
@@ -407,7 +498,7 @@ struct Loader {
     int lane;
 
     // Rows [row0, row0 + ROWS) of the tile, the wave's part; its K and V at
-    // LDS offsets kt and vt, its first key k0.
+    // LDS offsets kt and vt, its first key k0.  True: it needs patch().
     __device__ __forceinline__ bool issue(uint32_t kt, uint32_t vt, int k0, int row0) const
     {
         const int lr = lane / S::CPR, lc = lane % S::CPR;
@@ -755,9 +846,9 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
                 list[i] = id >= p.pages ? -1 : id;
             }
             __syncthreads();
-            bool dirty = false, next = false;
-            if (S::SHARED) {
+            if constexpr (S::SHARED) {
                 const int row0 = wave * S::ROWS;
+                bool dirty = false;
                 for (int i = -1; i < n; ++i) {
                     const uint32_t kt = lds0 + (i & 1) * 2 * S::TILE;
                     const int k0 = start + i * S::STEP;
@@ -773,6 +864,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
                     if (i >= 0) run_tile(kt, k0);
                 }
             } else {
+                bool dirty = false, next = false;
                 const uint32_t ring = lds0 + wave * 4 * S::TILE;
                 const int k1 = start + wave * S::KT;
                 for (int i = -1; i < n; ++i) {
