@@ -159,8 +159,8 @@ struct Args {
     float scale;
 };
 
-// x / group, exact while x * group is below 2^30: x is a row of a unit beside
-// the heads before its first, below 127 + group, and group below 2^15.
+// x / group, exact while x * group is below 2^31: x is a row of a unit beside
+// the heads before its first, below 255 + group, and group below 2^15.
 __device__ __forceinline__ uint32_t by_group(const Args& p, uint32_t x) { return __umulhi(2 * x, p.by_group); }
 
 // One kernel shape.  DP: head dimension padded to a matrix-core multiple;
@@ -171,7 +171,7 @@ struct Shape {
     static constexpr bool E4M3 = E4M3_, SHARED = SHARED_, FULL = FULL_;
     // Waves.  Split: two, so that two to four work-groups share a compute
     // unit and one streams while another begins or ends a unit.
-    static constexpr int W = SHARED ? 4 : DP == 256 && !E4M3 ? 1 : 2;
+    static constexpr int W = SHARED ? DP == 256 ? 4 : 8 : DP == 256 && !E4M3 ? 1 : 2;
     static constexpr int THREADS = 64 * W;
     static constexpr int WAVES_PER_SIMD = DP <= 128 ? 2 : 1;
     static constexpr int M = SHARED ? 32 * W : 32;                      // rows of a unit
@@ -183,9 +183,10 @@ struct Shape {
     static constexpr int CPR = RB / 16;                                 // 16-byte chunks of it
     static constexpr int RPI = 64 / CPR;                                // rows of one load instruction
     static constexpr int TILE = KT * RB;                                // bytes of K or of V
-    static constexpr int ROWS = SHARED ? KT / W : KT;                   // rows a wave loads
+    static constexpr int RAW = SHARED ? KT / W : KT, ROWS = RAW < RPI ? RPI : RAW;   // rows a wave loads
+    static constexpr int STAGES = SHARED ? 4 : 2;
     static constexpr int LOADS = ROWS / RPI;                            // for K, and as many for V
-    static constexpr int RING = 2 * 2 * TILE * (SHARED ? 1 : W);        // two stages of K and V
+    static constexpr int RING = STAGES * 2 * TILE * (SHARED ? 1 : W);   // stages of K and V
     static constexpr int OS = DP + 4;                                   // floats of a row in the joining buffer
     static constexpr int JOIN = SHARED ? 0 : W * M * OS * 4;
     static constexpr int BUFFER = RING > JOIN ? RING : JOIN;
@@ -848,20 +849,27 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
             __syncthreads();
             if constexpr (S::SHARED) {
                 const int row0 = wave * S::ROWS;
-                bool dirty = false;
-                for (int i = -1; i < n; ++i) {
-                    const uint32_t kt = lds0 + (i & 1) * 2 * S::TILE;
+                const bool loads = row0 < S::KT;
+                uint32_t flags = 0;
+                const auto fetch = [&](int i) {
+                    const uint32_t to = lds0 + (i % S::STAGES) * 2 * S::TILE;
+                    if (loads && ld.issue(to, to + S::TILE, start + i * S::STEP, row0)) flags |= 1u << (i % S::STAGES);
+                };
+                for (int i = 0; i < min(n, S::STAGES - 1); ++i) fetch(i);
+                for (int i = 0; i < n; ++i) {
+                    const uint32_t kt = lds0 + (i % S::STAGES) * 2 * S::TILE;
                     const int k0 = start + i * S::STEP;
-                    if (i >= 0) {
-                        wait_loads<0>();
-                        if (dirty) ld.patch(lds + (kt - lds0), lds + (kt - lds0) + S::TILE, k0, row0);
-                        __syncthreads();
+                    if (i + S::STAGES - 2 < n) wait_loads<(S::STAGES - 2) * 2 * S::LOADS>();
+                    else wait_loads<0>();
+                    if (flags >> (i % S::STAGES) & 1) {
+                        ld.patch(lds + (kt - lds0), lds + (kt - lds0) + S::TILE, k0, row0);
+                        flags &= ~(1u << (i % S::STAGES));
                     }
-                    if (i + 1 < n) {
-                        const uint32_t nt = lds0 + ((i + 1) & 1) * 2 * S::TILE;
-                        dirty = ld.issue(nt, nt + S::TILE, k0 + S::STEP, row0);
-                    }
-                    if (i >= 0) run_tile(kt, k0);
+                    wait_lds();
+                    __builtin_amdgcn_s_barrier();
+                    asm volatile("" ::: "memory");
+                    if (i + S::STAGES - 1 < n) fetch(i + S::STAGES - 1);
+                    run_tile(kt, k0);
                 }
             } else {
                 bool dirty = false, next = false;
