@@ -18,9 +18,12 @@
 // (key 16 t + 8 (j / 4) + 4 h + j % 4 for half h, element j).  V^T comes from
 // the row-major tile through the transposing LDS reads.
 //
-// Two shapes.  `Shared`: the work-group's four waves hold 32 rows each and
-// share key tiles of K and V in LDS, so a tile is read once for 128 rows; for
-// prompts and chunks, bound by the matrix cores.  `Split`: the waves hold the
+// Two shapes.  `Shared`: the work-group's four or eight waves hold 32 rows
+// each and share key tiles of K and V in LDS, so a tile is read once for 128 or
+// 256 rows; for prompts and chunks, bound by the matrix cores and the vector
+// instructions of the softmax, which hardly overlap (busy 49% and 45% of the
+// cycles of 4099 tokens over 12301 keys, 32 heads of 128: 655 us, 1.05 PFLOP/s
+// where a large library product reaches 1.24).  `Split`: the waves hold the
 // same up to 32 rows and each streams key tiles of its own, joined in LDS at
 // the end; for single and drafted tokens, bound by reading the cache.
 //
@@ -48,6 +51,12 @@ constexpr float kRaise = 8.0f;             // log2 by which a score may pass the
 constexpr int kListPages = 1024;           // page ids of a run's segment, in LDS
 constexpr int kListSeqs = 128;             // sequences whose lengths are kept in LDS
 constexpr int kComputeUnits = 256;
+// Rows a sequence (tokens x group) from which eight waves share tiles in place
+// of four: 256 rows to a tile halve its reads, but a unit's beginning and end
+// cost more.  4099 tokens over 12301 keys (16396 rows): 735 us with four, 655
+// with eight; 2048 over 8192: 262 and 250; 512 over 8192: 91 both; 128 over
+// 4096: 39 and 46.
+constexpr int64_t kManyRows = 2048;
 // Counts of arrived parts come first in the workspace, in every shape as many
 // bytes: calls of other shapes leave them alone.
 constexpr size_t kCounterBytes = 4096;
@@ -95,7 +104,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
     return __builtin_bit_cast(uint32_t, v);
 }
 
-__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32, 64); }
+// The largest, and the sum, of a lane's value and that of the wave's other half.
+__device__ __forceinline__ float max_halves(float x)
+{
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+__device__ __forceinline__ float sum_halves(float x)
+{
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
 
 // Partial sums cross work-groups on different XCDs: device-scope accesses.
 __device__ __forceinline__ void put2(float* p, float a, float b)
@@ -164,14 +183,14 @@ struct Args {
 __device__ __forceinline__ uint32_t by_group(const Args& p, uint32_t x) { return __umulhi(2 * x, p.by_group); }
 
 // One kernel shape.  DP: head dimension padded to a matrix-core multiple;
-// FULL: the head has all of it.
-template <int DP_, bool E4M3_, bool SHARED_, bool FULL_>
+// FULL: the head has all of it; SHARING: waves that share tiles, 0 for Split.
+template <int DP_, bool E4M3_, int SHARING, bool FULL_>
 struct Shape {
     static constexpr int DP = DP_;
-    static constexpr bool E4M3 = E4M3_, SHARED = SHARED_, FULL = FULL_;
+    static constexpr bool E4M3 = E4M3_, SHARED = SHARING != 0, FULL = FULL_;
     // Waves.  Split: two, so that two to four work-groups share a compute
     // unit and one streams while another begins or ends a unit.
-    static constexpr int W = SHARED ? DP == 256 ? 4 : 8 : DP == 256 && !E4M3 ? 1 : 2;
+    static constexpr int W = SHARED ? SHARING : DP == 256 && !E4M3 ? 1 : 2;
     static constexpr int THREADS = 64 * W;
     static constexpr int WAVES_PER_SIMD = DP <= 128 ? 2 : 1;
     static constexpr int M = SHARED ? 32 * W : 32;                      // rows of a unit
@@ -184,7 +203,8 @@ struct Shape {
     static constexpr int RPI = 64 / CPR;                                // rows of one load instruction
     static constexpr int TILE = KT * RB;                                // bytes of K or of V
     static constexpr int RAW = SHARED ? KT / W : KT, ROWS = RAW < RPI ? RPI : RAW;   // rows a wave loads
-    static constexpr int STAGES = SHARED ? 4 : 2;
+    // tiles in LDS: two where two work-groups share a compute unit
+    static constexpr int STAGES = SHARED && (W == 8 || WAVES_PER_SIMD == 1) ? 4 : 2;
     static constexpr int LOADS = ROWS / RPI;                            // for K, and as many for V
     static constexpr int RING = STAGES * 2 * TILE * (SHARED ? 1 : W);   // stages of K and V
     static constexpr int OS = DP + 4;                                   // floats of a row in the joining buffer
@@ -365,7 +385,7 @@ __device__ __forceinline__ float largest(const Scores<S>& sc)
 template <class S>
 __device__ __forceinline__ void raise(State<S>& st, float top, float c)
 {
-    top = fmaxf(top, other_half(top)) * c;
+    top = max_halves(top) * c;
     const bool raise = top > st.m + kRaise;
     if (__any(raise)) {
         // of this lane's row alone: other rows keep their reference and their bits
@@ -894,7 +914,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
             }
             done += n;
         }
-        st.l += other_half(st.l);
+        st.l = sum_halves(st.l);
         __syncthreads();
         if (plan[5]) restore(st, p, ld, u.base + from * S::STEP, u.base + (from + count) * S::STEP);
 
@@ -1131,26 +1151,33 @@ hipError_t run(const AttnParams& a, Args p, hipStream_t s)
     return hipGetLastError();
 }
 
-// Calls f with the shape for a cache and a bound on a sequence's rows.
-template <class F>
-auto with_shape(bool e4m3, int dim, bool shared, F f)
+// Waves that share key tiles.  Up to 32 rows a sequence and kv head stream
+// the cache once either way: none.
+int sharing(int64_t tokens, int64_t max_q, int group, int seqs)
 {
-    const auto by_dim = [&](auto e, auto sh) {
-        constexpr bool E = decltype(e)::value, SH = decltype(sh)::value;
-        if (dim == 64) return f(Shape<64, E, SH, true>());
-        if (dim == 128) return f(Shape<128, E, SH, true>());
-        if (dim == 256) return f(Shape<256, E, SH, true>());
-        if (dim <= 64) return f(Shape<64, E, SH, false>());
-        if (dim <= 96) return f(Shape<96, E, SH, false>());
-        if (dim <= 128) return f(Shape<128, E, SH, false>());
-        return f(Shape<256, E, SH, false>());
-    };
-    if (e4m3) return shared ? by_dim(std::true_type(), std::true_type()) : by_dim(std::true_type(), std::false_type());
-    return shared ? by_dim(std::false_type(), std::true_type()) : by_dim(std::false_type(), std::false_type());
+    if (max_q * group <= 32) return 0;
+    return tokens * group >= kManyRows * seqs ? 8 : 4;
 }
 
-// Up to 32 rows a sequence and kv head stream the cache once either way.
-bool is_shared(int64_t max_q, int group) { return max_q * group > 32; }
+// Calls f with the shape for a cache and a call's rows.
+template <class F>
+auto with_shape(bool e4m3, int dim, int waves, F f)
+{
+    const auto by_dim = [&](auto e, auto w) {
+        constexpr bool E = decltype(e)::value;
+        constexpr int W = decltype(w)::value, W256 = W == 8 ? 4 : W;   // (a wave of 256 dimensions takes a whole SIMD's registers)
+        if (dim == 64) return f(Shape<64, E, W, true>());
+        if (dim == 128) return f(Shape<128, E, W, true>());
+        if (dim == 256) return f(Shape<256, E, W256, true>());
+        if (dim <= 64) return f(Shape<64, E, W, false>());
+        if (dim <= 96) return f(Shape<96, E, W, false>());
+        if (dim <= 128) return f(Shape<128, E, W, false>());
+        return f(Shape<256, E, W256, false>());
+    };
+    const auto by_type = [&](auto w) { return e4m3 ? by_dim(std::true_type(), w) : by_dim(std::false_type(), w); };
+    if (waves == 0) return by_type(std::integral_constant<int, 0>());
+    return waves == 4 ? by_type(std::integral_constant<int, 4>()) : by_type(std::integral_constant<int, 8>());
+}
 
 }  // namespace
 
@@ -1158,7 +1185,7 @@ size_t attention_workspace_bytes(bool e4m3, int64_t tokens, int q_heads, int kv_
                                  int64_t max_q, int64_t max_kv)
 {
     const int group = q_heads / kv_heads;
-    return with_shape(e4m3, head_dim, is_shared(max_q < tokens ? max_q : tokens, group), [&](auto shape) {
+    return with_shape(e4m3, head_dim, sharing(tokens, max_q < tokens ? max_q : tokens, group, seqs), [&](auto shape) {
         return bytes<decltype(shape)>(tokens, group, kv_heads, seqs, max_kv);
     });
 }
@@ -1200,7 +1227,7 @@ hipError_t launch_attention(const AttnParams& a, hipStream_t s)
     p.group = a.group;
     p.by_group = uint32_t(((uint64_t(1) << 31) + a.group - 1) / a.group);
     p.scale = a.scale;
-    return with_shape(a.cache.e4m3, a.cache.head_dim, is_shared(a.max_q, a.group),
+    return with_shape(a.cache.e4m3, a.cache.head_dim, sharing(a.tokens, a.max_q, a.group, a.seqs),
                       [&](auto shape) { return run<decltype(shape)>(a, p, s); });
 }
 
