@@ -80,10 +80,16 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p)
 // 16 bytes per lane from global memory to LDS at lds + 16 * lane, with no
 // register between.  The compiler does not count these loads: every use waits
 // by hand (wait_loads).
+// ONCE: what no other work-group reads, which need not stay in the caches.
+template <bool ONCE>
 __device__ __forceinline__ void load_lds_uniform(uint32_t lds, uint64_t base, uint32_t offset)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
-                 : "memory");
+    if (ONCE)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(lds), "v"(offset), "s"(base)
+                     : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
+                     : "memory");
 }
 __device__ __forceinline__ void load_lds(uint32_t lds, uint64_t address)
 {
@@ -539,8 +545,8 @@ struct Loader {
                 const uint32_t slot = uint32_t((k0 + row0 + j * S::RPI) & mask);
                 const uint64_t off = (uint64_t(id) * p.page16 + uint64_t(slot) * p.slot16) << 4;
                 const int ck = lc ^ S::k_swizzle(row0 + j * S::RPI + lr), cv = lc ^ S::v_swizzle(row0 + j * S::RPI + lr);
-                if (S::FULL || ck < chunks) load_lds_uniform(kt + j * 1024, kbase + off, row_off + 16 * ck);
-                if (S::FULL || cv < chunks) load_lds_uniform(vt + j * 1024, vbase + off, row_off + 16 * cv);
+                if (S::FULL || ck < chunks) load_lds_uniform<!S::SHARED>(kt + j * 1024, kbase + off, row_off + 16 * ck);
+                if (S::FULL || cv < chunks) load_lds_uniform<!S::SHARED>(vt + j * 1024, vbase + off, row_off + 16 * cv);
             }
         } else {
 #pragma unroll 1
