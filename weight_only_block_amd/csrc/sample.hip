@@ -557,21 +557,25 @@ __device__ __forceinline__ void add_to_bins(Shared& s, const Row& r, const float
     for (int i = threadIdx.x; i < kBins; i += kThreads) s.weight[i] = 0, s.count[i] = 0;
     __syncthreads();
     const bool weigh = r.top_p < 1.0, rank = r.k < r.N;
-    // (eight weights side by side, as their operations wait on each other)
-    each_token(x, from, to, [&](const float (&v)[8], int64_t) {
-        int bin[8];
-        unsigned long long w[8];
+    // (four weights side by side, as their operations wait on each other)
+    each_token(x, from, to, [&](const float (&v)[8], int64_t i) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) bin[e] = bin_of(below_top(r.top, v[e]));
-        if (weigh) {
+        for (int h = 0; h < 8; h += 4) {
+            if (i - threadIdx.x + h * kThreads >= to) break;         // the same in every lane
+            int bin[4];
+            unsigned long long w[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = r.fixed(r.weight(r.exponent(v[e])));
-        }
+            for (int e = 0; e < 4; ++e) bin[e] = bin_of(below_top(r.top, v[h + e]));
+            if (weigh) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (!r.live(v[e])) continue;
-            if (rank) atomicAdd(&s.count[bin[e]], 1u);
-            if (weigh) atomicAdd(&s.weight[bin[e]], w[e]);
+                for (int e = 0; e < 4; ++e) w[e] = r.fixed(r.weight(r.exponent(v[h + e])));
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (!r.live(v[h + e])) continue;
+                if (rank) atomicAdd(&s.count[bin[e]], 1u);
+                if (weigh) atomicAdd(&s.weight[bin[e]], w[e]);
+            }
         }
     });
     __syncthreads();
