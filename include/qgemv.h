@@ -447,8 +447,8 @@ qg_status qg_rope_append(const qg_kv_cache *cache, const qg_rope *rope, const vo
  *   out = sum_j softmax_j(scale * q . k_j) v_j,   lse = log sum_j exp(scale * q . k_j)
  * Query head h reads kv head h / (q_heads / kv_heads).  One token a sequence,
  * a few drafted ones, whole chunks, or a mix of them in one call.  A row that
- * sees no key gets zeros, and -infinity as its lse.  Keys that a row does not
- * see do not reach it, whatever they hold.
+ * sees no key, or whose every score is -infinity, gets zeros, and -infinity as
+ * its lse.  Keys that a row does not see do not reach it, whatever they hold.
  *   q_bf16      device bf16, element (row, h, d) at row * q_token_stride +
  *               h * q_head_stride + d; 16-byte aligned, strides in 16 bytes
  *   out_bf16    device bf16; 8-byte aligned, strides in 8 bytes

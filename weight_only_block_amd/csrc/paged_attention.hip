@@ -25,7 +25,9 @@
 // cycles of 4099 tokens over 12301 keys, 32 heads of 128: 655 us, 1.05 PFLOP/s
 // where a large library product reaches 1.24).  `Split`: the waves hold the
 // same up to 32 rows and each streams key tiles of its own, joined in LDS at
-// the end; for single and drafted tokens, bound by reading the cache.
+// the end; for single and drafted tokens, bound by reading the cache (two
+// sequences of 131072 bf16 keys, 1.07 GB: 174 us, 6.2 TB/s where a plain read
+// reaches 6.8; 32 ragged ones, 215 MB: 45 us).
 //
 // Division of the work.  All units' key steps are laid out in one line, head
 // by head, and cut into equal runs, one per work-group, whatever the lengths
@@ -408,8 +410,9 @@ __device__ __forceinline__ void raise(State<S>& st, float top, float c)
     }
 }
 
-// Probabilities, which become bf16 (half a step, 2^-9 of each on average
-// less: errors of many keys cancel) for the matrix cores, and their sum.
+// Probabilities, which become bf16 for the matrix cores (each off by at most
+// half a step, 2^-8 of it; over many keys the errors cancel), and their sum,
+// which takes them unrounded.
 template <class S>
 __device__ __forceinline__ void probs(State<S>& st, const Scores<S>& sc, Probs<S>& pb, float c)
 {

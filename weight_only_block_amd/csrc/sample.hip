@@ -21,10 +21,10 @@
 // Bound by fp64 weights (64 rows of 151936, 39 MB: 9 us for the largest logits,
 // 18 us for the histogram with its weights, 33 us for the draw) and, for few
 // rows, by latency (one row: 4 + 7 + 14 us, most of the last a chain of reads
-// and sums by the row's last work-group).  Rows of up to 8192 logits, and rows of any length
-// where there are more than 128, are a work-group's each, with all steps in one
-// launch.  A row whose cut falls into bins of more than 4096 tokens (many
-// nearly equal logits) gets its key by a radix selection over the row.
+// and sums by the row's last work-group).  Rows of up to 8192 logits, and rows
+// of any length where there are more than 128, are a work-group's each, with all
+// steps in one launch.  A row whose cut falls into bins of more than 4096 tokens
+// (many nearly equal logits) gets its key by a radix selection over the row.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
