@@ -1172,7 +1172,8 @@ hipError_t run(const AttnParams& a, Args p, hipStream_t s)
 }
 
 // Waves that share key tiles.  Up to 32 rows a sequence and kv head stream
-// the cache once either way: none.
+// the cache once either way: none (32 sequences of up to 9000 bf16 keys, 28
+// rows: 82 us, shared 90; a few short ones are faster shared, 36 and 28).
 int sharing(int64_t tokens, int64_t max_q, int group, int seqs)
 {
     if (max_q * group <= 32) return 0;
