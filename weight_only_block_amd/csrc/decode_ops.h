@@ -84,6 +84,23 @@ struct AttnParams {
     void* workspace;
 };
 
+// A sequence's new rows [q0, q0 + n) and cached keys.
+struct Seq {
+    int q0, n, kv;
+};
+
+// From its starts and length as the caller's device memory holds them, whatever
+// that is, cut to the call's rows, to max_q rows and to cap keys.
+__host__ __device__ inline Seq cut_seq(int start, int next, int kv, int tokens, int max_q, int cap)
+{
+    const auto cut = [](int x, int most) { return x < 0 ? 0 : x < most ? x : most; };
+    Seq s;
+    s.q0 = cut(start, tokens);
+    s.n = cut(cut(next, tokens) - s.q0, max_q);   // (both within [0, tokens]: no wrap)
+    s.kv = cut(kv, cap);
+    return s;
+}
+
 size_t attention_workspace_bytes(bool e4m3, int64_t tokens, int q_heads, int kv_heads, int head_dim, int seqs,
                                  int64_t max_q, int64_t max_kv);
 hipError_t launch_attention(const AttnParams& p, hipStream_t s);

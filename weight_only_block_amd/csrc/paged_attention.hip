@@ -249,18 +249,9 @@ struct Shape {
     }
 };
 
-struct Seq {
-    int q0, n, kv;
-};
-
 __device__ __forceinline__ Seq load_seq(const Args& p, int b)
 {
-    const int a0 = p.q_start[b], a1 = p.q_start[b + 1], kv = p.kv_len[b];
-    Seq s;
-    s.q0 = max(0, min(a0, p.tokens));
-    s.n = max(0, min(min(a1, p.tokens) - s.q0, p.max_q));
-    s.kv = max(0, min(kv, p.cap));
-    return s;
+    return cut_seq(p.q_start[b], p.q_start[b + 1], p.kv_len[b], p.tokens, p.max_q, p.cap);
 }
 
 // From LDS where all sequences fit.
