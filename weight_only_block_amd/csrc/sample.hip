@@ -175,7 +175,9 @@ __device__ __forceinline__ Row row_of(const SampleParams& p, int64_t row, uint64
     const float t = p.temperature ? p.temperature[row] : 1.0f;
     // greedy, or nothing to weigh: a NaN wins, and a row of -infinity gives its first
     r.greedy = !(t > 0.0f) || r.top != r.top || r.top == -INFINITY;
-    r.rate = 1.44269504088896340736 / double(t);
+    // (never 0: under an infinite temperature -infinity still weighs nothing, and
+    // finite logits differ by too little to tell)
+    r.rate = fmax(1.44269504088896340736 / double(t), 1e-300);
     r.low = r.top == INFINITY ? INFINITY : float(fmax(double(r.top) - 1100.0 / r.rate, double(-__FLT_MAX__)));
     r.N = p.N;
     r.k = p.top_k && p.top_k[row] > 0 ? min(int64_t(p.top_k[row]), p.N) : p.N;
