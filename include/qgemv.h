@@ -504,8 +504,9 @@ qg_status qg_paged_attention(const qg_kv_cache *cache, const uint16_t *q_bf16, i
  *   temperature, top_p, min_p  device fp32[m], top_k device int32[m]; NULL for
  *               1, 1, 0 and none
  *   workspace   device, >= qg_sample_workspace_size(m, N) bytes, 16-byte
- *               aligned, of any contents.  Calls that share one must not
- *               overlap in time.
+ *               aligned, of any contents; a size serves every call of no more
+ *               rows and no more logits.  Calls that share one must not overlap
+ *               in time.
  * Weights and sums are 64-bit; results do not depend on timing.
  * 1 <= N < 2^31, m <= 65535; m = 0 is a no-op. */
 size_t    qg_sample_workspace_size(int64_t m, int64_t N);

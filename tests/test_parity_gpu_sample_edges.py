@@ -47,3 +47,17 @@ def test_infinite_temperature(n, opts):
             us = np.full(7, u, np.float32)
             print("case", n, opts, t, u, flush=True)
             assert np.array_equal(_draw(rows, us, **settings), _want(rows, us, **settings))
+
+
+def test_a_workspace_of_the_largest_batch_serves_smaller_ones():
+    n = 9000
+    rng = np.random.default_rng(1)
+    ws = torch.zeros(Q.sample_workspace_size(200, n), dtype=torch.uint8, device="cuda")
+    idx = torch.empty(200, dtype=torch.int32, device="cuda")
+    logits = (3 * rng.standard_normal((200, n))).astype(np.float32)
+    x, u = torch.from_numpy(logits).cuda(), rng.random(200).astype(np.float32)
+    for m, k in ((200, n), (128, n), (64, n), (1, n), (129, 8193), (3, 8192)):
+        Q.sample_f32(x[:m, :k], torch.from_numpy(u[:m]).cuda(), idx[:m], ws)
+        torch.cuda.synchronize()
+        rows = sorted({0, m // 2, m - 1})
+        assert np.array_equal(idx.cpu().numpy()[rows], ref.sample(logits[rows, :k], u[rows])), (m, k)

@@ -256,7 +256,7 @@ qg_status qg_sample_f32(const float* logits, int64_t m, int64_t N, int64_t ldx, 
     if (!logits || !u || !idx_out || !workspace) return QG_ERR_INVALID_ARG;
     if (m == 0) return QG_OK;
     if (m < 0 || m > 65535 || N < 1 || N > kMaxCount || ldx < N || ldx > kMaxStride) return QG_ERR_INVALID_ARG;
-    if (workspace_bytes < qg::sample_workspace_bytes(m, N)) return QG_ERR_INVALID_ARG;
+    if (workspace_bytes < qg::sample_workspace_need(m, N)) return QG_ERR_INVALID_ARG;
     if (!aligned(logits, 4) || !aligned(u, 4) || !aligned(idx_out, 4) || !aligned(workspace, 16) ||
         (temperature && !aligned(temperature, 4)) || (top_k && !aligned(top_k, 4)) || (top_p && !aligned(top_p, 4)) ||
         (min_p && !aligned(min_p, 4)))

@@ -117,7 +117,8 @@ struct SampleParams {
     void* workspace;
 };
 
-size_t sample_workspace_bytes(int64_t m, int64_t N);
+size_t sample_workspace_need(int64_t m, int64_t N);    // of this shape
+size_t sample_workspace_bytes(int64_t m, int64_t N);   // of this shape and every smaller one
 hipError_t launch_sample(const SampleParams& p, hipStream_t s);
 
 }  // namespace qg

@@ -1087,12 +1087,17 @@ __global__ __launch_bounds__(kThreads) void sample_draw(SampleParams p, Division
 
 }  // namespace
 
+size_t sample_workspace_need(int64_t m, int64_t N)
+{
+    if (m == 0 || division(m, N).chunks == 1) return 256;
+    return size_t(m) * sizeof(RowSpace);
+}
+
+// The largest need of up to m rows of up to N logits: rows of several
+// work-groups come in batches of up to kResident / 2.
 size_t sample_workspace_bytes(int64_t m, int64_t N)
 {
-    if (m == 0) return 256;
-    const Division d = division(m, N);
-    if (d.chunks == 1) return 256;
-    return size_t(m) * sizeof(RowSpace);
+    return sample_workspace_need(m < kResident / 2 ? m : kResident / 2, N);
 }
 
 hipError_t launch_sample(const SampleParams& p, hipStream_t s)

@@ -901,6 +901,7 @@ def paged_attention(cache: KVCache, q, out, q_start, kv_len, page_table, workspa
 
 
 def sample_workspace_size(m: int, N: int) -> int:
+    """Bytes of workspace for sample_f32 of up to m rows of up to N logits."""
     return int(lib().qg_sample_workspace_size(m, N))
 
 
