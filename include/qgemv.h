@@ -466,7 +466,9 @@ qg_status qg_rope_append(const qg_kv_cache *cache, const qg_rope *rope, const vo
  *   workspace   device, >= qg_paged_attention_workspace_size(...) bytes,
  *               16-byte aligned, all zero before the first call; a completed
  *               call leaves it ready for the next, of any shape that needs no
- *               more.  Calls that share one must not overlap in time.
+ *               more.  A size serves every call on such a cache with as many
+ *               query heads and no more tokens, sequences, max_q and max_kv.
+ *               Calls that share one must not overlap in time.
  * Scores, softmax statistics and sums are fp32; probabilities enter the
  * second product as bf16.  The split of a sequence over work-groups and the
  * order of every sum depend on the arguments alone: a result is the same bits

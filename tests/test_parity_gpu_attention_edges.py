@@ -35,3 +35,13 @@ def test_starts_that_do_not_ascend_write_no_other_rows(q_len, second):
     assert (out[tokens:] == 7).all() and (lse[tokens:] == 7).all()
     if second <= q_len:                                  # sequence 0 has no rows
         assert (out[:max(second, 0)] == 7).all()
+
+
+def test_a_workspace_of_the_largest_call_serves_smaller_ones():
+    # bounds of the largest call: 300 tokens of up to 40 sequences with up to 900 keys
+    problems = [Problem(3, [300], [900], 8, 1, 128, 16, "bf16"), Problem(3, [1] * 40, [300] * 40, 8, 1, 128, 16, "bf16"),
+                Problem(3, [1], [900], 8, 1, 128, 16, "bf16"), Problem(3, [60, 1, 5], [200, 900, 77], 8, 1, 128, 16, "bf16")]
+    n = Q.paged_attention_workspace_size(problems[0].cache, 300, 8, 40, 300, 900)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    for p in problems:
+        p.check(p.run(workspace=ws))

@@ -213,10 +213,10 @@ qg_status qg_paged_attention(const qg_kv_cache* cache, const uint16_t* q_bf16, i
         out_token_stride % 4 != 0 || out_head_stride % 4 != 0 || (lse && !aligned(lse, 4)) || !aligned(q_start, 4) ||
         !aligned(kv_len, 4) || !aligned(page_table, 4) || !aligned(workspace, 16))
         return QG_ERR_ALIGNMENT;
-    if (workspace_bytes < qg::attention_workspace_bytes(p.cache.e4m3, tokens, q_heads, p.cache.kv_heads, p.cache.head_dim, seqs,
-                                                        max_q, max_kv))
-        return QG_ERR_INVALID_ARG;
     if (tokens == 0 || seqs == 0 || max_q == 0) return QG_OK;
+    if (workspace_bytes < qg::attention_workspace_need(p.cache.e4m3, tokens, q_heads, p.cache.kv_heads, p.cache.head_dim,
+                                                       seqs, max_q, max_kv))
+        return QG_ERR_INVALID_ARG;
     p.q = q_bf16;
     p.q_token = q_token_stride;
     p.q_head = q_head_stride;

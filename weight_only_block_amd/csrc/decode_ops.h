@@ -101,6 +101,9 @@ __host__ __device__ inline Seq cut_seq(int start, int next, int kv, int tokens, 
     return s;
 }
 
+// Of this shape; of this shape and every smaller one.
+size_t attention_workspace_need(bool e4m3, int64_t tokens, int q_heads, int kv_heads, int head_dim, int seqs,
+                                int64_t max_q, int64_t max_kv);
 size_t attention_workspace_bytes(bool e4m3, int64_t tokens, int q_heads, int kv_heads, int head_dim, int seqs,
                                  int64_t max_q, int64_t max_kv);
 hipError_t launch_attention(const AttnParams& p, hipStream_t s);

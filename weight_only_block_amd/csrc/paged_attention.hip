@@ -1193,13 +1193,30 @@ auto with_shape(bool e4m3, int dim, int waves, F f)
 
 }  // namespace
 
-size_t attention_workspace_bytes(bool e4m3, int64_t tokens, int q_heads, int kv_heads, int head_dim, int seqs,
-                                 int64_t max_q, int64_t max_kv)
+size_t attention_workspace_need(bool e4m3, int64_t tokens, int q_heads, int kv_heads, int head_dim, int seqs,
+                                int64_t max_q, int64_t max_kv)
 {
     const int group = q_heads / kv_heads;
     return with_shape(e4m3, head_dim, sharing(tokens, max_q < tokens ? max_q : tokens, group, seqs), [&](auto shape) {
         return bytes<decltype(shape)>(tokens, group, kv_heads, seqs, max_kv);
     });
+}
+
+// The largest need of any shape within the bounds: each kernel shape's grows
+// with all of them, and smaller calls may take another one than the largest.
+size_t attention_workspace_bytes(bool e4m3, int64_t tokens, int q_heads, int kv_heads, int head_dim, int seqs,
+                                 int64_t max_q, int64_t max_kv)
+{
+    const int group = q_heads / kv_heads;
+    size_t most = 0;
+    for (int waves : {0, 4, 8}) {
+        if (waves > sharing(tokens, max_q < tokens ? max_q : tokens, group, 1)) break;
+        const size_t n = with_shape(e4m3, head_dim, waves, [&](auto shape) {
+            return bytes<decltype(shape)>(tokens, group, kv_heads, seqs, max_kv);
+        });
+        if (n > most) most = n;
+    }
+    return most;
 }
 
 hipError_t launch_attention(const AttnParams& a, hipStream_t s)

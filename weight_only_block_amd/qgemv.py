@@ -850,8 +850,8 @@ def rope_append(cache: KVCache, rope: Rope, q, k, v, pos, slots, q_out, stream=N
 
 def paged_attention_workspace_size(cache: KVCache, tokens: int, q_heads: int, seqs: int, max_q: int,
                                    max_kv: int) -> int:
-    """Bytes of workspace for paged_attention with these bounds; raises for
-    arguments the call would refuse."""
+    """Bytes of workspace for paged_attention with these bounds or smaller
+    ones; raises for arguments the call would refuse."""
     size = int(lib().qg_paged_attention_workspace_size(cache._ref, tokens, q_heads, seqs, max_q, max_kv))
     if size == 0:
         raise QGError(QG_ERR_INVALID_ARG, "qg_paged_attention_workspace_size")
