@@ -474,9 +474,10 @@ qg_status qg_rope_append(const qg_kv_cache *cache, const qg_rope *rope, const vo
  * order of every sum depend on the arguments alone: a result is the same bits
  * from run to run.  Where starts do not ascend, which rows are written, and
  * by which sequence, is not defined; nothing outside them is.
- * QG_ERR_INVALID_ARG also for q_heads no multiple of kv_heads and a scale that
- * is not finite; QG_ERR_UNSUPPORTED for tokens * q_heads above 2^31 - 1, max_kv
- * above 2^30, seqs above 65535, q_heads above 32767. */
+ * QG_ERR_INVALID_ARG also for q_heads no multiple of kv_heads, overlapping rows
+ * of out or lse and a scale that is not finite; QG_ERR_UNSUPPORTED for
+ * tokens * q_heads above 2^31 - 1, max_kv above 2^30, seqs above 65535, q_heads
+ * above 32767. */
 size_t    qg_paged_attention_workspace_size(const qg_kv_cache *cache, int64_t tokens, int32_t q_heads, int32_t seqs,
                                             int64_t max_q, int64_t max_kv);
 qg_status qg_paged_attention(const qg_kv_cache *cache, const uint16_t *q_bf16, int64_t q_token_stride,

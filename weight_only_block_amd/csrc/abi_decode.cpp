@@ -8,6 +8,7 @@
 
 #include "../../include/qgemv.h"
 #include "decode_ops.h"
+#include "rows.h"
 
 namespace {
 
@@ -34,7 +35,7 @@ qg_status check_cache(const qg_kv_cache* c, qg::CacheView* out)
     if ((c->page_size & (c->page_size - 1)) != 0 || c->page_size > (1 << 20)) return QG_ERR_UNSUPPORTED;
     if (!stride_ok(c->page_stride) || !stride_ok(c->head_stride) || !stride_ok(c->slot_stride))
         return QG_ERR_INVALID_ARG;
-    // rows must not overlap where there is more than one
+    // (dimensions of one entry have no stride that matters)
     if ((c->page_size > 1 && c->slot_stride < c->head_dim) || (c->kv_heads > 1 && c->head_stride < c->head_dim) ||
         (c->pages > 1 && c->page_stride < c->head_dim))
         return QG_ERR_INVALID_ARG;
@@ -43,6 +44,8 @@ qg_status check_cache(const qg_kv_cache* c, qg::CacheView* out)
         c->slot_stride % unit)
         return QG_ERR_ALIGNMENT;
     if (e4m3 && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))) return QG_ERR_ALIGNMENT;
+    qg::Dim dims[] = {{c->pages, c->page_stride}, {c->kv_heads, c->head_stride}, {c->page_size, c->slot_stride}};
+    if (!qg::rows_disjoint(dims, c->head_dim)) return QG_ERR_INVALID_ARG;
     out->k = static_cast<uint8_t*>(c->k);
     out->v = static_cast<uint8_t*>(c->v);
     out->k_scale = e4m3 ? c->k_scale : nullptr;
@@ -135,6 +138,8 @@ qg_status qg_rope_append(const qg_kv_cache* cache, const qg_rope* rope, const vo
     if (!aligned(q, size) || !aligned(k, size) || !aligned(v, size) || !aligned(pos, 4) || !aligned(slots, 8) ||
         !aligned(q_out, 2))
         return QG_ERR_ALIGNMENT;
+    qg::Dim dims[] = {{tokens, out_token_stride}, {q_heads, out_head_stride}};
+    if (!qg::rows_disjoint(dims, p.cache.head_dim)) return QG_ERR_INVALID_ARG;
     if (tokens == 0) return QG_OK;
     p.q = q;
     p.k = k;
@@ -213,6 +218,8 @@ qg_status qg_paged_attention(const qg_kv_cache* cache, const uint16_t* q_bf16, i
         out_token_stride % 4 != 0 || out_head_stride % 4 != 0 || (lse && !aligned(lse, 4)) || !aligned(q_start, 4) ||
         !aligned(kv_len, 4) || !aligned(page_table, 4) || !aligned(workspace, 16))
         return QG_ERR_ALIGNMENT;
+    qg::Dim dims[] = {{tokens, out_token_stride}, {q_heads, out_head_stride}};
+    if (!qg::rows_disjoint(dims, p.cache.head_dim)) return QG_ERR_INVALID_ARG;
     if (tokens == 0 || seqs == 0 || max_q == 0) return QG_OK;
     if (workspace_bytes < qg::attention_workspace_need(p.cache.e4m3, tokens, q_heads, p.cache.kv_heads, p.cache.head_dim,
                                                        seqs, max_q, max_kv))
