@@ -3,6 +3,7 @@ ascend, many sequences, long lists of pages, values that are not finite
 (tests/decode_reference.py holds the derivation of the tolerances)."""
 import pytest
 
+import tests.decode_reference as ref
 from tests.test_parity_gpu_attention import Problem
 from weight_only_block_amd import qgemv as Q
 
@@ -45,3 +46,38 @@ def test_a_workspace_of_the_largest_call_serves_smaller_ones():
     ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
     for p in problems:
         p.check(p.run(workspace=ws))
+
+
+def _same_specials(got, want):
+    got, want = got.double(), want.double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got == float("inf"), want == float("inf"))
+    assert torch.equal(got == -float("inf"), want == -float("inf"))
+
+
+@pytest.mark.parametrize("dim", [64, 80, 128, 256])
+@pytest.mark.parametrize("q_len,kv,key", [(1, 90, 70), (4, 90, 88), (4, 700, 698), (40, 200, 190), (40, 200, 100),
+                                          (130, 300, 171), (600, 700, 650)])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("far", [0, 1])
+def test_an_infinite_value_weighs_as_its_probability(dim, q_len, kv, key, value, far):
+    # a value of infinity gives infinity to the rows that see it, and NaN (zero times infinity) where its
+    # probability is zero, whether all rows of a tile see the key or only later ones
+    p = Problem(9, [q_len], [kv], 4, 2, dim, 16, "bf16")
+    p.q_dev.fill_(1.0)
+    p.q = p.q_dev.cpu()
+    page, row = int(p.table[0, key // 16]), key % 16
+    scale = dim ** -0.5
+    for cache_v, cache_k in ((p.cache.v, p.cache.k), (p.v, p.k)):
+        cache_v[page, :, row] = value
+        if far:
+            cache_k[page, :, row] = -1000.0                # a score of -1000 dim^0.5
+    print("case", dim, q_len, kv, key, value, far, flush=True)
+    got = p.run()
+    owned = [torch.where(t.float().isnan() | (t.float().abs() > 1e30), torch.zeros(()), t.float()).double()
+             for t in (p.k, p.v)]
+    owned[1][page, :, row] = value
+    want = ref.attention(p.q.double(), owned[0], owned[1], p.table.tolist(), p.q_start, p.kv_lens, scale)
+    _same_specials(got[0], want[0])
+    sees = kv - q_len + torch.arange(q_len) >= key
+    assert sees.any() and (torch.isnan(got[0][sees].float()) if far else got[0][sees].float() == value).all()

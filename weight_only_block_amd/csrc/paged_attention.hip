@@ -609,30 +609,53 @@ struct Loader {
     }
 };
 
-// Gives the lane's row the values that patch() took out, of keys [from, to).
+// Gives the lane's row the values that patch() took out, of keys [from, to),
+// each times its probability: infinity stays one, but for a probability of
+// zero, as in a tile that all rows see.  Split: a key is its own wave's alone;
+// tiles begin at `from`.
 template <class S>
-__device__ __forceinline__ void restore(State<S>& st, const Args& p, const Loader<S>& ld, int from, int to)
+__device__ __forceinline__ void restore(State<S>& st, const Args& p, const Loader<S>& ld, int from, int to, float c, int wave)
 {
-    const int h = opaque(threadIdx.x & 63) >> 5;
     const int mask = (1 << p.page_shift) - 1;
+    const float ref = st.m == -INFINITY ? 0.0f : st.m;
 #pragma unroll 1
     for (int key = max(from, ld.lo); key < min(to, ld.hi); ++key) {
         if (key >= ld.all_lo && key < ld.all_hi) continue;
+        if (!S::SHARED && (key - from) / S::KT % S::W != wave) continue;
         const int id = ld.table[key >> p.page_shift];
         if (id < 0 || id >= p.pages) continue;
-        const uint8_t* row = reinterpret_cast<const uint8_t*>(ld.vbase) +
-                             ((uint64_t(uint32_t(id)) * p.page16 + uint64_t(uint32_t(key & mask)) * p.slot16) << 4);
+        const uint64_t off = (uint64_t(uint32_t(id)) * p.page16 + uint64_t(uint32_t(key & mask)) * p.slot16) << 4;
+        const uint8_t* krow = reinterpret_cast<const uint8_t*>(ld.kbase + off);
+        const uint8_t* vrow = reinterpret_cast<const uint8_t*>(ld.vbase + off);
+        const int h = opaque(threadIdx.x & 63) >> 5;     // (here: offsets of all dimensions take no registers around the loop)
+        const auto value = [&](const uint8_t* row, int dim) {
+            return S::E4M3 ? __builtin_amdgcn_cvt_f32_fp8(int(row[dim]), 0)
+                           : __uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(row)[dim]) << 16);
+        };
+        float score = 0.0f;
+#pragma unroll
+        for (int t = 0; t < S::STEPS; ++t) {
+            const int d = S::E4M3 ? 32 * (t / 2) + 16 * h + 8 * (t % 2) : 16 * t + 8 * h;
+            if (S::FULL || d < p.dim) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) score = __builtin_fmaf(float(st.q[t][e]), value(krow, d + e), score);
+            }
+            asm volatile("" ::: "memory");       // few loads, and registers for them, at a time
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        const float pr = __builtin_amdgcn_exp2f(__builtin_fmaf(sum_halves(score), c, -ref));
         const bool sees = key >= st.rlo && key < st.rhi;
 #pragma unroll
         for (int d = 0; d < S::DB; ++d)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const int dim = 32 * d + 8 * (i / 4) + 4 * h + i % 4;
-                if (!S::FULL && dim >= p.dim) continue;
-                float v;
-                if (!S::E4M3) v = __uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(row)[dim]) << 16);
-                else v = __builtin_amdgcn_cvt_f32_fp8(int(row[dim]), 0);
-                if (sees && !(fabsf(v) < INFINITY)) st.o[d][i] += v;
+                if (!S::FULL && 32 * d + 16 * (i / 8) >= p.dim) continue;    // (whole sixteens)
+                const float v = value(vrow, 32 * d + 8 * (i / 4) + 4 * h + i % 4);
+                if (sees && !(fabsf(v) < INFINITY)) st.o[d][i] += pr * v;
+                if (i % 4 == 3) {
+                    asm volatile("" ::: "memory");
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
     }
 }
@@ -918,7 +941,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
         }
         st.l = sum_halves(st.l);
         __syncthreads();
-        if (plan[5]) restore(st, p, ld, u.base + from * S::STEP, u.base + (from + count) * S::STEP);
+        if (plan[5]) restore(st, p, ld, u.base + from * S::STEP, u.base + (from + count) * S::STEP, c, wave);
 
         // ---- results: whole units to the output, parts to the workspace
         const bool whole = count == u.steps;
