@@ -4,7 +4,7 @@ ascend, many sequences, long lists of pages, values that are not finite
 import pytest
 
 import tests.decode_reference as ref
-from tests.test_parity_gpu_attention import Problem
+from tests.test_parity_gpu_attention import Problem, _poisoned
 from weight_only_block_amd import qgemv as Q
 
 torch = pytest.importorskip("torch")
@@ -81,3 +81,62 @@ def test_an_infinite_value_weighs_as_its_probability(dim, q_len, kv, key, value,
     _same_specials(got[0], want[0])
     sees = kv - q_len + torch.arange(q_len) >= key
     assert sees.any() and (torch.isnan(got[0][sees].float()) if far else got[0][sees].float() == value).all()
+
+
+@pytest.mark.parametrize("seqs", [128, 129, 300, 1100])
+@pytest.mark.parametrize("kind,hq,hk,dim", [("bf16", 2, 1, 64), ("e4m3", 4, 2, 48)])
+@pytest.mark.parametrize("chunks", [0, 1, 2])
+def test_many_sequences(seqs, kind, hq, hk, dim, chunks):
+    # past 128 sequences lengths are read again for each unit; single tokens alone, with a few chunks, with long ones
+    g = torch.Generator().manual_seed(seqs + chunks)
+    q_lens = (torch.rand(seqs, generator=g) < 0.9).int().tolist()
+    kv_lens = torch.randint(0, 70, (seqs,), generator=g).tolist()
+    for b in range(5, seqs, 60):
+        q_lens[b] = [1, 40, 130][chunks]
+        kv_lens[b] = q_lens[b] + 25
+    q_lens[-1], kv_lens[-1] = q_lens[5], 500
+    p = Problem(seqs, q_lens, kv_lens, hq, hk, dim, 16, kind)
+    print("case", seqs, kind, hq, hk, dim, chunks, flush=True)
+    p.check(p.run())
+    if chunks:
+        p.check(p.run(window=37), window=37)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("q_len,dim,kv,page", [(1, 64, 60000, 1), (1, 48, 60001, 1), (4, 64, 60013, 1), (40, 64, 30000, 1),
+                                               (300, 48, 25000, 1), (1, 64, 240000, 2)])
+def test_runs_of_more_pages_than_the_list_holds(kind, q_len, dim, kv, page):
+    # a work-group's run reaches over more than 1024 pages
+    p = Problem(kv + q_len, [q_len], [kv], 8 if q_len == 300 else 1, 1, dim, page, kind)
+    print("case", kind, q_len, dim, kv, page, flush=True)
+    if q_len < 300:
+        p.check(p.run(scale=0.5), scale=0.5)
+        return
+    # (the definition of some rows: each as a call of its own prefix would give it)
+    out, lse = p.run()
+    rows = [0, 1, 170, 298, 299]
+    clean = [torch.nan_to_num(t.float().double(), nan=0.0, posinf=0.0, neginf=0.0) for t in (p.k, p.v)]
+    for i in rows:
+        want = ref.attention(p.q[i:i + 1].double(), *clean, p.table.tolist(), [0, 1], [kv - q_len + i + 1], dim ** -0.5, 0,
+                             p.ks, p.vs)
+        tol, lse_tol = ref.attention_tolerance(*want, dim)
+        assert ((out[i].double() - want[0][0]).abs() <= tol[0]).all()
+        assert ((lse[i].double() - want[1][0]).abs() <= lse_tol[0]).all()
+
+
+@pytest.mark.parametrize("dim", [64, 80, 128, 256])
+@pytest.mark.parametrize("q_len,kv,key,window", [(4, 90, 88, 0), (5, 700, 697, 0), (4, 300, 255, 43), (2, 90, 50, 39),
+                                                 (60, 190, 150, 0), (60, 190, 140, 33)])
+@pytest.mark.parametrize("name", ["k", "v"])
+def test_nan_of_an_8_bit_cache_reaches_its_rows_alone(dim, q_len, kv, key, window, name):
+    p = Problem(31, [q_len], [kv], 4, 2, dim, 16, "e4m3")
+    clean = p.run(window=window)
+    _poisoned(p, 0, key, [0, 1], {name: float("nan")})
+    print("case", dim, q_len, kv, key, window, name, flush=True)
+    got = p.run(window=window)
+    own = kv - q_len + torch.arange(q_len)
+    sees = (own >= key) & (own < key + window if window else own >= 0)
+    assert sees.any() and not sees.all()
+    assert torch.isnan(got[0][sees].float()).all()
+    assert torch.equal(got[0][~sees].view(torch.int16), clean[0][~sees].view(torch.int16))
+    assert torch.equal(got[1][~sees], clean[1][~sees])
