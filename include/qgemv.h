@@ -413,7 +413,7 @@ qg_status qg_rope_init(qg_rope *rope, int32_t rot_dim, int32_t interleaved, doub
                        double factor, int64_t original_len, double beta_fast, double beta_slow, double amplitude);
 
 /* Rotates the queries into q_out and the keys into the cache, and copies the
- * values into the cache, for `tokens` tokens in one launch:
+ * values into the cache, for `tokens` tokens (in one launch up to 2^23):
  *   q, k, v     device, fp32 (QG_SRC_F32, as the GEMV calls write) or bf16
  *               (QG_SRC_BF16): element (t, h, d) at t * token_stride +
  *               h * head_stride + d; views of one QKV row are fine

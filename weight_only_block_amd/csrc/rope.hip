@@ -210,7 +210,7 @@ void launch_wide(const RopeParams& p, dim3 grid, hipStream_t s)
 
 }  // namespace
 
-hipError_t launch_rope(const RopeParams& p, hipStream_t s)
+static hipError_t launch_tokens(const RopeParams& p, hipStream_t s)
 {
     if (!p.wide || p.rot_dim % 8 != 0) {
         hipLaunchKernelGGL(rope_append_narrow, dim3(unsigned(p.tokens)), dim3(256), 0, s, p);
@@ -229,6 +229,29 @@ hipError_t launch_rope(const RopeParams& p, hipStream_t s)
         else launch_wide<false, false>(p, grid, s);
     }
     return hipGetLastError();
+}
+
+// A grid has fewer than 2^32 threads (more are dropped without an error), and
+// a token takes 256: more tokens go in several launches.
+hipError_t launch_rope(const RopeParams& p, hipStream_t s)
+{
+    constexpr int64_t kMost = int64_t(1) << 23;
+    if (p.tokens <= kMost) return launch_tokens(p, s);
+    const int64_t size = p.f32 ? 4 : 2;
+    const auto on = [&](const void* x, int64_t elements) { return static_cast<const uint8_t*>(x) + elements * size; };
+    for (int64_t t = 0; t < p.tokens; t += kMost) {
+        RopeParams part = p;
+        part.q = on(p.q, t * p.q_token);
+        part.k = on(p.k, t * p.k_token);
+        part.v = on(p.v, t * p.v_token);
+        part.q_out += t * p.o_token;
+        part.pos += t;
+        part.slots += t;
+        part.tokens = p.tokens - t < kMost ? p.tokens - t : kMost;
+        const hipError_t e = launch_tokens(part, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace qg
