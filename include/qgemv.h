@@ -510,7 +510,11 @@ qg_status qg_paged_attention(const qg_kv_cache *cache, const uint16_t *q_bf16, i
  *               aligned, of any contents; a size serves every call of no more
  *               rows and no more logits.  Calls that share one must not overlap
  *               in time.
- * Weights and sums are 64-bit; results do not depend on timing.
+ * Weights are fp64.  top_p compares sums, and a candidate at the cut adds to
+ * the draw's, in 64-bit fixed point of b = min(50, 62 - bits of N) bits after the
+ * point (44 for 151936 logits) with the largest weight 1: a cut among tokens
+ * that weigh less than N 2^-b (1e-8 there) may fall some tokens beside the fp64
+ * one.  The draw's other sums are fp64.  Results do not depend on timing.
  * 1 <= N < 2^31, m <= 65535; m = 0 is a no-op. */
 size_t    qg_sample_workspace_size(int64_t m, int64_t N);
 qg_status qg_sample_f32(const float *logits, int64_t m, int64_t N, int64_t ldx, const float *u,

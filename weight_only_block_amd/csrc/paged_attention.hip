@@ -21,13 +21,14 @@
 // Two shapes.  `Shared`: the work-group's four or eight waves hold 32 rows
 // each and share key tiles of K and V in LDS, so a tile is read once for 128 or
 // 256 rows; for prompts and chunks, bound by the matrix cores and the vector
-// instructions of the softmax, which hardly overlap (busy 49% and 45% of the
-// cycles of 4099 tokens over 12301 keys, 32 heads of 128: 655 us, 1.05 PFLOP/s
-// where a large library product reaches 1.24).  `Split`: the waves hold the
+// instructions of the softmax, which hardly overlap (busy 49% and 46% of the
+// cycles of 4099 tokens over 12301 keys, 32 heads of 128: 649 to 690 us by the
+// card's clock, 1.0 to 1.06 PFLOP/s where a large library product reaches 1.24;
+// 722 us with e4m3 keys, whose fragments each wave converts for itself).  `Split`: the waves hold the
 // same up to 32 rows and each streams key tiles of its own, joined in LDS at
 // the end; for single and drafted tokens, bound by reading the cache (two
 // sequences of 131072 bf16 keys, 1.07 GB: 174 us, 6.2 TB/s where a plain read
-// reaches 6.8; 32 ragged ones, 215 MB: 45 us).
+// reaches 6.8; 32 ragged ones, 215 MB: 44 us).
 //
 // Division of the work.  All units' key steps are laid out in one line, head
 // by head, and cut into equal runs, one per work-group, whatever the lengths

@@ -18,13 +18,20 @@
 //      gives the key, adds the kept ones to the sums of their groups (256
 //      tokens, more in very long rows), finds the group that the uniform number
 //      falls into and the token in it.
-// Bound by fp64 weights (64 rows of 151936, 39 MB: 9 us for the largest logits,
-// 18 us for the histogram with its weights, 33 us for the draw) and, for few
-// rows, by latency (one row: 4 + 7 + 14 us, most of the last a chain of reads
-// and sums by the row's last work-group).  Rows of up to 8192 logits, and rows
-// of any length where there are more than 128, are a work-group's each, with all
-// steps in one launch.  A row whose cut falls into bins of more than 4096 tokens
-// (many nearly equal logits) gets its key by a radix selection over the row.
+// No row has all its logits weighed twice: the histogram weighs rows with
+// top-p, the draw all tokens of rows without a cut and the kept ones of others.
+// 64 rows of 151936, 39 MB, in mixed settings: 9 us for the largest logits, 18
+// for the histogram, bound by its fp64 weights, and 33 for the draw, bound by
+// fp64 weights one after another in rows without a cut (17 us of its scan, 7 with
+// top-k) and by the dependent steps at the end of rows with one (6 to 11 us).
+// All without a cut take 36 us, with top-k 44, top-p 61, both 56.  Few rows are
+// bound by latency (one: 4 + 6 + 14 us, most of the last a chain of reads and
+// sums by the row's last work-group).
+// Rows of up to 8192 logits, and rows of any length where there are more than
+// 128, are a work-group's each, with all steps in one launch.  A row whose cut
+// falls into bins of more than 4096 tokens (many nearly equal logits) gets its
+// key by a radix selection over the row, by one work-group (151936 logits within
+// 0.1 of each other and top-p: 256 us for one row, 313 for 64).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -813,7 +813,7 @@ def _stream_of(stream, device: int):
 
 def rope_append(cache: KVCache, rope: Rope, q, k, v, pos, slots, q_out, stream=None, check=True):
     """Rotates q [tokens][heads][dim] into q_out (bfloat16) and k into the
-    cache at each token's slot, and copies v there, in one launch.
+    cache at each token's slot, and copies v there, in one launch up to 2^23 tokens.
 
     q, k, v: device float32 or bfloat16, any token and head strides (views of
     one QKV row); pos: device int32 [tokens]; slots: device int64 [tokens], a
