@@ -469,11 +469,12 @@ qg_status qg_rope_append(const qg_kv_cache *cache, const qg_rope *rope, const vo
  *               more.  A size serves every call on such a cache with as many
  *               query heads and no more tokens, sequences, max_q and max_kv.
  *               Calls that share one must not overlap in time.
- * Scores, softmax statistics and sums are fp32; probabilities enter the
- * second product as bf16.  The split of a sequence over work-groups and the
- * order of every sum depend on the arguments alone: a result is the same bits
- * from run to run.  Where starts do not ascend, which rows are written, and
- * by which sequence, is not defined; nothing outside them is.
+ * Scores, softmax statistics and sums are fp32 (values above 2^120 / keys in
+ * magnitude may sum past its range); probabilities enter the second product as
+ * bf16.  The split of a sequence over work-groups and the order of every sum
+ * depend on the arguments alone: a result is the same bits from run to run.
+ * Where starts do not ascend, which rows are written, and by which sequence, is
+ * not defined; nothing outside them is.
  * QG_ERR_INVALID_ARG also for q_heads no multiple of kv_heads, overlapping rows
  * of out or lse and a scale that is not finite; QG_ERR_UNSUPPORTED for
  * tokens * q_heads above 2^31 - 1, max_kv above 2^30, seqs above 65535, q_heads

@@ -5,7 +5,8 @@
 //
 // with m a running reference of the row's scores, raised (and the sums scaled
 // down) only when a score passes it by 2^8: any reference gives the same
-// quotient, and p up to 2^8 loses nothing in fp32 or bf16.
+// quotient, and p up to 2^8 loses nothing in fp32 or bf16 (sums stay in range
+// for values up to 2^120 / keys).
 //
 // Rows.  The query heads that share a kv head are rows beside the tokens: row
 // r of a sequence is token r / group, head r % group, so a key tile is read
