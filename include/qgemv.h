@@ -358,16 +358,27 @@ qg_status qgemv_q8g64_argmax_noalloc(const void *w_packed, const uint16_t *x_bf1
  *   k_scale,    device fp32, one per kv head, QG_KV_E4M3 only (else ignored):
  *   v_scale     what an 8-bit code is multiplied by
  *   page_size   tokens per page, a power of two up to 2^20
- *   head_dim    a multiple of 16, up to 256
- *   dtype       QG_KV_BF16, or QG_KV_E4M3 (8-bit floats: 4 exponent and 3
- *               mantissa bits, largest 448, no infinity)
+ *   head_dim    a multiple of 16, up to 256; of 32 with QG_KV_MXFP4
+ *   dtype       QG_KV_BF16, QG_KV_E4M3 (8-bit floats: 4 exponent and 3
+ *               mantissa bits, largest 448, no infinity) or QG_KV_MXFP4
  *   strides     0..2^31 elements, multiples of 16 bytes; rows must not overlap
+ * QG_KV_MXFP4 holds blocks of 32 dimensions of a token's head: 32 4-bit codes,
+ * the even dimension in a byte's low half, and an exponent byte b.  A code's
+ * low three bits pick one of 0, 0.5, 1, 1.5, 2, 3, 4 and 6, its top bit is the
+ * sign, and the element is that times 2^(b - 127).  With b above 252 the whole
+ * block is NaN; with b of 0 or 1 (which no call here writes) elements below
+ * 2^-126 may count as zero.  The fields after dtype are read for this type only:
+ *   k_block_scale,  device bytes; block i of (page, h, s) at page *
+ *   v_block_scale   scale_page_stride + h * scale_head_stride + s *
+ *               scale_slot_stride + i, i < head_dim / 32, rows not overlapping,
+ *               strides 0..2^31 and any alignment
  * Errors of every call that takes one: QG_ERR_INVALID_ARG for a null pointer,
  * a size below 1 or overlapping rows, QG_ERR_UNSUPPORTED for a head_dim,
  * page_size or dtype outside the above, QG_ERR_ALIGNMENT for a pointer or
  * stride. */
 #define QG_KV_BF16 0
 #define QG_KV_E4M3 1
+#define QG_KV_MXFP4 3
 typedef struct qg_kv_cache {
     void *k;
     void *v;
@@ -381,6 +392,12 @@ typedef struct qg_kv_cache {
     int32_t page_size;
     int32_t head_dim;
     int32_t dtype;
+    /* QG_KV_MXFP4 */
+    uint8_t *k_block_scale;
+    uint8_t *v_block_scale;
+    int64_t scale_page_stride;
+    int64_t scale_head_stride;
+    int64_t scale_slot_stride;
 } qg_kv_cache;
 
 /* Rotary frequencies, made once per model by qg_rope_init (host only) and
@@ -426,7 +443,12 @@ qg_status qg_rope_init(qg_rope *rope, int32_t rot_dim, int32_t interleaved, doub
  * Dimensions from rot_dim on are copied.  Angles are exact to 2^-65 turns per
  * position whatever the position; the rotation is fp32.  A bf16 cache takes
  * values rounded to nearest even; an 8-bit one takes x / scale clamped to
- * +-448 and rounded to nearest even, NaN kept.
+ * +-448 and rounded to nearest even, NaN kept.  A 4-bit one takes blocks: the
+ * exponent byte b is that of the smallest power of two by which the block's
+ * largest magnitude is at most 7 (so that no element is off by more than one
+ * such power), kept within 2..252, and 255 for a block that holds a NaN;
+ * elements are rounded to the nearest code, ties to the even one, beyond 6 to
+ * 6.  Its keys are rotated in fp64, so that codes are those of the definition.
  * QG_ERR_INVALID_ARG: null pointer, tokens < 0, q_heads < 1, rot_dim above
  * head_dim, a stride out of 0..2^31, overlapping q_out rows; tokens = 0 does
  * nothing, and the stride of a dimension of one entry is ignored.  Pointers need their element's alignment; 16-byte aligned rows are
@@ -438,6 +460,23 @@ qg_status qg_rope_append(const qg_kv_cache *cache, const qg_rope *rope, const vo
                          int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, const int32_t *pos,
                          const int64_t *slots, uint16_t *q_out, int64_t out_token_stride, int64_t out_head_stride,
                          int64_t tokens, int32_t q_heads, void *hip_stream);
+
+/* Reads cached tokens back, as the numbers that they stand for: for token t
+ * < tokens, the keys and values at slots[t] go to
+ *   k_out, v_out  device, fp32 (QG_SRC_F32) or bf16 (QG_SRC_BF16) by out_dtype,
+ *               (t, h, d) at t * token_stride + h * head_stride + d; either one
+ *               NULL: not wanted.  Must not overlap the cache or each other.
+ *   slots       device int64[tokens], as for qg_rope_append; the same slot may
+ *               come several times; a token whose slot is outside the cache
+ *               leaves its rows as they were
+ * For another cache's type, another machine, or work on keys that other calls
+ * of this library do not do.  4-bit and bf16 values are exact in either type,
+ * but for those beyond its range (fp32 holds all; bf16 rounds none); an 8-bit
+ * one is code * scale in fp32, rounded once more to bf16 where asked for.
+ * Errors as qg_rope_append's. */
+qg_status qg_kv_read(const qg_kv_cache *cache, const int64_t *slots, void *k_out, void *v_out, int32_t out_dtype,
+                     int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                     int64_t tokens, void *hip_stream);
 
 /* Attention of each sequence's new tokens over its cached tokens (the new
  * ones among them).  For sequence b with n = q_start[b+1] - q_start[b] new

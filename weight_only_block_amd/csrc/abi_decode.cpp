@@ -1,5 +1,5 @@
 // C ABI of the operators between a decode step's GEMV calls (rotary positions
-// with cache append, paged attention, sampling): argument checks on the host
+// with cache append, cached tokens read back, paged attention, sampling): argument checks on the host
 // and one launch sequence on the caller's stream.  Nothing here allocates or
 // synchronizes, and nothing is enqueued for a rejected call.
 #include <hip/hip_runtime.h>
@@ -23,15 +23,17 @@ bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
 
 // The cache's description; head_dim a multiple of 16 up to 256, pages of a
 // power of two tokens, every row starting on 16 bytes.
-qg_status check_cache(const qg_kv_cache* c, qg::CacheView* out)
+qg_status check_cache(const qg_kv_cache* c, qg::CacheView* out, qg::BlockView* blocks)
 {
     if (!c || !c->k || !c->v) return QG_ERR_INVALID_ARG;
-    if (c->dtype != QG_KV_BF16 && c->dtype != QG_KV_E4M3) return QG_ERR_UNSUPPORTED;
-    const bool e4m3 = c->dtype == QG_KV_E4M3;
+    if (c->dtype != QG_KV_BF16 && c->dtype != QG_KV_E4M3 && c->dtype != QG_KV_MXFP4) return QG_ERR_UNSUPPORTED;
+    const bool e4m3 = c->dtype == QG_KV_E4M3, mxfp4 = c->dtype == QG_KV_MXFP4;
+    if (mxfp4 && (!c->k_block_scale || !c->v_block_scale)) return QG_ERR_INVALID_ARG;
     if (e4m3 && (!c->k_scale || !c->v_scale)) return QG_ERR_INVALID_ARG;
     if (c->pages < 1 || c->pages > kMaxCount || c->kv_heads < 1 || c->page_size < 1 || c->head_dim < 1)
         return QG_ERR_INVALID_ARG;
     if (c->head_dim % 16 != 0 || c->head_dim > qg::kMaxHeadDim || c->kv_heads > 65535) return QG_ERR_UNSUPPORTED;
+    if (mxfp4 && c->head_dim % qg::kBlock != 0) return QG_ERR_UNSUPPORTED;
     if ((c->page_size & (c->page_size - 1)) != 0 || c->page_size > (1 << 20)) return QG_ERR_UNSUPPORTED;
     if (!stride_ok(c->page_stride) || !stride_ok(c->head_stride) || !stride_ok(c->slot_stride))
         return QG_ERR_INVALID_ARG;
@@ -39,13 +41,23 @@ qg_status check_cache(const qg_kv_cache* c, qg::CacheView* out)
     if ((c->page_size > 1 && c->slot_stride < c->head_dim) || (c->kv_heads > 1 && c->head_stride < c->head_dim) ||
         (c->pages > 1 && c->page_stride < c->head_dim))
         return QG_ERR_INVALID_ARG;
-    const int64_t unit = e4m3 ? 16 : 8;   // elements in 16 bytes
+    const int64_t unit = mxfp4 ? 32 : e4m3 ? 16 : 8;   // elements in 16 bytes
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride % unit || c->head_stride % unit ||
         c->slot_stride % unit)
         return QG_ERR_ALIGNMENT;
     if (e4m3 && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))) return QG_ERR_ALIGNMENT;
     qg::Dim dims[] = {{c->pages, c->page_stride}, {c->kv_heads, c->head_stride}, {c->page_size, c->slot_stride}};
     if (!qg::rows_disjoint(dims, c->head_dim)) return QG_ERR_INVALID_ARG;
+    out->mxfp4 = mxfp4;
+    *blocks = {};
+    if (mxfp4) {
+        const int64_t page = c->pages > 1 ? c->scale_page_stride : 0, head = c->kv_heads > 1 ? c->scale_head_stride : 0;
+        const int64_t slot = c->page_size > 1 ? c->scale_slot_stride : 0;
+        if (!stride_ok(page) || !stride_ok(head) || !stride_ok(slot)) return QG_ERR_INVALID_ARG;
+        qg::Dim rows[] = {{c->pages, page}, {c->kv_heads, head}, {c->page_size, slot}};
+        if (!qg::rows_disjoint(rows, c->head_dim / qg::kBlock)) return QG_ERR_INVALID_ARG;
+        *blocks = {c->k_block_scale, c->v_block_scale, page, head, slot};
+    }
     out->k = static_cast<uint8_t*>(c->k);
     out->v = static_cast<uint8_t*>(c->v);
     out->k_scale = e4m3 ? c->k_scale : nullptr;
@@ -119,7 +131,8 @@ qg_status qg_rope_append(const qg_kv_cache* cache, const qg_rope* rope, const vo
     if (tokens < 0 || tokens > kMaxCount || q_heads < 1) return QG_ERR_INVALID_ARG;
     if (q_heads > 65535 || (src_dtype != QG_SRC_F32 && src_dtype != QG_SRC_BF16)) return QG_ERR_UNSUPPORTED;
     qg::RopeParams p;
-    const qg_status st = check_cache(cache, &p.cache);
+    qg::BlockView blocks;
+    const qg_status st = check_cache(cache, &p.cache, &blocks);
     if (st != QG_OK) return st;
     // a dimension of one entry has no stride that matters
     if (tokens <= 1) q_token_stride = k_token_stride = v_token_stride = out_token_stride = 0;
@@ -166,13 +179,59 @@ qg_status qg_rope_append(const qg_kv_cache* cache, const qg_rope* rope, const vo
     p.wide = aligned(q, 16) && aligned(k, 16) && aligned(v, 16) && aligned(q_out, 16);
     for (int i = 0; i < 8; ++i) p.wide = p.wide && strides[i] % (i < 6 ? unit : 8) == 0;
     (void)hipGetLastError();  // clear a stale error so the check below is ours
-    return qg::launch_rope(p, static_cast<hipStream_t>(hip_stream)) == hipSuccess ? QG_OK : QG_ERR_HIP;
+    return qg::launch_rope(p, blocks, static_cast<hipStream_t>(hip_stream)) == hipSuccess ? QG_OK : QG_ERR_HIP;
+}
+
+qg_status qg_kv_read(const qg_kv_cache* cache, const int64_t* slots, void* k_out, void* v_out, int32_t out_dtype,
+                     int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                     int64_t tokens, void* hip_stream)
+{
+    if (!slots || (!k_out && !v_out)) return QG_ERR_INVALID_ARG;
+    if (tokens < 0 || tokens > kMaxCount) return QG_ERR_INVALID_ARG;
+    if (out_dtype != QG_SRC_F32 && out_dtype != QG_SRC_BF16) return QG_ERR_UNSUPPORTED;
+    qg::ReadParams p;
+    const qg_status st = check_cache(cache, &p.cache, &p.blocks);
+    if (st != QG_OK) return st;
+    const int64_t heads = p.cache.kv_heads, dim = p.cache.head_dim;
+    p.f32 = out_dtype == QG_SRC_F32;
+    p.wide = true;
+    const uintptr_t size = p.f32 ? 4 : 2;
+    if (!aligned(slots, 8)) return QG_ERR_ALIGNMENT;
+    struct Rows {
+        void* at;
+        int64_t* token;
+        int64_t* head;
+    };
+    for (const Rows& r : {Rows{k_out, &k_token_stride, &k_head_stride}, Rows{v_out, &v_token_stride, &v_head_stride}}) {
+        if (!r.at) continue;
+        // a dimension of one entry has no stride that matters
+        if (tokens <= 1) *r.token = 0;
+        if (heads == 1) *r.head = 0;
+        if (!stride_ok(*r.token) || !stride_ok(*r.head)) return QG_ERR_INVALID_ARG;
+        if (!aligned(r.at, size)) return QG_ERR_ALIGNMENT;
+        qg::Dim dims[] = {{tokens, *r.token}, {heads, *r.head}};
+        if (!qg::rows_disjoint(dims, dim)) return QG_ERR_INVALID_ARG;
+        const int64_t unit = 16 / int64_t(size);
+        p.wide = p.wide && aligned(r.at, 16) && *r.token % unit == 0 && *r.head % unit == 0;
+    }
+    if (tokens == 0) return QG_OK;
+    p.slots = slots;
+    p.k = k_out;
+    p.v = v_out;
+    p.k_token = k_token_stride;
+    p.k_head = k_head_stride;
+    p.v_token = v_token_stride;
+    p.v_head = v_head_stride;
+    p.tokens = tokens;
+    (void)hipGetLastError();
+    return qg::launch_read(p, static_cast<hipStream_t>(hip_stream)) == hipSuccess ? QG_OK : QG_ERR_HIP;
 }
 
 static qg_status check_attention_shape(const qg_kv_cache* cache, int64_t tokens, int32_t q_heads, int32_t seqs,
-                                       int64_t max_q, int64_t max_kv, qg::CacheView* view)
+                                       int64_t max_q, int64_t max_kv, qg::CacheView* view,
+                                       qg::BlockView* blocks)
 {
-    const qg_status st = check_cache(cache, view);
+    const qg_status st = check_cache(cache, view, blocks);
     if (st != QG_OK) return st;
     if (tokens < 0 || tokens > kMaxCount || seqs < 0 || max_q < 0 || max_q > kMaxCount || max_kv < 0 ||
         max_kv > kMaxCount || q_heads < 1 || q_heads % view->kv_heads != 0)
@@ -186,8 +245,9 @@ size_t qg_paged_attention_workspace_size(const qg_kv_cache* cache, int64_t token
                                          int64_t max_q, int64_t max_kv)
 {
     qg::CacheView view;
-    if (check_attention_shape(cache, tokens, q_heads, seqs, max_q, max_kv, &view) != QG_OK) return 0;
-    return qg::attention_workspace_bytes(view.e4m3, tokens, q_heads, view.kv_heads, view.head_dim, seqs, max_q, max_kv);
+    qg::BlockView blocks;
+    if (check_attention_shape(cache, tokens, q_heads, seqs, max_q, max_kv, &view, &blocks) != QG_OK) return 0;
+    return qg::attention_workspace_bytes(view, tokens, q_heads, seqs, max_q, max_kv);
 }
 
 qg_status qg_paged_attention(const qg_kv_cache* cache, const uint16_t* q_bf16, int64_t q_token_stride,
@@ -200,7 +260,7 @@ qg_status qg_paged_attention(const qg_kv_cache* cache, const uint16_t* q_bf16, i
 {
     if (!q_bf16 || !out_bf16 || !q_start || !kv_len || !page_table || !workspace) return QG_ERR_INVALID_ARG;
     qg::AttnParams p;
-    const qg_status st = check_attention_shape(cache, tokens, q_heads, seqs, max_q, max_kv, &p.cache);
+    const qg_status st = check_attention_shape(cache, tokens, q_heads, seqs, max_q, max_kv, &p.cache, &p.blocks);
     if (st != QG_OK) return st;
     // a dimension of one entry has no stride that matters
     if (tokens <= 1) q_token_stride = out_token_stride = lse_token_stride = 0;
@@ -221,8 +281,7 @@ qg_status qg_paged_attention(const qg_kv_cache* cache, const uint16_t* q_bf16, i
     qg::Dim dims[] = {{tokens, out_token_stride}, {q_heads, out_head_stride}};
     if (!qg::rows_disjoint(dims, p.cache.head_dim)) return QG_ERR_INVALID_ARG;
     if (tokens == 0 || seqs == 0 || max_q == 0) return QG_OK;
-    if (workspace_bytes < qg::attention_workspace_need(p.cache.e4m3, tokens, q_heads, p.cache.kv_heads, p.cache.head_dim,
-                                                       seqs, max_q, max_kv))
+    if (workspace_bytes < qg::attention_workspace_need(p.cache, tokens, q_heads, seqs, max_q, max_kv))
         return QG_ERR_INVALID_ARG;
     p.q = q_bf16;
     p.q_token = q_token_stride;

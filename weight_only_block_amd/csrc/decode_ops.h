@@ -1,6 +1,7 @@
 // Internal interface of the operators between a decode step's GEMV calls:
-// rotary positions with cache append (rope.hip), attention over the paged
-// cache (paged_attention.hip) and token sampling (sample.hip).
+// rotary positions with cache append (rope.hip, rope_mxfp4.hip), cached tokens
+// read back (kv_read.hip), attention over the paged cache (paged_attention.hip)
+// and token sampling (sample.hip).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stddef.h>
@@ -30,6 +31,14 @@ __device__ inline void fetch_arguments()
 }
 #endif
 
+#ifdef __HIP_DEVICE_COMPILE__
+// The scale that the 4-bit conversions take for a block's exponent byte: they
+// read its exponent bits alone, all set for NaN and none for 2^-127.
+__device__ __forceinline__ float block_scale(uint32_t b) { return __uint_as_float((b > 252 ? 255u : b) << 23); }
+#else
+__device__ inline float block_scale(uint32_t) { return 0.0f; }
+#endif
+
 constexpr int kMaxHeadDim = 256;
 constexpr int kMaxRotPairs = kMaxHeadDim / 2;
 
@@ -42,8 +51,17 @@ struct CacheView {
     int64_t page_stride, head_stride, slot_stride;
     int64_t pages;
     int32_t kv_heads, page_shift, head_dim;
-    bool e4m3;
+    bool e4m3, mxfp4;                          // mxfp4: codes, two elements a byte
 };
+
+// A 4-bit cache's exponent bytes (strides in bytes).
+struct BlockView {
+    uint8_t* k;
+    uint8_t* v;
+    int64_t page_stride, head_stride, slot_stride;
+};
+
+constexpr int kBlock = 32;        // dimensions that share an exponent byte
 
 struct RopeParams {
     CacheView cache;
@@ -64,7 +82,22 @@ struct RopeParams {
     uint64_t turns[kMaxRotPairs];   // turns per position, 64-bit binary fraction
 };
 
-hipError_t launch_rope(const RopeParams& p, hipStream_t s);
+hipError_t launch_rope(const RopeParams& p, const BlockView& blocks, hipStream_t s);
+hipError_t launch_rope_mxfp4(const RopeParams& p, const BlockView& blocks, hipStream_t s);   // at most 2^23 tokens
+
+struct ReadParams {
+    CacheView cache;
+    const int64_t* slots;
+    void* k;                // null: not wanted
+    void* v;
+    int64_t k_token, k_head, v_token, v_head;   // strides, elements
+    int64_t tokens;
+    bool f32;
+    bool wide;              // every row starts on 16 bytes
+    BlockView blocks;
+};
+
+hipError_t launch_read(const ReadParams& p, hipStream_t s);
 
 struct AttnParams {
     CacheView cache;
@@ -82,6 +115,7 @@ struct AttnParams {
     int32_t seqs, q_heads, group;
     float scale;
     void* workspace;
+    BlockView blocks;
 };
 
 // A sequence's new rows [q0, q0 + n) and cached keys.
@@ -102,10 +136,10 @@ __host__ __device__ inline Seq cut_seq(int start, int next, int kv, int tokens, 
 }
 
 // Of this shape; of this shape and every smaller one.
-size_t attention_workspace_need(bool e4m3, int64_t tokens, int q_heads, int kv_heads, int head_dim, int seqs,
-                                int64_t max_q, int64_t max_kv);
-size_t attention_workspace_bytes(bool e4m3, int64_t tokens, int q_heads, int kv_heads, int head_dim, int seqs,
-                                 int64_t max_q, int64_t max_kv);
+size_t attention_workspace_need(const CacheView& cache, int64_t tokens, int q_heads, int seqs, int64_t max_q,
+                                int64_t max_kv);
+size_t attention_workspace_bytes(const CacheView& cache, int64_t tokens, int q_heads, int seqs, int64_t max_q,
+                                 int64_t max_kv);
 hipError_t launch_attention(const AttnParams& p, hipStream_t s);
 
 struct SampleParams {

@@ -188,17 +188,27 @@ struct Args {
     float scale;
 };
 
+// A 4-bit cache has exponent bytes beside its codes (strides in bytes).
+struct BlockArgs : Args {
+    const uint8_t* k_block;
+    const uint8_t* v_block;
+    uint32_t block_page, block_head, block_slot;
+};
+
+enum Kind { kBf16, kE4m3, kMxfp4 };
+
 // x / group, exact while x * group is below 2^31: x is a row of a unit beside
 // the heads before its first, below 255 + group, and group below 2^15.
 __device__ __forceinline__ uint32_t by_group(const Args& p, uint32_t x) { return __umulhi(2 * x, p.by_group); }
 
 // One kernel shape.  DP: head dimension padded to a matrix-core multiple;
 // FULL: the head has all of it; SHARING: waves that share tiles, 0 for Split.
-template <int DP_, bool E4M3_, int SHARING, bool FULL_>
+template <int DP_, Kind KIND, int SHARING, bool FULL_>
 struct Shape {
     static constexpr int DP = DP_;
-    static constexpr bool E4M3 = E4M3_, SHARED = SHARING != 0, FULL = FULL_;
-    static constexpr int ES = E4M3 ? 1 : 2;
+    static constexpr bool E4M3 = KIND == kE4m3, MXFP4 = KIND == kMxfp4, SHARED = SHARING != 0, FULL = FULL_;
+    using Arguments = std::conditional_t<MXFP4, BlockArgs, Args>;
+    static constexpr int ES = E4M3 ? 1 : 2;                             // (4-bit tiles are bf16 in LDS)
     static constexpr int RB = (DP == 96 ? 128 : DP) * ES;               // bytes of a tile row
     // Waves.  Split: as many as leave a compute unit two work-groups or more,
     // so that one streams while another begins or ends a unit; with rows of 128
@@ -216,8 +226,12 @@ struct Shape {
     static constexpr int TILE = KT * RB;                                // bytes of K or of V
     static constexpr int RAW = SHARED ? KT / W : KT, ROWS = RAW < RPI ? RPI : RAW;   // rows a wave loads
     // tiles in LDS: two where two work-groups share a compute unit
-    static constexpr int STAGES = SHARED && (W == 8 || WAVES_PER_SIMD == 1) ? 4 : 2;
+    // (4-bit ones pass through registers, which hold the next tile)
+    static constexpr int STAGES = MXFP4 ? SHARED ? 2 : 1 : SHARED && (W == 8 || WAVES_PER_SIMD == 1) ? 4 : 2;
     static constexpr int LOADS = ROWS / RPI;                            // for K, and as many for V
+    // 4-bit: blocks of a row, those of K and V that a thread loads of its work-group's or its wave's tile
+    static constexpr int NB = DP / kBlock, BLOCK_THREADS = SHARED ? THREADS : 64;
+    static constexpr int BLOCKS_EACH = (2 * KT * NB + BLOCK_THREADS - 1) / BLOCK_THREADS;
     static constexpr int RING = STAGES * 2 * TILE * (SHARED ? 1 : W);   // stages of K and V
     static constexpr int OS = DP + 4;                                   // floats of a row in the joining buffer
     static constexpr int JOIN = SHARED ? 0 : W * M * OS * 4;
@@ -511,7 +525,7 @@ __device__ __forceinline__ void compute(State<S>& st, const uint8_t* kt, const u
 // The loads of one tile, and what the tile needs before use.
 template <class S>
 struct Loader {
-    const Args& p;
+    const typename S::Arguments& p;
     const int32_t* list;      // LDS: page ids from page `first_page` on, -1 outside the sequence or the cache
     int first_page;
     const int32_t* table;     // the sequence's row of the page table
@@ -521,6 +535,7 @@ struct Loader {
     int all_lo, all_hi;       // and that every row sees
     int64_t* poisoned;        // LDS
     int lane;
+    uint64_t kblock, vblock;  // 4-bit: exponent bytes of this kv head
 
     // Rows [row0, row0 + ROWS) of the tile, the wave's part; its K and V at
     // LDS offsets kt and vt, its first key k0.  True: it needs patch().
@@ -611,12 +626,90 @@ struct Loader {
     }
 };
 
+// A thread's part of a tile of a 4-bit cache, on its way through registers:
+// blocks x, x + BLOCK_THREADS, ... of the tile's K and then V, block by block
+// of a row and row by row.
+template <class S>
+struct Blocks {
+    u32x4 codes[S::BLOCKS_EACH];
+    uint32_t exponent[S::BLOCKS_EACH];
+    int page[S::BLOCKS_EACH];           // -1: outside the sequence or the cache
+
+    static constexpr int EACH = S::KT * S::NB;
+
+    __device__ __forceinline__ static bool none(const Loader<S>& ld, int x)
+    {
+        return (2 * EACH % S::BLOCK_THREADS != 0 && x >= 2 * EACH) || (!S::FULL && x % S::NB * kBlock >= ld.p.dim);
+    }
+
+    // Begins the loads of the tile whose first key is k0.
+    __device__ __forceinline__ void fetch(const Loader<S>& ld, int k0, int thread)
+    {
+        const int mask = (1 << ld.p.page_shift) - 1;
+#pragma unroll
+        for (int i = 0; i < S::BLOCKS_EACH; ++i) {
+            const int x = thread + i * S::BLOCK_THREADS;
+            codes[i] = u32x4{0, 0, 0, 0};
+            exponent[i] = 0;
+            page[i] = -1;
+            if (none(ld, x)) continue;
+            const int y = x % EACH, key = k0 + y / S::NB, b = y % S::NB;
+            page[i] = ld.list[(key >> ld.p.page_shift) - ld.first_page];
+            const uint64_t id = uint32_t(max(0, page[i])), slot = uint32_t(key & mask);
+            const bool v = x >= EACH;
+            const uint8_t* at = reinterpret_cast<const uint8_t*>((v ? ld.vbase : ld.kbase) + ((id * ld.p.page16 + slot * ld.p.slot16 + b) << 4));
+            const uint8_t* e = reinterpret_cast<const uint8_t*>((v ? ld.vblock : ld.kblock) + id * ld.p.block_page + slot * ld.p.block_slot + b);
+            codes[i] = *reinterpret_cast<const u32x4*>(at);
+            exponent[i] = *e;
+        }
+    }
+
+    // Writes them to the tiles in LDS as bf16, which holds every value.  Rows
+    // outside [lo, hi) hold another's data and become zeros; keys of a page
+    // outside the cache become NaN.  A value that is NaN at a key that only some
+    // rows see would be NaN in the others too: it becomes 0, and rows that see
+    // it get it back at the end (restore).
+    __device__ __forceinline__ void land(const Loader<S>& ld, uint8_t* kt, uint8_t* vt, int k0, int thread) const
+    {
+#pragma unroll
+        for (int i = 0; i < S::BLOCKS_EACH; ++i) {
+            const int x = thread + i * S::BLOCK_THREADS;
+            if (none(ld, x)) continue;
+            const int y = x % EACH, row = y / S::NB, key = k0 + row, b = y % S::NB;
+            const bool v = x >= EACH;
+            const bool outside = key < ld.lo || key >= ld.hi, lost = page[i] < 0;
+            uint32_t e = lost ? 255 : exponent[i];
+            u32x4 c = codes[i];
+            if (outside || (v && lost)) {
+                c = u32x4{0, 0, 0, 0};
+                e = 0;
+            } else if (v && e > 252 && (key < ld.all_lo || key >= ld.all_hi)) {
+                c = u32x4{0, 0, 0, 0};
+                e = 0;
+                *ld.poisoned = 1;
+            }
+            const float scale = block_scale(e);
+            const int swizzle = v ? S::v_swizzle(row) : S::k_swizzle(row);
+            uint8_t* to = (v ? vt : kt) + row * S::RB;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                union { u32x4 u; bf16x2 p[4]; } a;
+                a.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], scale, 0);
+                a.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], scale, 1);
+                a.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], scale, 2);
+                a.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], scale, 3);
+                *reinterpret_cast<u32x4*>(to + (((4 * b + j) ^ swizzle) << 4)) = a.u;
+            }
+        }
+    }
+};
+
 // Gives the lane's row the values that patch() took out, of keys [from, to),
 // each times its probability: infinity stays one, but for a probability of
 // zero, as in a tile that all rows see.  Split: a key is its own wave's alone;
 // tiles begin at `from`.
 template <class S>
-__device__ __forceinline__ void restore(State<S>& st, const Args& p, const Loader<S>& ld, int from, int to, float c, int wave)
+__device__ __forceinline__ void restore(State<S>& st, const typename S::Arguments& p, const Loader<S>& ld, int from, int to, float c, int wave)
 {
     const int mask = (1 << p.page_shift) - 1;
     const float ref = st.m == -INFINITY ? 0.0f : st.m;
@@ -626,6 +719,23 @@ __device__ __forceinline__ void restore(State<S>& st, const Args& p, const Loade
         if (!S::SHARED && (key - from) / S::KT % S::W != wave) continue;
         const int id = ld.table[key >> p.page_shift];
         if (id < 0 || id >= p.pages) continue;
+        if constexpr (S::MXFP4) {
+            // whole blocks of NaN, which no probability takes away
+            const uint8_t* e = reinterpret_cast<const uint8_t*>(ld.vblock + uint64_t(uint32_t(id)) * p.block_page +
+                                                                uint64_t(uint32_t(key & mask)) * p.block_slot);
+            const bool sees = key >= st.rlo && key < st.rhi;
+#pragma unroll 1
+            for (int d = 0; d < S::DB; ++d) {
+                if (!S::FULL && d * kBlock >= p.dim) break;
+                const bool nan = sees && e[d] > 252;
+#pragma unroll
+                for (int x = 0; x < S::DB; ++x)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (x == d && nan) st.o[x][i] = __builtin_nanf("");
+            }
+            continue;
+        }
         const uint64_t off = (uint64_t(uint32_t(id)) * p.page16 + uint64_t(uint32_t(key & mask)) * p.slot16) << 4;
         const uint8_t* krow = reinterpret_cast<const uint8_t*>(ld.kbase + off);
         const uint8_t* vrow = reinterpret_cast<const uint8_t*>(ld.vbase + off);
@@ -663,7 +773,7 @@ __device__ __forceinline__ void restore(State<S>& st, const Args& p, const Loade
 }
 
 template <class S>
-__global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kernel(Args p)
+__global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kernel(typename S::Arguments p)
 {
     extern __shared__ __align__(1024) uint8_t lds[];
     int32_t* list = reinterpret_cast<int32_t*>(lds + S::BUFFER);
@@ -672,7 +782,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
     Seq* seqs = reinterpret_cast<Seq*>(plan + 8);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-    fetch_arguments<sizeof(Args)>();
+    fetch_arguments<sizeof(p)>();
 
     // ---- the line of work: this run's part of it.  Each thread sums a run of
     // units: those of some sequences, or where sequences have many tiles and
@@ -854,12 +964,17 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
             }
         }
 
-        Loader<S> ld{p, list, 0, p.table + uint64_t(uint32_t(b)) * p.table_stride, 0, 0, 0, u.lo, u.hi, 0, u.first + 1, plan + 5, ulane};
+        Loader<S> ld{p, list, 0, p.table + uint64_t(uint32_t(b)) * p.table_stride, 0, 0, 0, u.lo, u.hi, 0, u.first + 1, plan + 5, ulane, 0, 0};
         if (p.window > 0) ld.all_lo = max(0, u.last - p.window + 1);
         ld.pages = int((uint32_t(s.kv) + (1u << p.page_shift) - 1) >> p.page_shift);
         const uint64_t head_bytes = uint64_t(uniform(int64_t(uint64_t(uint32_t(kvh)) * p.head16 << 4)));
         ld.kbase = reinterpret_cast<uint64_t>(p.k) + head_bytes;
         ld.vbase = reinterpret_cast<uint64_t>(p.v) + head_bytes;
+        if constexpr (S::MXFP4) {
+            const uint64_t head_blocks = uint64_t(uniform(int64_t(uint64_t(uint32_t(kvh)) * p.block_head)));
+            ld.kblock = reinterpret_cast<uint64_t>(p.k_block) + head_blocks;
+            ld.vblock = reinterpret_cast<uint64_t>(p.v_block) + head_blocks;
+        }
         if (threadIdx.x == 0) plan[5] = 0;
 
         // The scale's sign goes into the queries, so that the largest score
@@ -894,7 +1009,25 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
                 list[i] = id >= p.pages ? -1 : id;
             }
             __syncthreads();
-            if constexpr (S::SHARED) {
+            if constexpr (S::MXFP4) {
+                // the next tile's loads run beside this one's products
+                const int thread = S::SHARED ? opaque(threadIdx.x) : ulane;
+                const int k1 = S::SHARED ? start : start + wave * S::KT;
+                const uint32_t ring = S::SHARED ? 0 : wave * 2 * S::TILE;
+                Blocks<S> next;
+                next.fetch(ld, k1, thread);
+                for (int i = 0; i < n; ++i) {
+                    const int k0 = k1 + i * S::STEP;
+                    const uint32_t kt = ring + (i % S::STAGES) * 2 * S::TILE;
+                    next.land(ld, lds + kt, lds + kt + S::TILE, k0, thread);
+                    if (i + 1 < n) next.fetch(ld, k0 + S::STEP, thread);
+                    wait_lds();
+                    if (S::SHARED) __builtin_amdgcn_s_barrier();
+                    asm volatile("" ::: "memory");
+                    run_tile(lds0 + kt, k0);
+                    asm volatile("" ::: "memory");
+                }
+            } else if constexpr (S::SHARED) {
                 const int row0 = wave * S::ROWS;
                 const bool loads = row0 < S::KT;
                 uint32_t flags = 0;
@@ -1173,7 +1306,7 @@ size_t bytes(int64_t tokens, int group, int kv_heads, int seqs, int64_t max_kv)
 }
 
 template <class S>
-hipError_t run(const AttnParams& a, Args p, hipStream_t s)
+hipError_t run(const AttnParams& a, const BlockArgs& all, hipStream_t s)
 {
     const int64_t grid = workers<S>(a.tokens, a.group, a.cache.kv_heads, a.seqs, a.max_kv);
     static const hipError_t attr = [] {
@@ -1183,6 +1316,7 @@ hipError_t run(const AttnParams& a, Args p, hipStream_t s)
         return e;
     }();
     if (attr != hipSuccess && S::LDS > 64 * 1024) return attr;
+    const typename S::Arguments p = all;
     hipLaunchKernelGGL((attention_kernel<S>), dim3(unsigned(grid)), dim3(S::THREADS), S::LDS, s, p);
     return hipGetLastError();
 }
@@ -1198,10 +1332,11 @@ int sharing(int64_t tokens, int64_t max_q, int group, int seqs)
 
 // Calls f with the shape for a cache and a call's rows.
 template <class F>
-auto with_shape(bool e4m3, int dim, int waves, F f)
+auto with_shape(const CacheView& cache, int waves, F f)
 {
+    const int dim = cache.head_dim;
     const auto by_dim = [&](auto e, auto w) {
-        constexpr bool E = decltype(e)::value;
+        constexpr Kind E = decltype(e)::value;
         constexpr int W = decltype(w)::value, W256 = W == 8 ? 4 : W;   // (a wave of 256 dimensions takes a whole SIMD's registers)
         if (dim == 64) return f(Shape<64, E, W, true>());
         if (dim == 128) return f(Shape<128, E, W, true>());
@@ -1211,33 +1346,36 @@ auto with_shape(bool e4m3, int dim, int waves, F f)
         if (dim <= 128) return f(Shape<128, E, W, false>());
         return f(Shape<256, E, W256, false>());
     };
-    const auto by_type = [&](auto w) { return e4m3 ? by_dim(std::true_type(), w) : by_dim(std::false_type(), w); };
+    const auto by_type = [&](auto w) {
+        if (cache.mxfp4) return by_dim(std::integral_constant<Kind, kMxfp4>(), w);
+        return cache.e4m3 ? by_dim(std::integral_constant<Kind, kE4m3>(), w) : by_dim(std::integral_constant<Kind, kBf16>(), w);
+    };
     if (waves == 0) return by_type(std::integral_constant<int, 0>());
     return waves == 4 ? by_type(std::integral_constant<int, 4>()) : by_type(std::integral_constant<int, 8>());
 }
 
 }  // namespace
 
-size_t attention_workspace_need(bool e4m3, int64_t tokens, int q_heads, int kv_heads, int head_dim, int seqs,
-                                int64_t max_q, int64_t max_kv)
+size_t attention_workspace_need(const CacheView& cache, int64_t tokens, int q_heads, int seqs, int64_t max_q,
+                                int64_t max_kv)
 {
-    const int group = q_heads / kv_heads;
-    return with_shape(e4m3, head_dim, sharing(tokens, max_q < tokens ? max_q : tokens, group, seqs), [&](auto shape) {
-        return bytes<decltype(shape)>(tokens, group, kv_heads, seqs, max_kv);
+    const int group = q_heads / cache.kv_heads;
+    return with_shape(cache, sharing(tokens, max_q < tokens ? max_q : tokens, group, seqs), [&](auto shape) {
+        return bytes<decltype(shape)>(tokens, group, cache.kv_heads, seqs, max_kv);
     });
 }
 
 // The largest need of any shape within the bounds: each kernel shape's grows
 // with all of them, and smaller calls may take another one than the largest.
-size_t attention_workspace_bytes(bool e4m3, int64_t tokens, int q_heads, int kv_heads, int head_dim, int seqs,
-                                 int64_t max_q, int64_t max_kv)
+size_t attention_workspace_bytes(const CacheView& cache, int64_t tokens, int q_heads, int seqs, int64_t max_q,
+                                 int64_t max_kv)
 {
-    const int group = q_heads / kv_heads;
+    const int group = q_heads / cache.kv_heads;
     size_t most = 0;
     for (int waves : {0, 4, 8}) {
         if (waves > sharing(tokens, max_q < tokens ? max_q : tokens, group, 1)) break;
-        const size_t n = with_shape(e4m3, head_dim, waves, [&](auto shape) {
-            return bytes<decltype(shape)>(tokens, group, kv_heads, seqs, max_kv);
+        const size_t n = with_shape(cache, waves, [&](auto shape) {
+            return bytes<decltype(shape)>(tokens, group, cache.kv_heads, seqs, max_kv);
         });
         if (n > most) most = n;
     }
@@ -1246,9 +1384,9 @@ size_t attention_workspace_bytes(bool e4m3, int64_t tokens, int q_heads, int kv_
 
 hipError_t launch_attention(const AttnParams& a, hipStream_t s)
 {
-    const int unit = a.cache.e4m3 ? 16 : 8;   // elements in 16 bytes
+    const int unit = a.cache.mxfp4 ? 32 : a.cache.e4m3 ? 16 : 8;   // elements in 16 bytes
     const int64_t cap = a.table_cols << a.cache.page_shift;
-    Args p;
+    BlockArgs p;
     p.k = a.cache.k;
     p.v = a.cache.v;
     p.k_scale = a.cache.k_scale;
@@ -1281,7 +1419,12 @@ hipError_t launch_attention(const AttnParams& a, hipStream_t s)
     p.group = a.group;
     p.by_group = uint32_t(((uint64_t(1) << 31) + a.group - 1) / a.group);
     p.scale = a.scale;
-    return with_shape(a.cache.e4m3, a.cache.head_dim, sharing(a.tokens, a.max_q, a.group, a.seqs),
+    p.k_block = a.blocks.k;
+    p.v_block = a.blocks.v;
+    p.block_page = uint32_t(a.blocks.page_stride);
+    p.block_head = uint32_t(a.blocks.head_stride);
+    p.block_slot = uint32_t(a.blocks.slot_stride);
+    return with_shape(a.cache, sharing(a.tokens, a.max_q, a.group, a.seqs),
                       [&](auto shape) { return run<decltype(shape)>(a, p, s); });
 }
 

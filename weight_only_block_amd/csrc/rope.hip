@@ -210,8 +210,9 @@ void launch_wide(const RopeParams& p, dim3 grid, hipStream_t s)
 
 }  // namespace
 
-static hipError_t launch_tokens(const RopeParams& p, hipStream_t s)
+static hipError_t launch_tokens(const RopeParams& p, const BlockView& blocks, hipStream_t s)
 {
+    if (p.cache.mxfp4) return launch_rope_mxfp4(p, blocks, s);
     if (!p.wide || p.rot_dim % 8 != 0) {
         hipLaunchKernelGGL(rope_append_narrow, dim3(unsigned(p.tokens)), dim3(256), 0, s, p);
         return hipGetLastError();
@@ -233,10 +234,10 @@ static hipError_t launch_tokens(const RopeParams& p, hipStream_t s)
 
 // A grid has fewer than 2^32 threads (more are dropped without an error), and
 // a token takes 256: more tokens go in several launches.
-hipError_t launch_rope(const RopeParams& p, hipStream_t s)
+hipError_t launch_rope(const RopeParams& p, const BlockView& blocks, hipStream_t s)
 {
     constexpr int64_t kMost = int64_t(1) << 23;
-    if (p.tokens <= kMost) return launch_tokens(p, s);
+    if (p.tokens <= kMost) return launch_tokens(p, blocks, s);
     const int64_t size = p.f32 ? 4 : 2;
     const auto on = [&](const void* x, int64_t elements) { return static_cast<const uint8_t*>(x) + elements * size; };
     for (int64_t t = 0; t < p.tokens; t += kMost) {
@@ -248,7 +249,7 @@ hipError_t launch_rope(const RopeParams& p, hipStream_t s)
         part.pos += t;
         part.slots += t;
         part.tokens = p.tokens - t < kMost ? p.tokens - t : kMost;
-        const hipError_t e = launch_tokens(part, s);
+        const hipError_t e = launch_tokens(part, blocks, s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

@@ -36,7 +36,7 @@ FMT_Q8G128_MMA = 9
 FMT_Q8PC_MMA = 10
 FMT_Q4G32_MMA = 11
 
-KV_BF16, KV_E4M3 = 0, 1
+KV_BF16, KV_E4M3, KV_MXFP4 = 0, 1, 3
 SRC_F32, SRC_BF16 = 0, 1
 ROPE_PLAIN, ROPE_LINEAR, ROPE_YARN = 0, 1, 2
 
@@ -47,7 +47,9 @@ class _CacheStruct(ctypes.Structure):
     """qg_kv_cache."""
     _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
                 + [(n, ctypes.c_int64) for n in ("pages", "page_stride", "head_stride", "slot_stride")]
-                + [(n, ctypes.c_int32) for n in ("kv_heads", "page_size", "head_dim", "dtype")])
+                + [(n, ctypes.c_int32) for n in ("kv_heads", "page_size", "head_dim", "dtype")]
+                + [(n, ctypes.c_void_p) for n in ("k_block_scale", "v_block_scale")]
+                + [(n, ctypes.c_int64) for n in ("scale_page_stride", "scale_head_stride", "scale_slot_stride")])
 
 
 class _RopeStruct(ctypes.Structure):
@@ -123,6 +125,7 @@ def lib() -> ctypes.CDLL:
             "qg_argmax_f32": ([p, i64, i64, i64, p, p, sz, p], st),
             "qg_rope_init": ([p, i32, i32, f64, i32, f64, i64, f64, f64, f64], st),
             "qg_rope_append": ([p, p, p, p, p, i32] + [i64] * 6 + [p, p, p, i64, i64, i64, i32, p], st),
+            "qg_kv_read": ([p, p, p, p, i32, i64, i64, i64, i64, i64, p], st),
             "qg_paged_attention_workspace_size": ([p, i64, i32, i32, i64, i64], sz),
             "qg_paged_attention": ([p, p, i64, i64, p, i64, i64, p, i64, p, p, p, i64, i64, i64, i32, i32, i64, i64,
                                     ctypes.c_float, i64, p, sz, p], st),
@@ -687,34 +690,54 @@ class KVCache:
     k, v: device bfloat16 or float8_e4m3fn tensors [page][kv head][slot][dim]
     (any strides with the dimension innermost, the same for both); k_scale,
     v_scale: device float32 [kv heads], for float8 only.  A token's slot number
-    is page * page_size + slot.  Holds references to the tensors."""
+    is page * page_size + slot.  Holds references to the tensors.
+
+    For 4 bits, k and v are uint8 (or float4_e2m1fn_x2) with dim / 2 bytes a
+    row, the even dimension in the low half, and k_scale, v_scale uint8 (or
+    float8_e8m0fnu) [page][kv head][slot][dim / 32], any strides, the same for
+    both: the exponent byte of each block of 32 dimensions (KV_MXFP4)."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         where = "KVCache"
-        kinds = {"bfloat16": KV_BF16, "float8_e4m3fn": KV_E4M3}
-        kind = str(k.dtype).replace("torch.", "")
-        if kind not in kinds or v.dtype != k.dtype:
-            raise QGError(QG_ERR_INVALID_ARG, where + ": k and v must both be bfloat16 or float8_e4m3fn")
+        kinds = {"bfloat16": KV_BF16, "float8_e4m3fn": KV_E4M3, "uint8": KV_MXFP4, "float4_e2m1fn_x2": KV_MXFP4}
+        kind = kinds.get(str(k.dtype).replace("torch.", ""))
+        if kind is None or v.dtype != k.dtype:
+            raise QGError(QG_ERR_INVALID_ARG, where + ": k and v must both be bfloat16, float8_e4m3fn or uint8 (4-bit codes)")
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1 or k.numel() == 0:
             raise QGError(QG_ERR_INVALID_ARG, where + ": k and v must be [page][kv head][slot][dim] of one shape and "
                           "strides, the dimension contiguous")
         self.k, self.v = k, v
         pages, heads, size, dim = k.shape
-        if kinds[kind] == KV_E4M3:
+        each = 2 if kind == KV_MXFP4 else 1                 # elements of a tensor entry
+        dim *= each
+        blocks = (None, None, 0, 0, 0)
+        if kind == KV_E4M3:
             if k_scale is None or v_scale is None:
                 raise QGError(QG_ERR_INVALID_ARG, where + ": a float8 cache needs k_scale and v_scale")
             for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
                 _need(t, where, name, _F32, heads)
                 if t.dim() != 1 or t.numel() != heads or not t.is_contiguous():
                     raise QGError(QG_ERR_INVALID_ARG, "%s: %s must be contiguous [kv heads]" % (where, name))
+        elif kind == KV_MXFP4:
+            if dim % 32:
+                raise QGError(QG_ERR_UNSUPPORTED, "%s: a 4-bit cache of %d dimensions, needs a multiple of 32" % (where, dim))
+            shape = (pages, heads, size, dim // 32)
+            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if t is None or str(t.dtype) not in ("torch.uint8", "torch.float8_e8m0fnu") or t.shape != shape or \
+                        (t.stride(3) != 1 and shape[3] > 1) or t.stride() != k_scale.stride():
+                    raise QGError(QG_ERR_INVALID_ARG, "%s: a 4-bit cache needs %s, uint8 or float8_e8m0fnu %s, the last "
+                                  "dimension contiguous, strides the same for both" % (where, name, shape))
+            blocks = (k_scale.data_ptr(), v_scale.data_ptr()) + tuple(_step(k_scale, i) for i in range(3))
         else:
             k_scale = v_scale = None
         _on_gpu(where, k=k, v=v, k_scale=k_scale, v_scale=v_scale)
         _one_device(where, k, v, k_scale, v_scale)
         self.k_scale, self.v_scale = k_scale, v_scale
         self.kv_heads, self.page_size, self.head_dim = heads, size, dim
-        self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), pages, _step(k, 0),
-                                    _step(k, 1), _step(k, 2), heads, size, dim, kinds[kind])
+        per_head = kind == KV_E4M3
+        self._struct = _CacheStruct(k.data_ptr(), v.data_ptr(), _ptr(k_scale) if per_head else None,
+                                    _ptr(v_scale) if per_head else None, pages, each * _step(k, 0), each * _step(k, 1),
+                                    each * _step(k, 2), heads, size, dim, kind, *blocks)
         self._ref = ctypes.addressof(self._struct)
         self.device = k.get_device()
 
@@ -843,6 +866,32 @@ def rope_append(cache: KVCache, rope: Rope, q, k, v, pos, slots, q_out, stream=N
                               SRC_F32 if kind == dt.f32 else SRC_BF16, sq[0], sq[1], sk[0], sk[1],
                               sv[0], sv[1], pos.data_ptr(), slots.data_ptr(), q_out.data_ptr(), so[0], so[1], tokens,
                               heads, _stream_of(stream, dev))
+    if check and st:
+        _check(st, where)
+    return st
+
+
+def kv_read(cache: KVCache, slots, k_out=None, v_out=None, stream=None, check=True):
+    """Reads the cached keys and values at slots (device int64 [tokens]) back
+    into k_out and v_out, device float32 or bfloat16 [tokens][kv heads][dim] of
+    any token and head strides, either one None.  A slot outside the cache
+    leaves its rows as they were."""
+    where = "qg_kv_read"
+    dt = _DT or _dtypes()
+    first = v_out if k_out is None else k_out
+    if first is None or slots.dim() != 1:
+        raise QGError(QG_ERR_INVALID_ARG, where + ": needs k_out or v_out, and slots [tokens]")
+    dev = cache.device
+    tokens = slots.shape[0]
+    kind = (first.dtype,) if first.dtype in dt.src else dt.src
+    rows = (tokens, cache.kv_heads, cache.head_dim)
+    _fits(slots, where, "slots", dt.i64, (tokens,), dev)
+    sk = (0, 0) if k_out is None else _fits(k_out, where, "k_out", kind, rows, dev)
+    sv = (0, 0) if v_out is None else _fits(v_out, where, "v_out", kind, rows, dev)
+    if tokens == 0:
+        return QG_OK
+    st = lib().qg_kv_read(cache._ref, slots.data_ptr(), _ptr(k_out), _ptr(v_out), SRC_F32 if kind == dt.f32 else SRC_BF16,
+                          sk[0], sk[1], sv[0], sv[1], tokens, _stream_of(stream, dev))
     if check and st:
         _check(st, where)
     return st
