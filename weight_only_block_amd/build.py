@@ -32,7 +32,7 @@ def _run(cmd):
 
 HIP_SOURCES = ["kern_q8g64.hip", "kern_q4g32.hip", "kern_q8g128.hip", "kern_q8pc.hip",
                "kern_q4g32_swiglu.hip", "kern_argmax_epi.hip", "kern_mma.hip", "argmax.hip", "read_stream.hip",
-               "rope.hip", "rope_mxfp4.hip", "kv_read.hip", "paged_attention.hip", "sample.hip", "launch.hip",
+               "rope.hip", "rope_mxfp4.hip", "kv_read.hip", "paged_attention.hip", "paged_attention_few.hip", "sample.hip", "launch.hip",
                "abi.cpp", "abi_decode.cpp"]
 HOST_SOURCES = ["qpack.cpp"]
 

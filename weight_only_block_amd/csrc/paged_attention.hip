@@ -42,40 +42,22 @@
 
 #include <type_traits>
 
+#include "attention_common.h"
 #include "decode_ops.h"
 
 namespace qg {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kAhead = 4;                  // LDS reads ahead of their matrix products
-constexpr float kRaise = 8.0f;             // log2 by which a score may pass the reference
 constexpr int kListPages = 1024;           // page ids of a run's segment, in LDS
 constexpr int kListSeqs = 128;             // sequences whose lengths are kept in LDS
-constexpr int kComputeUnits = 256;
 // Rows a sequence (tokens x group) from which eight waves share tiles in place
 // of four: 256 rows to a tile halve its reads, but a unit's beginning and end
 // cost more.  4099 tokens over 12301 keys (16396 rows): 735 us with four, 655
 // with eight; 2048 over 8192: 262 and 250; 512 over 8192: 91 both; 128 over
 // 4096: 39 and 46.
 constexpr int64_t kManyRows = 2048;
-// Counts of arrived parts come first in the workspace, in every shape as many
-// bytes: calls of other shapes leave them alone.
-constexpr size_t kCounterBytes = 4096;
-constexpr int32_t kMaxWindow = 1 << 30;    // no shorter than the longest sequence
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef int i32x2 __attribute__((ext_vector_type(2)));
-typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
 
 __device__ __forceinline__ uint32_t lds_offset(const void* p)
 {
@@ -100,107 +82,6 @@ __device__ __forceinline__ void load_lds(uint32_t lds, uint64_t address)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(address) : "memory");
 }
-template <int N>
-__device__ __forceinline__ void wait_loads()   // all but the last N
-{
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
-{
-    bf16x2 v;
-    v[0] = (__bf16)a;
-    v[1] = (__bf16)b;
-    return __builtin_bit_cast(uint32_t, v);
-}
-
-// The largest, and the sum, of a lane's value and that of the wave's other half.
-__device__ __forceinline__ float max_halves(float x)
-{
-    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
-}
-__device__ __forceinline__ float sum_halves(float x)
-{
-    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return __uint_as_float(s[0]) + __uint_as_float(s[1]);
-}
-
-// Partial sums cross work-groups on different XCDs: device-scope accesses.
-__device__ __forceinline__ void put2(float* p, float a, float b)
-{
-    const uint64_t v = uint64_t(__float_as_uint(a)) | uint64_t(__float_as_uint(b)) << 32;
-    __hip_atomic_store(reinterpret_cast<uint64_t*>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ void get2(const float* p, float* a, float* b)
-{
-    const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    *a = __uint_as_float(uint32_t(v));
-    *b = __uint_as_float(uint32_t(v >> 32));
-}
-
-// A value the compiler knows nothing of.  Lane numbers pass through it where a
-// part of the kernel begins: what depends on them is then worked out there,
-// not all together ahead of the loop over units, where hundreds of
-// instructions, each fetched from a cold cache, stood before the first load.
-__device__ __forceinline__ int opaque(int x)
-{
-    asm volatile("" : "+v"(x));
-    return x;
-}
-
-// a / b for a below 2^52, b > 0.
-__device__ __forceinline__ int64_t divide(int64_t a, int64_t b)
-{
-    int64_t q = int64_t(double(a) * __builtin_amdgcn_rcp(double(b)));   // off by a little
-    while (q * b > a) --q;
-    while ((q + 1) * b <= a) ++q;
-    return q;
-}
-
-// The same value in every lane, in scalar registers.
-__device__ __forceinline__ int64_t uniform(int64_t x)
-{
-    const uint32_t lo = uint32_t(__builtin_amdgcn_readfirstlane(int(x)));
-    const uint32_t hi = uint32_t(__builtin_amdgcn_readfirstlane(int(x >> 32)));
-    return int64_t(uint64_t(hi) << 32 | lo);
-}
-
-// The kernel's arguments, strides and sizes in 32 bits (few scalar registers).
-struct Args {
-    const uint8_t* k;
-    const uint8_t* v;
-    const float* k_scale;
-    const float* v_scale;
-    const uint16_t* q;
-    uint16_t* out;
-    float* lse;
-    const int32_t* q_start;
-    const int32_t* kv_len;
-    const int32_t* table;
-    uint8_t* workspace;
-    uint32_t page16, head16, slot16;          // cache strides in 16 bytes
-    uint32_t q_token, q_head, o_token, o_head, lse_token, table_stride;
-    int32_t pages, kv_heads, page_shift, dim;
-    int32_t tokens, max_q, cap, window, seqs; // cap: keys a sequence may have; window 0: none
-    int32_t group;
-    uint32_t by_group;                        // ceil(2^31 / group)
-    float scale;
-};
-
-// A 4-bit cache has exponent bytes beside its codes (strides in bytes).
-struct BlockArgs : Args {
-    const uint8_t* k_block;
-    const uint8_t* v_block;
-    uint32_t block_page, block_head, block_slot;
-};
-
-enum Kind { kBf16, kE4m3, kMxfp4 };
-
-// x / group, exact while x * group is below 2^31: x is a row of a unit beside
-// the heads before its first, below 255 + group, and group below 2^15.
-__device__ __forceinline__ uint32_t by_group(const Args& p, uint32_t x) { return __umulhi(2 * x, p.by_group); }
 
 // One kernel shape.  DP: head dimension padded to a matrix-core multiple;
 // FULL: the head has all of it; SHARING: waves that share tiles, 0 for Split.
@@ -208,7 +89,6 @@ template <int DP_, Kind KIND, int SHARING, bool FULL_>
 struct Shape {
     static constexpr int DP = DP_;
     static constexpr bool E4M3 = KIND == kE4m3, MXFP4 = KIND == kMxfp4, SHARED = SHARING != 0, FULL = FULL_;
-    static constexpr bool NARROW = false;
     using Arguments = std::conditional_t<MXFP4, BlockArgs, Args>;
     static constexpr int ES = E4M3 ? 1 : 2;                             // (4-bit tiles are bf16 in LDS)
     static constexpr int RB = (DP == 96 ? 128 : DP) * ES;               // bytes of a tile row
@@ -238,8 +118,7 @@ struct Shape {
     static constexpr int OS = DP + 4;                                   // floats of a row in the joining buffer
     static constexpr int JOIN = SHARED ? 0 : W * M * OS * 4;
     static constexpr int BUFFER = RING > JOIN ? RING : JOIN;
-    static constexpr int LIST = kListPages;
-    static constexpr int LDS = BUFFER + LIST * 4 + 2 * W * 32 * 4 + 64 + kListSeqs * 12;
+    static constexpr int LDS = BUFFER + kListPages * 4 + 2 * W * 32 * 4 + 64 + kListSeqs * 12;
     // work-groups that a compute unit holds (160 KB of LDS, two waves of up to
     // 256 registers a SIMD or one of 512)
     static constexpr int BY_LDS = 160 * 1024 / LDS, BY_WAVES = 4 * WAVES_PER_SIMD / W;
@@ -249,7 +128,6 @@ struct Shape {
     static constexpr int LEAST = SHARED ? 4 : 2;
     static constexpr int EXTRA = SHARED ? 5 : 3;
     static constexpr float JOINED = SHARED ? 1.0f : 0.25f;               // what joining a part costs
-    static constexpr int PARTS = 16;                                    // whose loads are in flight together
     static constexpr int SLOT = SHARED ? W * (DP * 32 + 128) : M * DP + 2 * M;   // floats of a partial result
     static constexpr int STEPS = DP / 16;                               // products along the dimension
     static constexpr int DB = DP / 32;
@@ -268,48 +146,6 @@ struct Shape {
                                                           : (row & 3) << 1 | ((row >> 3) & 1) << 3;
     }
 };
-
-// The shape of `Split` over a 4-bit cache: 32 T dimensions, 16 R rows a unit.
-template <int T_, int R_>
-struct NarrowShape {
-    static constexpr int T = T_, R = R_, DP = 32 * T, DB = T;
-    static constexpr bool E4M3 = false, MXFP4 = true, SHARED = false, FULL = true, NARROW = true;
-    using Arguments = BlockArgs;
-    static constexpr int RB = T <= 2 ? 64 * T : T <= 4 ? 256 : 512;     // bytes of a row of V in LDS, a power of two
-    static constexpr int W = 4, THREADS = 64 * W;
-    static constexpr int M = 16 * R;
-    static constexpr int KT = 32, STEP = KT * W;
-    static constexpr int TILE = KT * RB;                                // of V, bf16
-    // exponent bytes that a lane's 8 T dimensions of a key reach into
-    static constexpr int NS = T == 7 ? 3 : T == 3 || T >= 5 ? 2 : 1;
-    static constexpr int REGISTERS = 8 * T * R + 4 * T * R + 8 * T + 8 * NS + 56;
-    static constexpr int WAVES_PER_SIMD = REGISTERS <= 128 ? 4 : REGISTERS <= 168 ? 3 : REGISTERS <= 256 ? 2 : 1;
-    static constexpr int OS = DP + 4;                                   // floats of a row in the joining buffer
-    static constexpr int RING = W * TILE, JOIN = W * M * OS * 4;
-    static constexpr int BUFFER = RING > JOIN ? RING : JOIN;
-    static constexpr int LIST = kListPages / 2;
-    static constexpr int LDS = BUFFER + LIST * 4 + 2 * W * 32 * 4 + 64 + kListSeqs * 12;
-    static constexpr int BY_LDS = 160 * 1024 / LDS, BY_WAVES = 4 * WAVES_PER_SIMD / W;
-    static constexpr int PER_CU = BY_LDS < BY_WAVES ? BY_LDS : BY_WAVES;
-    static constexpr int LEAST = 2, EXTRA = 3, PARTS = 8;
-    static constexpr float JOINED = 0.25f;
-    static constexpr int SLOT = M * DP + 2 * M;
-
-    // The chunk of 8 dimensions is moved so that 16 keys of one chunk (what a
-    // wave's quarter writes) and 8 keys of two neighbours (what a half reads)
-    // lie in different banks of 256 bytes.
-    static __device__ __forceinline__ int swizzle(int key)
-    {
-        if (T == 1) return ((key >> 2) & 1) << 1 | ((key >> 3) & 1);
-        if (T == 2) return ((key >> 1) & 3) << 1 | ((key >> 3) & 1);
-        return (key & 7) << 1 | ((key >> 3) & 1);
-    }
-};
-
-__device__ __forceinline__ Seq load_seq(const Args& p, int b)
-{
-    return cut_seq(p.q_start[b], p.q_start[b + 1], p.kv_len[b], p.tokens, p.max_q, p.cap);
-}
 
 // From LDS where all sequences fit.
 __device__ __forceinline__ Seq get_seq(const Args& p, const Seq* seqs, int b)
@@ -698,10 +534,11 @@ struct Blocks {
             page[i] = ld.list[(key >> ld.p.page_shift) - ld.first_page];
             const uint64_t id = uint32_t(max(0, page[i])), slot = uint32_t(key & mask);
             const bool v = x >= EACH;
-            const uint8_t* at = reinterpret_cast<const uint8_t*>((v ? ld.vbase : ld.kbase) + ((id * ld.p.page16 + slot * ld.p.slot16 + b) << 4));
-            const uint8_t* e = reinterpret_cast<const uint8_t*>((v ? ld.vblock : ld.kblock) + id * ld.p.block_page + slot * ld.p.block_slot + b);
-            codes[i] = *reinterpret_cast<const u32x4*>(at);
-            exponent[i] = *e;
+            // (a generic pointer would make flat loads, waited for with those of LDS)
+            typedef __attribute__((address_space(1))) const u32x4* codes_ptr;
+            typedef __attribute__((address_space(1))) const uint8_t* exponent_ptr;
+            codes[i] = *codes_ptr((v ? ld.vbase : ld.kbase) + ((id * ld.p.page16 + slot * ld.p.slot16 + b) << 4));
+            exponent[i] = *exponent_ptr((v ? ld.vblock : ld.kblock) + id * ld.p.block_page + slot * ld.p.block_slot + b);
         }
     }
 
@@ -744,254 +581,6 @@ struct Blocks {
         }
     }
 };
-
-// ---- 4-bit keys and few rows (NarrowShape).  S^T = K Q^T and O^T = V^T P^T by
-// 16x16x32 products.  Lane l holds of key l % 16 the 8 T dimensions from 8 T
-// (l / 16) on, as they come from memory: four codes a byte pair, a step of eight
-// a register, which the conversion to bf16 scales, so keys go to the matrix
-// cores without LDS.  Values have to lie key by key in a lane: they are written
-// to LDS as bf16 rows and read back through the transposing reads, in the order
-// of keys that the scores' lanes have (two tiles' keys 4 g .. 4 g + 3).
-template <class S>
-struct NarrowState {
-    f32x4 o[S::R][2 * S::T];
-    bf16x8 q[S::R][S::T];
-    float m[S::R], l[S::R];    // reference; this quarter's share of the sum
-    int rlo[S::R], rhi[S::R];  // keys the lane's rows see
-};
-
-// Two tiles of 16 keys of K and of V on their way through registers.
-template <class S>
-struct NarrowTile {
-    uint32_t k[2][S::T], v[2][S::T];
-    uint32_t ke[2][S::NS], ve[2][S::NS];
-    int page[2];               // of the lane's key: -1 outside the sequence or the cache
-
-    template <int N>
-    __device__ __forceinline__ static void load_words(uint32_t* to, const uint8_t* at)
-    {
-        // rows begin on 16 bytes, a lane's part of them on 4
-        typedef uint32_t words __attribute__((ext_vector_type(4), aligned(4)));
-        typedef uint32_t three __attribute__((ext_vector_type(3), aligned(4)));
-        typedef uint32_t two __attribute__((ext_vector_type(2), aligned(4)));
-        constexpr int n = N >= 4 ? 4 : N;
-        if constexpr (n == 4) {
-            const words x = __builtin_nontemporal_load(reinterpret_cast<const words*>(at));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) to[i] = x[i];
-        } else if constexpr (n == 3) {
-            const three x = __builtin_nontemporal_load(reinterpret_cast<const three*>(at));
-#pragma unroll
-            for (int i = 0; i < 3; ++i) to[i] = x[i];
-        } else if constexpr (n == 2) {
-            const two x = __builtin_nontemporal_load(reinterpret_cast<const two*>(at));
-            to[0] = x[0], to[1] = x[1];
-        } else {
-            to[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(at));
-        }
-        if constexpr (N > 4) load_words<N - 4>(to + 4, at + 16);
-    }
-
-    // Begins the loads of keys [k0, k0 + 32).
-    __device__ __forceinline__ void fetch(const Loader<S>& ld, int k0, int lane)
-    {
-        const int col = lane & 15, g = lane >> 4, b0 = 8 * S::T * g / kBlock;
-        const int mask = (1 << ld.p.page_shift) - 1;
-        // a tile's 16 keys lie in one page, whose address every lane shares
-        const bool even = ld.p.page_shift >= 4 && ld.p.slot16 < (1u << 20) && ld.p.block_slot < (1u << 24);
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-            const int first = k0 + 16 * a, key = even ? first : first + col;
-            int id = ld.list[(key >> ld.p.page_shift) - ld.first_page];
-            if (even) id = __builtin_amdgcn_readfirstlane(id);
-            page[a] = id;
-            const uint64_t n = uint32_t(max(0, id)), slot = uint32_t(key & mask);
-            const uint64_t codes = (n * ld.p.page16 + slot * ld.p.slot16) << 4, bytes = n * ld.p.block_page + slot * ld.p.block_slot;
-            const uint32_t code_at = (even ? uint32_t(col) * (ld.p.slot16 * 16) : 0) + 4 * S::T * g;
-            const uint32_t byte_at = even ? uint32_t(col) * ld.p.block_slot : 0;
-            load_words<S::T>(k[a], reinterpret_cast<const uint8_t*>(ld.kbase + codes) + code_at);
-            load_words<S::T>(v[a], reinterpret_cast<const uint8_t*>(ld.vbase + codes) + code_at);
-#pragma unroll
-            for (int x = 0; x < S::NS; ++x) {
-                // (past the row's last block: not used)
-                const uint32_t at = byte_at + uint32_t(min(b0 + x, S::T - 1));
-                ke[a][x] = reinterpret_cast<const uint8_t*>(ld.kblock + bytes)[at];
-                ve[a][x] = reinterpret_cast<const uint8_t*>(ld.vblock + bytes)[at];
-            }
-        }
-    }
-
-    // Of the lane's dimensions, step t (eight of them) lies in this of its blocks.
-    __device__ __forceinline__ static float scale_of(const float* scales, int t, int g)
-    {
-        if constexpr (S::T == 8) return scales[t / 4];
-        if constexpr (S::NS == 1) return scales[0];
-        const int b = (S::T * g + t) / 4 - S::T * g / 4;
-        float x = scales[0];
-#pragma unroll
-        for (int i = 1; i < S::NS; ++i) x = b >= i ? scales[i] : x;
-        return x;
-    }
-
-    __device__ __forceinline__ static bf16x8 values(uint32_t codes, float scale)
-    {
-        union { bf16x8 v; bf16x2 p[4]; } a;
-        a.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0);
-        a.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1);
-        a.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2);
-        a.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3);
-        return a.v;
-    }
-};
-
-// A value over the four lanes that hold a row's keys.
-template <class F>
-__device__ __forceinline__ float over_quarters(float x, F f)
-{
-    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = f(__uint_as_float(a[0]), __uint_as_float(a[1]));
-    const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return f(__uint_as_float(b[0]), __uint_as_float(b[1]));
-}
-
-// Two tiles against the wave's rows; vt: the wave's rows of V in LDS.
-template <class S>
-__device__ __forceinline__ void narrow_compute(NarrowState<S>& st, NarrowTile<S>& tile, const Loader<S>& ld, uint8_t* vt, int k0,
-                                               float c, int lane)
-{
-    const int col = lane & 15, g = lane >> 4;
-    const bool masked = k0 < ld.all_lo || k0 + S::KT > ld.all_hi;
-    const bool dirty = masked || __any((tile.page[0] | tile.page[1]) < 0);
-    if (dirty) {
-        // Rows outside [lo, hi) hold another's data, which must not be NaN (their
-        // scores are masked): an exponent byte of 0 makes it too small to count.
-        // Keys of a page outside the cache become NaN.  Values that are NaN at
-        // a key that only some rows see are taken out as well; rows that see it
-        // get them back at the end (narrow_restore).
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-            const int key = k0 + 16 * a + col;
-            const bool outside = key < ld.lo || key >= ld.hi, lost = tile.page[a] < 0;
-            const bool some = key < ld.all_lo || key >= ld.all_hi;
-#pragma unroll
-            for (int x = 0; x < S::NS; ++x) {
-                if (lost) tile.ke[a][x] = 255;
-                const bool nan = tile.ve[a][x] > 252 && some && !outside && !lost;
-                if (nan) *ld.poisoned = 1;
-                if (outside || lost || nan) tile.ve[a][x] = 0;
-            }
-        }
-    }
-    f32x4 sc[S::R][2];
-#pragma unroll
-    for (int r = 0; r < S::R; ++r)
-#pragma unroll
-        for (int a = 0; a < 2; ++a) sc[r][a] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    float ks[2][S::NS], vs[2][S::NS];
-#pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int x = 0; x < S::NS; ++x) ks[a][x] = block_scale(tile.ke[a][x]), vs[a][x] = block_scale(tile.ve[a][x]);
-#pragma unroll
-    for (int t = 0; t < S::T; ++t)
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-            const bf16x8 f = tile.values(tile.k[a][t], tile.scale_of(ks[a], t, g));
-#pragma unroll
-            for (int r = 0; r < S::R; ++r) sc[r][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, st.q[r][t], sc[r][a], 0, 0, 0);
-        }
-#pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int t = 0; t < S::T; ++t) {
-            *reinterpret_cast<bf16x8*>(vt + (16 * a + col) * S::RB + (((S::T * g + t) ^ S::swizzle(col)) << 4)) =
-                tile.values(tile.v[a][t], tile.scale_of(vs[a], t, g));
-        }
-    asm volatile("" ::: "memory");
-
-    bf16x8 pb[S::R];
-#pragma unroll
-    for (int r = 0; r < S::R; ++r) {
-        if (masked) {
-            const uint32_t width = uint32_t(st.rhi[r] - st.rlo[r]);
-            const int first = k0 + 4 * g - st.rlo[r];
-#pragma unroll
-            for (int a = 0; a < 2; ++a)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (uint32_t(first + 16 * a + i) >= width) sc[r][a][i] = -INFINITY;
-        }
-        float top = sc[r][0][0];
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[r][a][i]);
-        // the row's largest only where some lane's passes the reference by too much
-        if (__any(top * c > st.m[r] + kRaise)) {
-            top = over_quarters(top, [](float x, float y) { return fmaxf(x, y); }) * c;
-            const bool raise = top > st.m[r] + kRaise;
-            // of this lane's row alone: other rows keep their reference and their bits
-            const float mn = raise ? top : st.m[r];
-            const float keep = raise ? __builtin_amdgcn_exp2f(st.m[r] - mn) : 1.0f;
-            st.m[r] = mn;
-            st.l[r] *= keep;
-#pragma unroll
-            for (int n = 0; n < 2 * S::T; ++n) st.o[r][n] *= keep;
-        }
-        const float ref = st.m[r] == -INFINITY ? 0.0f : st.m[r];
-        union { bf16x8 v; uint32_t u[4]; } pr;
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[r][a][2 * x], c, -ref));
-                const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[r][a][2 * x + 1], c, -ref));
-                st.l[r] += p0;
-                st.l[r] += p1;
-                pr.u[2 * a + x] = pack_bf16(p0, p1);
-            }
-        pb[r] = pr.v;
-    }
-
-    const int key = 4 * g + col / 4;
-    const uint8_t* row = vt + key * S::RB + (col & 1) * 8;
-    const int chunk = ((col & 3) / 2) ^ S::swizzle(key);      // (16 keys on have the same)
-#pragma unroll
-    for (int n = 0; n < 2 * S::T; ++n) {
-        const uint8_t* at = row + ((chunk ^ (2 * n)) << 4);
-        union { bf16x8 v; s16x4 h[2]; } f;
-        f.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
-        f.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 16 * S::RB));
-#pragma unroll
-        for (int r = 0; r < S::R; ++r) st.o[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.v, pb[r], st.o[r][n], 0, 0, 0);
-    }
-    asm volatile("" ::: "memory");
-}
-
-// Gives the lane's rows the blocks of NaN that were taken out of values at keys
-// [from, to), which no probability takes away.
-template <class S>
-__device__ __forceinline__ void narrow_restore(NarrowState<S>& st, const Loader<S>& ld, int from, int to)
-{
-    const int mask = (1 << ld.p.page_shift) - 1;
-#pragma unroll 1
-    for (int key = max(from, ld.lo); key < min(to, ld.hi); ++key) {
-        if (key >= ld.all_lo && key < ld.all_hi) continue;
-        const int id = ld.table[key >> ld.p.page_shift];
-        if (id < 0 || id >= ld.p.pages) continue;
-        const uint8_t* e = reinterpret_cast<const uint8_t*>(ld.vblock + uint64_t(uint32_t(id)) * ld.p.block_page +
-                                                            uint64_t(uint32_t(key & mask)) * ld.p.block_slot);
-#pragma unroll
-        for (int b = 0; b < S::T; ++b) {
-            if (e[b] <= 252) continue;
-#pragma unroll
-            for (int r = 0; r < S::R; ++r)
-                if (key >= st.rlo[r] && key < st.rhi[r])
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) st.o[r][2 * b + i / 4][i % 4] = __builtin_nanf("");
-        }
-    }
-}
 
 // Gives the lane's row the values that patch() took out, of keys [from, to),
 // each times its probability: infinity stays one, but for a probability of
@@ -1066,7 +655,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
 {
     extern __shared__ __align__(1024) uint8_t lds[];
     int32_t* list = reinterpret_cast<int32_t*>(lds + S::BUFFER);
-    float* ml = reinterpret_cast<float*>(list + S::LIST);      // [2][W][32]
+    float* ml = reinterpret_cast<float*>(list + kListPages);      // [2][W][32]
     int64_t* plan = reinterpret_cast<int64_t*>(ml + 2 * S::W * 32);   // 8 values
     Seq* seqs = reinterpret_cast<Seq*>(plan + 8);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1215,26 +804,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
 
         // ---- the wave's rows
         const int ulane = opaque(lane), col = ulane & 31, h = ulane >> 5;
-        std::conditional_t<S::NARROW, NarrowState<S>, State<S>> st;
-        if constexpr (S::NARROW) {
-#pragma unroll
-            for (int x = 0; x < S::R; ++x) {
-                // rows past the last repeat it and are never written
-                const uint32_t r = uint32_t(u.lane0 + min(16 * x + (ulane & 15), u.rows - 1)), step = by_group(p, r);
-                const uint32_t head = uint32_t(kvh) * uint32_t(p.group) + (r - step * uint32_t(p.group));
-                const uint16_t* qrow = p.q + uint64_t(uint32_t(s.q0 + u.token0) + step) * p.q_token + uint64_t(head) * p.q_head;
-                const int pos = u.first + int(step);
-                st.rhi[x] = max(0, pos + 1);
-                st.rlo[x] = p.window > 0 ? min(st.rhi[x], max(0, pos - p.window + 1)) : 0;
-                st.m[x] = -INFINITY;
-                st.l[x] = 0.0f;
-#pragma unroll
-                for (int t = 0; t < S::T; ++t)
-                    st.q[x][t] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(qrow + 8 * (S::T * (ulane >> 4) + t)));
-#pragma unroll
-                for (int n = 0; n < 2 * S::T; ++n) st.o[x][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            }
-        } else {
+        State<S> st;
         const int row = S::SHARED ? wave * 32 + col : col;
         // rows past the last repeat it and are never written
         const uint32_t r = uint32_t(u.lane0 + min(row, u.rows - 1)), step = by_group(p, r);
@@ -1256,7 +826,6 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
         for (int d = 0; d < S::DB; ++d)
 #pragma unroll
             for (int i = 0; i < 16; ++i) st.o[d][i] = 0.0f;
-        }
         // keys that every row of this wave sees, and that any does
         const int wr0 = S::SHARED ? wave * 32 : 0;
         const bool busy = wr0 < u.rows;
@@ -1292,23 +861,15 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
         float c = p.scale * ks * kLog2e;
         if (c < 0.0f) {
             c = -c;
-            if constexpr (S::NARROW) {
-#pragma unroll
-                for (int x = 0; x < S::R * S::T; ++x) {
-                    bf16x8& q = st.q[x / S::T][x % S::T];
-                    q = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, q) ^ 0x80008000u);
-                }
-            } else {
 #pragma unroll
             for (int t = 0; t < S::STEPS; ++t) st.q[t] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, st.q[t]) ^ 0x80008000u);
-            }
         }
         if (c < 1e-37f) c = 1e-37f;
 
         const auto run_tile = [&](uint32_t at_lds, int k0) {
             if (!busy || k0 >= any_hi || k0 + S::KT <= any_lo) return;
             const uint8_t* kt = lds + (at_lds - lds0);
-            if constexpr (!S::NARROW) compute<S>(st, kt, kt + S::TILE, k0, c, k0 < all_lo || k0 + S::KT > all_hi, ulane);
+            compute<S>(st, kt, kt + S::TILE, k0, c, k0 < all_lo || k0 + S::KT > all_hi, ulane);
         };
 
         // ---- segments of the run whose page ids fit the list
@@ -1316,7 +877,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
             const int start = __builtin_amdgcn_readfirstlane(u.base + (from + done) * S::STEP);
             ld.first_page = start >> p.page_shift;
             // steps whose last key's page is in the list
-            const int64_t span = (int64_t(ld.first_page + S::LIST) << p.page_shift) - start;
+            const int64_t span = (int64_t(ld.first_page + kListPages) << p.page_shift) - start;
             const int n = int(min(int64_t(count - done), span / S::STEP));
             const int want = int((uint32_t(start + n * S::STEP - 1) >> p.page_shift) - ld.first_page + 1);
             __syncthreads();
@@ -1326,21 +887,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
                 list[i] = id >= p.pages ? -1 : id;
             }
             __syncthreads();
-            if constexpr (S::NARROW) {
-                // the next step's loads run beside this one's products
-                const int k1 = start + wave * S::KT;
-                uint8_t* vt = lds + wave * S::TILE;
-                NarrowTile<S> x, y;
-                x.fetch(ld, k1, ulane);
-                for (int i = 0; i < n; i += 2) {
-                    const int k0 = k1 + i * S::STEP;
-                    if (i + 1 < n) y.fetch(ld, k0 + S::STEP, ulane);
-                    if (k0 < ld.hi) narrow_compute<S>(st, x, ld, vt, k0, c, ulane);
-                    if (i + 1 == n) break;
-                    if (i + 2 < n) x.fetch(ld, k0 + 2 * S::STEP, ulane);
-                    if (k0 + S::STEP < ld.hi) narrow_compute<S>(st, y, ld, vt, k0 + S::STEP, c, ulane);
-                }
-            } else if constexpr (S::MXFP4) {
+            if constexpr (S::MXFP4) {
                 // the next tile's loads run beside this one's products
                 const int thread = S::SHARED ? opaque(threadIdx.x) : ulane;
                 const int k1 = S::SHARED ? start : start + wave * S::KT;
@@ -1405,18 +952,9 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
             }
             done += n;
         }
-        if constexpr (S::NARROW) {
-#pragma unroll
-            for (int x = 0; x < S::R; ++x) st.l[x] = over_quarters(st.l[x], [](float a, float b) { return a + b; });
-        } else {
         st.l = sum_halves(st.l);
-        }
         __syncthreads();
-        if constexpr (S::NARROW) {
-            if (plan[5]) narrow_restore<S>(st, ld, u.base + from * S::STEP, u.base + (from + count) * S::STEP);
-        } else {
         if (plan[5]) restore(st, p, ld, u.base + from * S::STEP, u.base + (from + count) * S::STEP, c, wave);
-        }
 
         // ---- results: whole units to the output, parts to the workspace
         const bool whole = count == u.steps;
@@ -1442,7 +980,6 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
         // by register pair, so that its stores and loads are contiguous.
         const uint32_t lane_at = uint32_t(wave) * (S::DB * 8 + 1) * 128 + 2 * lane2;
         const auto write_rows = [&] {
-            if constexpr (S::SHARED) {
             const int row = wave * 32 + col2;
             if (row >= u.rows) return;
             const float inv = inverse(st.l);
@@ -1455,9 +992,8 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
                     put_out(row, at_d, st.o[d][4 * x], st.o[d][4 * x + 1], st.o[d][4 * x + 2], st.o[d][4 * x + 3], inv);
                 }
             if (p.lse && h2 == 0) put_lse(row, st.m, st.l);
-            }
         };
-        if constexpr (S::SHARED) {
+        if (S::SHARED) {
             if (!whole && busy) {
                 float* o = slot + lane_at;
 #pragma unroll
@@ -1468,34 +1004,6 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
             }
         } else {
             // the waves' sums meet in LDS
-            if constexpr (S::NARROW) {
-                const int c2 = lane2 & 15, g2 = lane2 >> 4;
-                if (g2 == 0) {
-#pragma unroll
-                    for (int x = 0; x < S::R; ++x)
-                        ml[wave * 32 + 16 * x + c2] = st.m[x], ml[(S::W + wave) * 32 + 16 * x + c2] = st.l[x];
-                }
-                __syncthreads();
-#pragma unroll
-                for (int x = 0; x < S::R; ++x) {
-                    const int row = 16 * x + c2;
-                    if (row >= u.rows) continue;
-                    float m = -INFINITY, l = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < S::W; ++w) m = fmaxf(m, ml[w * 32 + row]);
-                    const float ref = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-                    for (int w = 0; w < S::W; ++w) l += ml[(S::W + w) * 32 + row] * __builtin_amdgcn_exp2f(ml[w * 32 + row] - ref);
-                    const float keep = __builtin_amdgcn_exp2f(st.m[x] - ref);
-                    float* buf = reinterpret_cast<float*>(lds) + (wave * S::M + row) * S::OS + 4 * g2;
-#pragma unroll
-                    for (int n = 0; n < 2 * S::T; ++n) *reinterpret_cast<f32x4*>(buf + 16 * n) = st.o[x][n] * keep;
-                    if (wave == 0 && g2 == 0) {
-                        if (!whole) put2(slot + S::M * S::DP + 2 * row, m, l);
-                        else if (p.lse) put_lse(row, m, l);
-                    }
-                }
-            } else {
             if (h2 == 0) ml[wave * 32 + col2] = st.m, ml[(S::W + wave) * 32 + col2] = st.l;
             __syncthreads();
             float m = -INFINITY, l = 0.0f;
@@ -1518,7 +1026,6 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
                     if (!whole) put2(slot + S::M * S::DP + 2 * col2, m, l);
                     else if (p.lse) put_lse(col2, m, l);
                 }
-            }
             }
             __syncthreads();
             // (references and sums of the rows stay in ml)
@@ -1568,7 +1075,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
             }
             __syncthreads();
             if (plan[4]) {
-                // The unit's parts in run order; Split: eight or sixteen parts' loads at a time.
+                // The unit's parts in run order; Split: sixteen parts' loads at a time.
                 const int parts = run_of(begin + S::EXTRA + u.steps - 1) - wf + 1;
                 // only the first can have begun in its run, all others continue one
                 const int slot0 = wf * 2 + (run_start(wf) > begin ? 0 : 1);
@@ -1610,10 +1117,10 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
                     const int rw = i / QUADS, d = (i % QUADS) * 4;
                     if (!S::FULL && d >= p.dim) continue;
                     float m = -INFINITY, l = 0.0f, a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    for (int x = 0; x < parts; x += S::PARTS) {
-                        float pm[S::PARTS], pl[S::PARTS], v[S::PARTS][4];
+                    for (int x = 0; x < parts; x += 16) {
+                        float pm[16], pl[16], v[16][4];
 #pragma unroll
-                        for (int e = 0; e < S::PARTS; ++e) {
+                        for (int e = 0; e < 16; ++e) {
                             // Narrow heads: past the last part it once more, for at a branch
                             // the loads before are waited for (8 sequences of up to 9000 keys,
                             // 32 heads of 64: 23.6 -> 20.0 us); with 128 dimensions the loads
@@ -1628,18 +1135,18 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
                         }
                         asm volatile("" ::: "memory");
 #pragma unroll
-                        for (int e = 1; e < S::PARTS; ++e)
+                        for (int e = 1; e < 16; ++e)
                             if (S::DP <= 64 && x + e >= parts) pm[e] = -INFINITY, pl[e] = v[e][0] = v[e][1] = v[e][2] = v[e][3] = 0.0f;
                         float mn = m;
 #pragma unroll
-                        for (int e = 0; e < S::PARTS; ++e) mn = fmaxf(mn, pm[e]);
+                        for (int e = 0; e < 16; ++e) mn = fmaxf(mn, pm[e]);
                         const float ref = mn == -INFINITY ? 0.0f : mn, keep = __builtin_amdgcn_exp2f(m - ref);
                         m = mn;
                         l *= keep;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) a[j] *= keep;
 #pragma unroll
-                        for (int e = 0; e < S::PARTS; ++e) {
+                        for (int e = 0; e < 16; ++e) {
                             const float share = __builtin_amdgcn_exp2f(pm[e] - ref);
                             l += pl[e] * share;
 #pragma unroll
@@ -1695,7 +1202,7 @@ hipError_t run(const AttnParams& a, const BlockArgs& all, hipStream_t s)
 // Waves that share key tiles.  Up to 32 rows a sequence and kv head stream
 // the cache once either way: none (32 sequences of up to 9000 bf16 keys, 28
 // rows: 82 us, shared 90; a few short ones are faster shared, 36 and 28).
-// A 4-bit cache's rows go by sixteens: up to 16 rows, -1.
+// Over a 4-bit cache they have kernels of their own, by 16 rows: -1 up to 16.
 int sharing(const CacheView& cache, int64_t tokens, int64_t max_q, int group, int seqs)
 {
     if (cache.mxfp4 && max_q * group <= 16) return -1;
@@ -1723,24 +1230,21 @@ auto with_shape(const CacheView& cache, int waves, F f)
         if (cache.mxfp4) return by_dim(std::integral_constant<Kind, kMxfp4>(), w);
         return cache.e4m3 ? by_dim(std::integral_constant<Kind, kE4m3>(), w) : by_dim(std::integral_constant<Kind, kBf16>(), w);
     };
-    if (cache.mxfp4 && waves <= 0) {
-        const auto narrow = [&](auto r) {
-            constexpr int R = decltype(r)::value;
-            switch (dim / kBlock) {
-            case 1: return f(NarrowShape<1, R>());
-            case 2: return f(NarrowShape<2, R>());
-            case 3: return f(NarrowShape<3, R>());
-            case 4: return f(NarrowShape<4, R>());
-            case 5: return f(NarrowShape<5, R>());
-            case 6: return f(NarrowShape<6, R>());
-            case 7: return f(NarrowShape<7, R>());
-            default: return f(NarrowShape<8, R>());
-            }
-        };
-        return waves < 0 ? narrow(std::integral_constant<int, 1>()) : narrow(std::integral_constant<int, 2>());
-    }
-    if (waves <= 0) return by_type(std::integral_constant<int, 0>());
+    if (waves == 0) return cache.e4m3 ? by_dim(std::integral_constant<Kind, kE4m3>(), std::integral_constant<int, 0>())
+                                      : by_dim(std::integral_constant<Kind, kBf16>(), std::integral_constant<int, 0>());
     return waves == 4 ? by_type(std::integral_constant<int, 4>()) : by_type(std::integral_constant<int, 8>());
+}
+
+}  // namespace
+
+namespace {
+
+size_t shape_bytes(const CacheView& cache, int waves, int64_t tokens, int group, int seqs, int64_t max_kv)
+{
+    if (cache.mxfp4 && waves <= 0) return attention_few_bytes({cache.head_dim, cache.kv_heads, seqs, waves == 0, max_kv});
+    return with_shape(cache, waves, [&](auto shape) {
+        return bytes<decltype(shape)>(tokens, group, cache.kv_heads, seqs, max_kv);
+    });
 }
 
 }  // namespace
@@ -1749,9 +1253,7 @@ size_t attention_workspace_need(const CacheView& cache, int64_t tokens, int q_he
                                 int64_t max_kv)
 {
     const int group = q_heads / cache.kv_heads;
-    return with_shape(cache, sharing(cache, tokens, max_q < tokens ? max_q : tokens, group, seqs), [&](auto shape) {
-        return bytes<decltype(shape)>(tokens, group, cache.kv_heads, seqs, max_kv);
-    });
+    return shape_bytes(cache, sharing(cache, tokens, max_q < tokens ? max_q : tokens, group, seqs), tokens, group, seqs, max_kv);
 }
 
 // The largest need of any shape within the bounds: each kernel shape's grows
@@ -1763,9 +1265,8 @@ size_t attention_workspace_bytes(const CacheView& cache, int64_t tokens, int q_h
     size_t most = 0;
     for (int waves : {-1, 0, 4, 8}) {
         if (waves > sharing(cache, tokens, max_q < tokens ? max_q : tokens, group, 1)) break;
-        const size_t n = with_shape(cache, waves, [&](auto shape) {
-            return bytes<decltype(shape)>(tokens, group, cache.kv_heads, seqs, max_kv);
-        });
+        if (waves < 0 && !cache.mxfp4) continue;
+        const size_t n = shape_bytes(cache, waves, tokens, group, seqs, max_kv);
         if (n > most) most = n;
     }
     return most;
@@ -1813,8 +1314,10 @@ hipError_t launch_attention(const AttnParams& a, hipStream_t s)
     p.block_page = uint32_t(a.blocks.page_stride);
     p.block_head = uint32_t(a.blocks.head_stride);
     p.block_slot = uint32_t(a.blocks.slot_stride);
-    return with_shape(a.cache, sharing(a.cache, a.tokens, a.max_q, a.group, a.seqs),
-                      [&](auto shape) { return run<decltype(shape)>(a, p, s); });
+    const int waves = sharing(a.cache, a.tokens, a.max_q, a.group, a.seqs);
+    if (a.cache.mxfp4 && waves <= 0)
+        return launch_attention_few({a.cache.head_dim, a.cache.kv_heads, a.seqs, waves == 0, a.max_kv}, &p, s);
+    return with_shape(a.cache, waves, [&](auto shape) { return run<decltype(shape)>(a, p, s); });
 }
 
 }  // namespace qg
