@@ -247,7 +247,7 @@ size_t qg_paged_attention_workspace_size(const qg_kv_cache* cache, int64_t token
     qg::CacheView view;
     qg::BlockView blocks;
     if (check_attention_shape(cache, tokens, q_heads, seqs, max_q, max_kv, &view, &blocks) != QG_OK) return 0;
-    return qg::attention_workspace_bytes(view, tokens, q_heads, seqs, max_q, max_kv);
+    return qg::attention_workspace_bytes(view, blocks, tokens, q_heads, seqs, max_q, max_kv);
 }
 
 qg_status qg_paged_attention(const qg_kv_cache* cache, const uint16_t* q_bf16, int64_t q_token_stride,
@@ -281,7 +281,7 @@ qg_status qg_paged_attention(const qg_kv_cache* cache, const uint16_t* q_bf16, i
     qg::Dim dims[] = {{tokens, out_token_stride}, {q_heads, out_head_stride}};
     if (!qg::rows_disjoint(dims, p.cache.head_dim)) return QG_ERR_INVALID_ARG;
     if (tokens == 0 || seqs == 0 || max_q == 0) return QG_OK;
-    if (workspace_bytes < qg::attention_workspace_need(p.cache, tokens, q_heads, seqs, max_q, max_kv))
+    if (workspace_bytes < qg::attention_workspace_need(p.cache, p.blocks, tokens, q_heads, seqs, max_q, max_kv))
         return QG_ERR_INVALID_ARG;
     p.q = q_bf16;
     p.q_token = q_token_stride;

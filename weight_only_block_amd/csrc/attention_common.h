@@ -9,13 +9,15 @@
 namespace qg {
 
 // What the kernels of few rows on a 4-bit cache are chosen and sized by:
-// `second`, more than 16 rows a sequence and kv head (up to 32).
+// `second`, more than 16 rows a sequence and kv head (up to 32); `even`, 16
+// keys of a tile lie in one page, and offsets within it in 32 bits.
 struct FewSize {
     int dim, kv_heads, seqs;
-    bool second;
+    bool second, even;
     int64_t max_kv;
 };
-size_t attention_few_bytes(const FewSize& z);
+size_t attention_few_need(const FewSize& z);    // of this shape
+size_t attention_few_bytes(const FewSize& z);   // of this shape and every smaller one
 hipError_t launch_attention_few(const FewSize& z, const void* block_args, hipStream_t s);
 
 namespace {

@@ -136,10 +136,10 @@ __host__ __device__ inline Seq cut_seq(int start, int next, int kv, int tokens, 
 }
 
 // Of this shape; of this shape and every smaller one.
-size_t attention_workspace_need(const CacheView& cache, int64_t tokens, int q_heads, int seqs, int64_t max_q,
-                                int64_t max_kv);
-size_t attention_workspace_bytes(const CacheView& cache, int64_t tokens, int q_heads, int seqs, int64_t max_q,
-                                 int64_t max_kv);
+size_t attention_workspace_need(const CacheView& cache, const BlockView& blocks, int64_t tokens, int q_heads, int seqs,
+                                int64_t max_q, int64_t max_kv);
+size_t attention_workspace_bytes(const CacheView& cache, const BlockView& blocks, int64_t tokens, int q_heads, int seqs,
+                                 int64_t max_q, int64_t max_kv);
 hipError_t launch_attention(const AttnParams& p, hipStream_t s);
 
 struct SampleParams {

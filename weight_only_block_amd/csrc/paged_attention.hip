@@ -1239,9 +1239,14 @@ auto with_shape(const CacheView& cache, int waves, F f)
 
 namespace {
 
-size_t shape_bytes(const CacheView& cache, int waves, int64_t tokens, int group, int seqs, int64_t max_kv)
+FewSize few_size(const CacheView& cache, const BlockView& blocks, int waves, int seqs, int64_t max_kv)
 {
-    if (cache.mxfp4 && waves <= 0) return attention_few_bytes({cache.head_dim, cache.kv_heads, seqs, waves == 0, max_kv});
+    const bool even = cache.page_shift >= 4 && cache.slot_stride < (int64_t(1) << 25) && blocks.slot_stride < (int64_t(1) << 24);
+    return {cache.head_dim, cache.kv_heads, seqs, waves == 0, even, max_kv};
+}
+
+size_t shared_bytes(const CacheView& cache, int waves, int64_t tokens, int group, int seqs, int64_t max_kv)
+{
     return with_shape(cache, waves, [&](auto shape) {
         return bytes<decltype(shape)>(tokens, group, cache.kv_heads, seqs, max_kv);
     });
@@ -1249,24 +1254,27 @@ size_t shape_bytes(const CacheView& cache, int waves, int64_t tokens, int group,
 
 }  // namespace
 
-size_t attention_workspace_need(const CacheView& cache, int64_t tokens, int q_heads, int seqs, int64_t max_q,
-                                int64_t max_kv)
+size_t attention_workspace_need(const CacheView& cache, const BlockView& blocks, int64_t tokens, int q_heads, int seqs,
+                                int64_t max_q, int64_t max_kv)
 {
     const int group = q_heads / cache.kv_heads;
-    return shape_bytes(cache, sharing(cache, tokens, max_q < tokens ? max_q : tokens, group, seqs), tokens, group, seqs, max_kv);
+    const int waves = sharing(cache, tokens, max_q < tokens ? max_q : tokens, group, seqs);
+    if (cache.mxfp4 && waves <= 0) return attention_few_need(few_size(cache, blocks, waves, seqs, max_kv));
+    return shared_bytes(cache, waves, tokens, group, seqs, max_kv);
 }
 
 // The largest need of any shape within the bounds: each kernel shape's grows
 // with all of them, and smaller calls may take another one than the largest.
-size_t attention_workspace_bytes(const CacheView& cache, int64_t tokens, int q_heads, int seqs, int64_t max_q,
-                                 int64_t max_kv)
+size_t attention_workspace_bytes(const CacheView& cache, const BlockView& blocks, int64_t tokens, int q_heads, int seqs,
+                                 int64_t max_q, int64_t max_kv)
 {
     const int group = q_heads / cache.kv_heads;
     size_t most = 0;
     for (int waves : {-1, 0, 4, 8}) {
         if (waves > sharing(cache, tokens, max_q < tokens ? max_q : tokens, group, 1)) break;
         if (waves < 0 && !cache.mxfp4) continue;
-        const size_t n = shape_bytes(cache, waves, tokens, group, seqs, max_kv);
+        const size_t n = cache.mxfp4 && waves <= 0 ? attention_few_bytes(few_size(cache, blocks, waves, seqs, max_kv))
+                                                   : shared_bytes(cache, waves, tokens, group, seqs, max_kv);
         if (n > most) most = n;
     }
     return most;
@@ -1316,7 +1324,7 @@ hipError_t launch_attention(const AttnParams& a, hipStream_t s)
     p.block_slot = uint32_t(a.blocks.slot_stride);
     const int waves = sharing(a.cache, a.tokens, a.max_q, a.group, a.seqs);
     if (a.cache.mxfp4 && waves <= 0)
-        return launch_attention_few({a.cache.head_dim, a.cache.kv_heads, a.seqs, waves == 0, a.max_kv}, &p, s);
+        return launch_attention_few(few_size(a.cache, a.blocks, waves, a.seqs, a.max_kv), &p, s);
     return with_shape(a.cache, waves, [&](auto shape) { return run<decltype(shape)>(a, p, s); });
 }
 

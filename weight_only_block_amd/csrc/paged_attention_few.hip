@@ -27,6 +27,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "attention_common.h"
 #include "decode_ops.h"
 
@@ -41,22 +43,26 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(1))) const uint8_t* global_ptr;
 
 constexpr int kAhead = 4;          // LDS reads ahead of their matrix products
-constexpr int kDeviceScope = 16;   // of a buffer access: past the XCD's own cache
+// Of a buffer access: past the XCD's own cache; not to stay in the caches.
+constexpr int kDeviceScope = 16, kOnce = 2;
 constexpr uint32_t kNowhere = 0x1fffffffu;   // floats: past every buffer below
 
-// 32 T dimensions, 16 R rows.
-template <int T_, int R_>
+// 32 T dimensions, 16 R rows; EVEN: 16 keys of a tile lie in one page; W waves
+// a work-group.
+template <int T_, int R_, bool EVEN_, int W_>
 struct Few {
     static constexpr int T = T_, R = R_, DP = 32 * T;
+    static constexpr bool EVEN = EVEN_;
     static constexpr int RB = T <= 2 ? 64 * T : T <= 4 ? 256 : 512;     // bytes of a row of V in LDS, a power of two
-    static constexpr int W = 4, THREADS = 64 * W;
+    static constexpr int W = W_, THREADS = 64 * W;
     static constexpr int M = 16 * R;
     static constexpr int KT = 32, STEP = KT * W;                        // keys of a wave's tiles, of a step
     static constexpr int TILE = KT * RB;
     // exponent bytes that a lane's 8 T dimensions of a key reach into
     static constexpr int NS = T == 7 ? 3 : T == 3 || T >= 5 ? 2 : 1;
-    static constexpr int REGISTERS = 8 * T * R + 4 * T * R + 4 * T + 4 * NS + 70;
-    static constexpr int WAVES_PER_SIMD = REGISTERS <= 128 ? 4 : REGISTERS <= 168 ? 3 : REGISTERS <= 256 ? 2 : 1;
+    static constexpr int REGISTERS = 8 * T * R + 4 * T * R + 4 * T + 4 * NS + 72;
+    // (four waves of 128 registers a SIMD are not better than three of 168)
+    static constexpr int WAVES_PER_SIMD = REGISTERS <= 110 ? 4 : REGISTERS <= 160 && W == 4 ? 3 : REGISTERS <= 240 ? 2 : 1;
     static constexpr int OS = DP + 4;                                   // floats of a row in the joining buffer
     static constexpr int RING = W * TILE, JOIN = W * M * OS * 4;
     static constexpr int BUFFER = RING > JOIN ? RING : JOIN;
@@ -68,7 +74,10 @@ struct Few {
     static constexpr int LEAST = 2, EXTRA = 3;
     static constexpr float JOINED = 0.25f;
     static constexpr int SLOT = M * DP + 2 * M;                         // floats of a partial result
-    static constexpr int QUADS = DP / 4, PARTS = 8;                     // parts whose loads are in flight together
+    // Joining: four values at a time, so many of them a thread, and parts whose
+    // loads are in flight together.
+    static constexpr int QUADS = DP / 4, ITEMS = (M * QUADS + THREADS - 1) / THREADS;
+    static constexpr int PARTS = 8;
 
     // The chunk of 8 dimensions is moved so that 16 keys of one chunk (what a
     // wave's quarter writes) and 8 keys of two neighbours (what a half reads)
@@ -125,6 +134,12 @@ struct Place {
     }
 };
 
+// Memory from an address that all lanes share, for offsets of 32 bits.
+__device__ __forceinline__ auto buffer_at(uint64_t address)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(address), 0, -1, 0x00020000);
+}
+
 // Two tiles of 16 keys of K and of V on their way through registers.
 template <class S>
 struct Tile {
@@ -138,32 +153,68 @@ struct Tile {
     {
         constexpr int n = N >= 4 ? 4 : N;
         if constexpr (n == 1) {
-            to[0] = __builtin_nontemporal_load(reinterpret_cast<__attribute__((address_space(1))) const uint32_t*>(at));
+            to[0] = *reinterpret_cast<__attribute__((address_space(1))) const uint32_t*>(at);
         } else {
             typedef uint32_t words __attribute__((ext_vector_type(n), aligned(4)));
-            const words x = __builtin_nontemporal_load(reinterpret_cast<__attribute__((address_space(1))) const words*>(at));
+            const words x = *reinterpret_cast<__attribute__((address_space(1))) const words*>(at);
 #pragma unroll
             for (int i = 0; i < n; ++i) to[i] = x[i];
         }
         if constexpr (N > 4) load_words<N - 4>(to + 4, at + 16);
     }
+    // The same at an offset from an address that all lanes share.
+    template <int N, class B>
+    __device__ __forceinline__ static void load_words(uint32_t* to, B base, uint32_t at)
+    {
+        if constexpr (N >= 4) {
+            const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(base, at, 0, kOnce);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[i] = x[i];
+        } else if constexpr (N == 3) {
+            const auto x = __builtin_amdgcn_raw_buffer_load_b96(base, at, 0, kOnce);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) to[i] = x[i];
+        } else if constexpr (N == 2) {
+            const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(base, at, 0, kOnce);
+            to[0] = x[0], to[1] = x[1];
+        } else {
+            to[0] = __builtin_amdgcn_raw_buffer_load_b32(base, at, 0, kOnce);
+        }
+        if constexpr (N > 4) load_words<N - 4>(to + 4, base, at + 16);
+    }
 
-    // Tile a's parts of the lane's key: page and slot uniform with offsets of
-    // the lane beside them, or all the lane's own.
-    __device__ __forceinline__ void fetch(const Place& at, int a, int id, uint32_t slot, uint32_t code_at, uint32_t byte_at, int b0)
+    // Tile a's parts of the lanes' keys, 16 rows of a page from `slot` on.
+    __device__ __forceinline__ void fetch_page(const Place& at, int a, int id, uint32_t slot, uint32_t code_at, uint32_t byte_at, int b0)
     {
         page[a] = id;
         const uint64_t n = uint32_t(max(0, id));
         const uint64_t codes = (n * at.p.page16 + uint64_t(slot) * at.p.slot16) << 4;
         const uint64_t bytes = n * at.p.block_page + uint64_t(slot) * at.p.block_slot;
-        load_words<S::T>(k[a], global_ptr(at.k + codes) + code_at);
-        load_words<S::T>(v[a], global_ptr(at.v + codes) + code_at);
+        load_words<S::T>(k[a], buffer_at(at.k + codes), code_at);
+        load_words<S::T>(v[a], buffer_at(at.v + codes), code_at);
 #pragma unroll
         for (int x = 0; x < S::NS; ++x) {
             // (past the row's last block: not used)
             const uint32_t byte = byte_at + uint32_t(min(b0 + x, S::T - 1));
-            ke[a][x] = global_ptr(at.k_block + bytes)[byte];
-            ve[a][x] = global_ptr(at.v_block + bytes)[byte];
+            ke[a][x] = __builtin_amdgcn_raw_buffer_load_b8(buffer_at(at.k_block + bytes), byte, 0, 0);
+            ve[a][x] = __builtin_amdgcn_raw_buffer_load_b8(buffer_at(at.v_block + bytes), byte, 0, 0);
+        }
+    }
+
+    // The same for a page of the lane's own.
+    __device__ __forceinline__ void fetch_row(const Place& at, int a, int id, uint32_t slot, uint32_t part, int b0)
+    {
+        page[a] = id;
+        const uint64_t n = uint32_t(max(0, id));
+        const uint64_t codes = ((n * at.p.page16 + uint64_t(slot) * at.p.slot16) << 4) + part;
+        const uint64_t bytes = n * at.p.block_page + uint64_t(slot) * at.p.block_slot;
+        load_words<S::T>(k[a], global_ptr(at.k + codes));
+        load_words<S::T>(v[a], global_ptr(at.v + codes));
+#pragma unroll
+        for (int x = 0; x < S::NS; ++x) {
+            const int b = min(b0 + x, S::T - 1);
+            ke[a][x] = global_ptr(at.k_block + bytes)[b];
+            ve[a][x] = global_ptr(at.v_block + bytes)[b];
         }
     }
 
@@ -385,6 +436,81 @@ __device__ __forceinline__ f32x2 get2(float* base, uint32_t at)
     return __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(parts_buffer(base), at * 4, 0, kDeviceScope));
 }
 
+// Joins a unit's parts, the first at slot `first`, part x > 0 at slot rest + 2 x,
+// in an order that depends on their number and the rows alone.  A thread has
+// up to ITEMS times four values; the loads of PARTS parts, of all of them, are
+// in flight together, and what is past the rows or the parts reads nowhere (at
+// a branch the loads before it would be waited for).  Few rows: groups of
+// threads take PARTS parts in turn, and their sums meet in LDS.
+template <class S, class F>
+__device__ __forceinline__ void join_parts(float* slots, int first, int rest, int parts, int rows, uint8_t* lds, F out)
+{
+    const int tid = opaque(threadIdx.x), items = rows * S::QUADS;
+    int groups = 1;
+    while (items * groups * 2 <= S::THREADS && groups * S::PARTS < parts) groups *= 2;
+    const int group = groups > 1 ? tid / items : 0, item = tid - group * items;
+    f32x4 a[S::ITEMS];
+    float m[S::ITEMS], l[S::ITEMS];
+#pragma unroll
+    for (int i = 0; i < S::ITEMS; ++i) a[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f}, m[i] = -INFINITY, l[i] = 0.0f;
+#pragma unroll 1
+    for (int x = group * S::PARTS; x < (group < groups ? parts : 0); x += groups * S::PARTS) {
+        f32x2 pm[S::ITEMS][S::PARTS];
+        f32x4 v[S::ITEMS][S::PARTS];
+#pragma unroll
+        for (int e = 0; e < S::PARTS; ++e) {
+            const uint32_t from = uint32_t(x + e ? rest + 2 * (x + e) : first) * S::SLOT;
+#pragma unroll
+            for (int i = 0; i < S::ITEMS; ++i) {
+                const int at = item + i * S::THREADS;
+                const bool none = x + e >= parts || at >= items;
+                pm[i][e] = get2(slots, none ? kNowhere : from + S::M * S::DP + 2 * (at / S::QUADS));
+                v[i][e] = get4(slots, none ? kNowhere : from + at * 4);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < S::ITEMS; ++i) {
+            float mn = m[i];
+#pragma unroll
+            for (int e = 0; e < S::PARTS; ++e) {
+                if (x + e >= parts) pm[i][e][0] = -INFINITY;
+                mn = fmaxf(mn, pm[i][e][0]);
+            }
+            const float ref = mn == -INFINITY ? 0.0f : mn, keep = __builtin_amdgcn_exp2f(m[i] - ref);
+            m[i] = mn;
+            l[i] *= keep;
+            a[i] *= keep;
+#pragma unroll
+            for (int e = 0; e < S::PARTS; ++e) {
+                const float share = __builtin_amdgcn_exp2f(pm[i][e][0] - ref);
+                l[i] += pm[i][e][1] * share;
+                a[i] += v[i][e] * share;
+            }
+        }
+    }
+    if (groups > 1) {
+        f32x4* sums = reinterpret_cast<f32x4*>(lds);                   // [groups][items]
+        f32x2* refs = reinterpret_cast<f32x2*>(sums + S::THREADS);
+        if (group < groups) sums[tid] = a[0], refs[tid] = f32x2{m[0], l[0]};
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll 1
+        for (int e = 1; e < groups; ++e) {
+            const f32x2 r = refs[e * items + item];
+            const float mn = fmaxf(m[0], r[0]), ref = mn == -INFINITY ? 0.0f : mn;
+            const float keep = __builtin_amdgcn_exp2f(m[0] - ref), share = __builtin_amdgcn_exp2f(r[0] - ref);
+            m[0] = mn;
+            l[0] = l[0] * keep + r[1] * share;
+            a[0] = a[0] * keep + sums[e * items + item] * share;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < S::ITEMS; ++i) {
+        const int at = item + i * S::THREADS;
+        if (at < items) out(at / S::QUADS, at % S::QUADS * 4, a[i], m[i], l[i]);
+    }
+}
+
 template <class S>
 __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel(BlockArgs p)
 {
@@ -474,11 +600,10 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel
             // ---- this wave's tiles: two of 16 keys a step.  A tile lies in one
             // page: lane j holds that of tile j of 64, or lanes look up their keys'.
             const int k1 = u.base + from * S::STEP + wave * S::KT;
-            const bool even = p.page_shift >= 4 && p.slot16 < (1u << 20) && p.block_slot < (1u << 24);
             int ids = -1;
             const auto look_up = [&](int step) { ids = place.page_of(k1 + (step + (ulane >> 1)) * S::STEP + 16 * (ulane & 1)); };
             const bool keys = u.hi > u.lo;
-            if (keys && even) look_up(0);
+            if (S::EVEN && keys) look_up(0);
 
             // ---- the rows
             State<S> st;
@@ -515,39 +640,38 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel
             // ---- the tiles
             uint8_t* vt = lds + wave * S::TILE;
             bool poisoned = false;
-            Tile<S> tile;
             const int n = keys ? count : 0;
-#pragma unroll 1
-            for (int i = -1; i < n; ++i) {
+            const auto fetch = [&](Tile<S>& tile, int i) {
+                const int k0 = k1 + i * S::STEP, mask = (1 << p.page_shift) - 1, b0 = 8 * S::T * g / kBlock;
+                const uint32_t part = 4 * S::T * g;
+                if (S::EVEN && i > 0 && i % 32 == 0) look_up(i);
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    if (S::EVEN) {
+                        tile.fetch_page(place, a, __builtin_amdgcn_readlane(ids, 2 * (i % 32) + a), uint32_t((k0 + 16 * a) & mask),
+                                        uint32_t(col) * (p.slot16 * 16) + part, uint32_t(col) * p.block_slot, b0);
+                    } else {
+                        const int key = k0 + 16 * a + col;
+                        tile.fetch_row(place, a, place.page_of(key), uint32_t(key & mask), part, b0);
+                    }
+                }
+            };
+            // The loads of the step after next begin once this one's registers are
+            // converted, ahead of the softmax and the second product.
+            const auto step = [&](Tile<S>& tile, int i) {
                 const int k0 = k1 + i * S::STEP;
-                const bool live = i >= 0 && k0 < u.hi, masked = k0 < u.all_lo || k0 + S::KT > u.all_hi;
+                const bool live = k0 < u.hi, masked = k0 < u.all_lo || k0 + S::KT > u.all_hi;
                 f32x4 sc[S::R][2];
                 if (live) poisoned |= consume<S>(st, tile, sc, u, masked, vt, k0, ulane);
                 asm volatile("" ::: "memory");
-                // The next step's loads begin once this one's registers are
-                // converted, ahead of the softmax and the second product.
-                if (i + 1 < n) {
-                    const int next = k0 + S::STEP, mask = (1 << p.page_shift) - 1, b0 = 8 * S::T * g / kBlock;
-                    const uint32_t part = 4 * S::T * g;
-                    if (even) {
-                        if (i >= 0 && (i + 1) % 32 == 0) look_up(i + 1);
-#pragma unroll
-                        for (int a = 0; a < 2; ++a) {
-                            const int id = __builtin_amdgcn_readlane(ids, 2 * ((i + 1) % 32) + a);
-                            tile.fetch(place, a, id, uint32_t((next + 16 * a) & mask), uint32_t(col) * (p.slot16 * 16) + part,
-                                       uint32_t(col) * p.block_slot, b0);
-                        }
-                    } else {
-#pragma unroll
-                        for (int a = 0; a < 2; ++a) {
-                            const int key = next + 16 * a + col;
-                            tile.fetch(place, a, place.page_of(key), uint32_t(key & mask), part, 0, b0);
-                        }
-                    }
-                }
+                if (i + 1 < n) fetch(tile, i + 1);
                 if (live) accumulate<S>(st, sc, masked, vt, k0, c, ulane);
                 asm volatile("" ::: "memory");
-            }
+            };
+            Tile<S> tile;
+            if (n > 0) fetch(tile, 0);
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) step(tile, i);
             if (poisoned) restore<S>(st, place, u, u.base + from * S::STEP, u.base + (from + count) * S::STEP, wave);
 
             // ---- the waves' sums meet in LDS; whole units go to the output, parts
@@ -695,30 +819,52 @@ int64_t workers(const FewSize& z)
     return need < most ? (need + 7) / 8 * 8 : most;
 }
 
-template <class F>
-auto with_few(int dim, bool second, F f)
+// Pages of fewer than 16 tokens, and rows gigabytes apart, have one kernel.
+// Second sixteens of rows make parts twice as large: eight waves a work-group
+// leave half as many parts, but half as many runs, which lose where each begins
+// and ends several units (5 tokens over 8000 keys, 2 sequences of 8 heads: 17.2
+// us against 20.6; 6 over up to 6007, 12 sequences: 20.9 against 23.0; 8 over
+// 2000: 15.4 against 17.4; 24 over 8000: 53.5 against 53.7; 32 over up to 4000:
+// 28.6 against 26.9; 100 over up to 2000: 42.2 against 35.4; 4 over up to 900:
+// 14.0 against 13.1).
+bool wide_groups(const FewSize& z)
 {
-    const auto by_dim = [&](auto r) {
+    return z.second && z.even && z.dim <= 128 && int64_t(z.seqs) * z.kv_heads <= 192 && z.max_kv > 1024;
+}
+
+template <class F>
+auto with_few(const FewSize& z, bool wide, F f)
+{
+    const auto by_dim = [&](auto r, auto even) {
         constexpr int R = decltype(r)::value;
-        switch (dim / kBlock) {
-        case 1: return f(Few<1, R>());
-        case 2: return f(Few<2, R>());
-        case 3: return f(Few<3, R>());
-        case 4: return f(Few<4, R>());
-        case 5: return f(Few<5, R>());
-        case 6: return f(Few<6, R>());
-        case 7: return f(Few<7, R>());
-        default: return f(Few<8, R>());
+        constexpr bool E = decltype(even)::value;
+        switch (z.dim / kBlock) {
+        case 1: return f(Few<1, R, E, 4>());
+        case 2: return f(Few<2, R, E, 4>());
+        case 3: return f(Few<3, R, E, 4>());
+        case 4: return f(Few<4, R, E, 4>());
+        case 5: return f(Few<5, R, E, 4>());
+        case 6: return f(Few<6, R, E, 4>());
+        case 7: return f(Few<7, R, E, 4>());
+        default: return f(Few<8, R, E, 4>());
         }
     };
-    return second ? by_dim(std::integral_constant<int, 2>()) : by_dim(std::integral_constant<int, 1>());
+    if (!z.even) return by_dim(std::integral_constant<int, 2>(), std::false_type());
+    if (!z.second) return by_dim(std::integral_constant<int, 1>(), std::true_type());
+    if (!wide) return by_dim(std::integral_constant<int, 2>(), std::true_type());
+    switch (z.dim / kBlock) {
+    case 1: return f(Few<1, 2, true, 8>());
+    case 2: return f(Few<2, 2, true, 8>());
+    case 3: return f(Few<3, 2, true, 8>());
+    default: return f(Few<4, 2, true, 8>());
+    }
 }
 
 }  // namespace
 
-size_t attention_few_bytes(const FewSize& z)
+static size_t few_bytes(const FewSize& z, bool wide)
 {
-    return with_few(z.dim, z.second, [&](auto shape) {
+    return with_few(z, wide, [&](auto shape) {
         using S = decltype(shape);
         static_assert(kComputeUnits * S::PER_CU * 4 <= kCounterBytes, "a count a run");
         static_assert(size_t(kComputeUnits) * S::PER_CU * 2 * S::SLOT < kNowhere - 4, "offsets of parts in 31 bits");
@@ -726,9 +872,14 @@ size_t attention_few_bytes(const FewSize& z)
     });
 }
 
+size_t attention_few_need(const FewSize& z) { return few_bytes(z, wide_groups(z)); }
+
+// (smaller calls may take the four waves, whose runs are as many or more)
+size_t attention_few_bytes(const FewSize& z) { return few_bytes(z, false); }
+
 hipError_t launch_attention_few(const FewSize& z, const void* args, hipStream_t s)
 {
-    return with_few(z.dim, z.second, [&](auto shape) {
+    return with_few(z, wide_groups(z), [&](auto shape) {
         using S = decltype(shape);
         static const hipError_t attr = [] {
             const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(few_rows_kernel<S>),
