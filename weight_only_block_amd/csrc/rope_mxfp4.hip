@@ -131,48 +131,164 @@ struct Angles {
     }
 };
 
-// A magnitude as an integer that orders as it does: the upper word of the fp64
-// number, and whether anything is set below it.
-__device__ __forceinline__ uint32_t magnitude(double x)
+// y in fp32, rounded to odd where it is not exact: a later rounding to fewer
+// bits, and a comparison with a number of fewer bits, go as those of y.
+__device__ __forceinline__ float to_odd(double y)
 {
-    const uint64_t b = uint64_t(__double_as_longlong(x));
-    return uint32_t(b >> 32) << 1 | (uint32_t(b) != 0 ? 1u : 0u);
+    const float f = float(y);
+    const double d = __builtin_fabs(double(f)), a = __builtin_fabs(y);
+    const uint32_t bits = __float_as_uint(f);
+    const uint32_t step = bits & 1 ? 0 : d < a ? 1 : d > a ? ~0u : 0;
+    return __uint_as_float(bits + step);
 }
 
-__device__ __forceinline__ uint32_t code_of(double x, int e)
+// A block's largest magnitude, as bits, to the exponent of its scale: 1.75 2^k
+// is 7 times 2^(k - 2).
+__device__ __forceinline__ int exponent_of(uint32_t most)
 {
-    const double y = __builtin_ldexp(x, -e);
-    const uint32_t m = magnitude(y);
-    const uint32_t size = (m > 0x3fd00000u * 2u ? 1 : 0) + (m >= 0x3fe80000u * 2u ? 1 : 0) + (m > 0x3ff40000u * 2u ? 1 : 0) +
-                          (m >= 0x3ffc0000u * 2u ? 1 : 0) + (m > 0x40040000u * 2u ? 1 : 0) + (m >= 0x400c0000u * 2u ? 1 : 0) +
-                          (m > 0x40140000u * 2u ? 1 : 0);
-    return size | uint32_t(uint64_t(__double_as_longlong(x)) >> 60 & 8);
+    const int e = int(most >> 23) - 127 - 2 + ((most & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return min(max(e, -125), 125);
 }
+__device__ __forceinline__ float scale_of(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
+__device__ __forceinline__ bool is_nan(uint32_t most) { return most > 0x7f800000u; }
+__device__ __forceinline__ uint32_t magnitude(float y) { return __float_as_uint(y) & 0x7fffffffu; }
+
+// The same value of the threads around: of the other in its pair, of the other
+// pair of its four, of the other four of its eight (where each four agree).
+__device__ __forceinline__ uint32_t most_of_four(uint32_t x)
+{
+    x = max(x, uint32_t(__builtin_amdgcn_mov_dpp(int(x), 0xb1, 0xf, 0xf, true)));
+    return max(x, uint32_t(__builtin_amdgcn_mov_dpp(int(x), 0x4e, 0xf, 0xf, true)));
+}
+__device__ __forceinline__ uint32_t other_four(uint32_t x) { return uint32_t(__builtin_amdgcn_mov_dpp(int(x), 0x141, 0xf, 0xf, true)); }
 
 // A thread's four elements into the cache, with the seven threads around it
 // that hold the rest of their block.
-__device__ __forceinline__ void store_block(const double* y, int d, uint8_t* codes, uint8_t* exponents)
+__device__ __forceinline__ void store_block(const double* x, int d, uint8_t* codes, uint8_t* exponents)
 {
+    float y[kRun];
     uint32_t most = 0;
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) most = max(most, magnitude(y[i]));
-#pragma unroll
-    for (int x = 1; x < kBlock / kRun; x <<= 1) most = max(most, uint32_t(__shfl_xor(int(most), x, 64)));
-    const bool nan = most > 0x7ff00000u * 2u;
-    // 1.75 2^k is 7 times the scale 2^(k - 2)
-    const int k = int(most >> 21) - 1023;
-    int e = k - 2 + ((most & 0x1fffffu) > 0x180000u ? 1 : 0);
-    e = min(max(e, -125), 125);
-    uint32_t word = 0;
-    if (!nan) {
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) word |= code_of(y[i], e) << (4 * i);
+    for (int i = 0; i < kRun; ++i) {
+        y[i] = to_odd(x[i]);
+        most = max(most, magnitude(y[i]));
     }
-    *reinterpret_cast<uint16_t*>(codes + d / 2) = uint16_t(word);
-    if (d % kBlock == 0) exponents[d / kBlock] = uint8_t(nan ? 255 : e + 127);
+    most = most_of_four(most);
+    most = max(most, other_four(most));
+    const int e = exponent_of(most);
+    uint32_t word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, y[0], y[1], scale_of(e), 0);
+    word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, y[2], y[3], scale_of(e), 1);
+    *reinterpret_cast<uint16_t*>(codes + d / 2) = uint16_t(is_nan(most) ? 0 : word);
+    if (d % kBlock == 0) exponents[d / kBlock] = uint8_t(is_nan(most) ? 255 : e + 127);
 }
 
-// A work-group takes rounds of heads of one token: first of queries, then of
+// Rows on 16 bytes, and pairs (i, i + rot_dim / 2) with rot_dim and the head in
+// whole 64s, or pairs of neighbours with rot_dim in whole 8s.  As rope.hip's
+// wide kernel: a thread holds one eighth-of-a-dimension place, two runs of four
+// elements, of every LANES-th head.  Runs that turn with one another lie in
+// blocks of eight threads each, runs of neighbours in one of four threads.  The
+// keys' angles in fp64 are worked out once a token, by one thread each.
+template <bool F32, bool INTER>
+__global__ __launch_bounds__(kThreads) void rope_append_mxfp4_wide(RopeParams p, BlockView blocks)
+{
+    __shared__ double angle[2][kMaxRotPairs];
+    const int64_t token = blockIdx.x;
+    const int dim = p.cache.head_dim, places = dim / 8;
+    const int lanes = kThreads / places;             // heads at a time
+    const int j = threadIdx.x % places, first = threadIdx.x / places + blockIdx.y * lanes;
+    const int kv_heads = p.cache.kv_heads, heads = p.q_heads + 2 * kv_heads;
+    const uint64_t pos = uint64_t(int64_t(p.pos[token]));
+    const int64_t slot = p.slots[token], page = slot >> p.cache.page_shift;
+    const bool live = slot >= 0 && page < p.cache.pages;
+    // (one round of heads a work-group, or all of them)
+    const int round = blockIdx.y;
+    const bool keys = live && (gridDim.y == 1 || (round >= p.q_heads / lanes && round <= (p.q_heads + kv_heads - 1) / lanes));
+    if (keys)
+        for (int i = threadIdx.x; i < p.rot_dim / 2; i += kThreads) turn(pos, p.turns[i], p.amplitude, &angle[0][i], &angle[1][i]);
+    const bool turns = 8 * j < p.rot_dim, split = turns && !INTER;
+    const int a = split ? 4 * j : 8 * j, b = split ? a + p.rot_dim / 2 : a + 4;
+    const int step = lanes * gridDim.y;
+    int head = first < int(blockIdx.y + 1) * lanes ? first : heads;     // (threads past the last place have none)
+    if (head < p.q_heads) {
+        float cs[4], sn[4];
+        if (turns) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) turn(pos, p.turns[4 * j + i], p.amplitude, &cs[i], &sn[i]);
+        }
+        for (; head < p.q_heads; head += step) {
+            const int64_t at = token * p.q_token + head * p.q_head;
+            float x[8], y[8];
+            load_run<F32>(p.q, at + a, x);
+            load_run<F32>(p.q, at + b, x + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = INTER ? 2 * i : i, o = INTER ? 2 * i + 1 : i + 4;
+                y[e] = turns ? __builtin_fmaf(x[e], cs[i], -(x[o] * sn[i])) : x[e];
+                y[o] = turns ? __builtin_fmaf(x[o], cs[i], x[e] * sn[i]) : x[o];
+            }
+            uint16_t* out = p.q_out + token * p.o_token + head * p.o_head;
+            bf16x4 u, v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = (__bf16)y[i], v[i] = (__bf16)y[4 + i];
+            *reinterpret_cast<bf16x4*>(out + a) = u;
+            *reinterpret_cast<bf16x4*>(out + b) = v;
+        }
+    }
+    if (!live) return;               // (all threads of the work-group)
+    if (keys) __syncthreads();
+    const int64_t row = slot & ((int64_t(1) << p.cache.page_shift) - 1);
+    const int64_t cell = (page * p.cache.page_stride + row * p.cache.slot_stride) / 2;
+    const int64_t block = page * blocks.page_stride + row * blocks.slot_stride;
+    for (; head < heads; head += step) {
+        const bool is_k = head < p.q_heads + kv_heads;
+        const int h = head - p.q_heads - (is_k ? 0 : kv_heads);
+        const void* src = is_k ? p.k : p.v;
+        const int64_t at = is_k ? token * p.k_token + h * p.k_head : token * p.v_token + h * p.v_head;
+        float x[8], y[8];
+        load_run<F32>(src, at + a, x);
+        load_run<F32>(src, at + b, x + 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = x[i];
+        if (turns && is_k) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = INTER ? 2 * i : i, o = INTER ? 2 * i + 1 : i + 4;
+                const double c = angle[0][4 * j + i], s = angle[1][4 * j + i], u = double(x[e]), v = double(x[o]);
+                y[e] = to_odd(__builtin_fma(u, c, -(v * s)));
+                y[o] = to_odd(__builtin_fma(v, c, u * s));
+            }
+        }
+        uint32_t most_a = 0, most_b = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) most_a = max(most_a, magnitude(y[i])), most_b = max(most_b, magnitude(y[4 + i]));
+        if (!split) most_a = most_b = max(most_a, most_b);
+        most_a = most_of_four(most_a);
+        most_b = most_of_four(most_b);
+        const uint32_t more_a = other_four(most_a), more_b = other_four(most_b);
+        if (split) most_a = max(most_a, more_a), most_b = max(most_b, more_b);
+        const int ea = exponent_of(most_a), eb = exponent_of(most_b);
+        uint32_t word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, y[0], y[1], scale_of(ea), 0);
+        word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, y[2], y[3], scale_of(ea), 1);
+        if (is_nan(most_a)) word = 0;
+        uint32_t more = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, y[4], y[5], scale_of(eb), 0);
+        more = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(more, y[6], y[7], scale_of(eb), 1);
+        if (is_nan(most_b)) more = 0;
+        const uint8_t byte_a = uint8_t(is_nan(most_a) ? 255 : ea + 127), byte_b = uint8_t(is_nan(most_b) ? 255 : eb + 127);
+        uint8_t* codes = (is_k ? p.cache.k : p.cache.v) + cell + h * (p.cache.head_stride / 2);
+        uint8_t* exponents = (is_k ? blocks.k : blocks.v) + block + h * blocks.head_stride;
+        if (split) {
+            *reinterpret_cast<uint16_t*>(codes + a / 2) = uint16_t(word);
+            *reinterpret_cast<uint16_t*>(codes + b / 2) = uint16_t(more);
+            if (j % 8 == 0) exponents[a / kBlock] = byte_a, exponents[b / kBlock] = byte_b;
+        } else {
+            *reinterpret_cast<uint32_t*>(codes + a / 2) = word | more << 16;
+            if (j % 4 == 0) exponents[a / kBlock] = byte_a;
+        }
+    }
+}
+
+// Any rot_dim, alignment and stride.  A thread holds four neighbours; a
+// work-group takes rounds of heads of one token: first of queries, then of
 // keys, then of values, as many heads a round as the threads hold.
 template <bool F32, bool INTER, bool WIDE>
 __global__ __launch_bounds__(kThreads) void rope_append_mxfp4(RopeParams p, BlockView blocks)
@@ -244,10 +360,17 @@ __global__ __launch_bounds__(kThreads) void rope_append_mxfp4(RopeParams p, Bloc
 }
 
 template <bool F32, bool INTER>
-void launch(const RopeParams& p, const BlockView& blocks, dim3 grid, hipStream_t s)
+void launch(const RopeParams& p, const BlockView& blocks, hipStream_t s)
 {
+    const int dim = p.cache.head_dim;
+    const bool eights = p.wide && (INTER ? p.rot_dim % 8 == 0 : p.rot_dim % 64 == 0 && dim % 64 == 0);
+    const int lanes = kThreads / (dim / (eights ? 8 : kRun)), kv = p.cache.kv_heads;
+    const int rounds = eights ? (p.q_heads + 2 * kv + lanes - 1) / lanes : (p.q_heads + lanes - 1) / lanes + 2 * ((kv + lanes - 1) / lanes);
+    // few tokens: a work-group a round; many: all rounds of a token share the angles
+    const dim3 grid(unsigned(p.tokens), p.tokens * rounds <= 1024 ? rounds : 1);
+    if (eights) hipLaunchKernelGGL((rope_append_mxfp4_wide<F32, INTER>), grid, dim3(kThreads), 0, s, p, blocks);
     // a run and its partners begin on a multiple of four dimensions
-    if (p.wide && p.rot_dim % 8 == 0) hipLaunchKernelGGL((rope_append_mxfp4<F32, INTER, true>), grid, dim3(kThreads), 0, s, p, blocks);
+    else if (p.wide && p.rot_dim % 8 == 0) hipLaunchKernelGGL((rope_append_mxfp4<F32, INTER, true>), grid, dim3(kThreads), 0, s, p, blocks);
     else hipLaunchKernelGGL((rope_append_mxfp4<F32, INTER, false>), grid, dim3(kThreads), 0, s, p, blocks);
 }
 
@@ -255,16 +378,12 @@ void launch(const RopeParams& p, const BlockView& blocks, dim3 grid, hipStream_t
 
 hipError_t launch_rope_mxfp4(const RopeParams& p, const BlockView& blocks, hipStream_t s)
 {
-    const int lanes = kThreads / (p.cache.head_dim / kRun);
-    const int rounds = (p.q_heads + lanes - 1) / lanes + 2 * ((p.cache.kv_heads + lanes - 1) / lanes);
-    // few tokens: a work-group a round; many: all rounds of a token share the angles
-    const dim3 grid(unsigned(p.tokens), p.tokens * rounds <= 1024 ? rounds : 1);
     if (p.f32) {
-        if (p.interleaved) launch<true, true>(p, blocks, grid, s);
-        else launch<true, false>(p, blocks, grid, s);
+        if (p.interleaved) launch<true, true>(p, blocks, s);
+        else launch<true, false>(p, blocks, s);
     } else {
-        if (p.interleaved) launch<false, true>(p, blocks, grid, s);
-        else launch<false, false>(p, blocks, grid, s);
+        if (p.interleaved) launch<false, true>(p, blocks, s);
+        else launch<false, false>(p, blocks, s);
     }
     return hipGetLastError();
 }
