@@ -29,7 +29,13 @@
 // same up to 32 rows and each streams key tiles of its own, joined in LDS at
 // the end; for single and drafted tokens, bound by reading the cache (two
 // sequences of 131072 bf16 keys, 1.07 GB: 174 us, 6.2 TB/s where a plain read
-// reaches 6.8; 32 ragged ones, 215 MB: 44 us).
+// reaches 6.8; 32 ragged ones, 215 MB: 44 us).  Over a 4-bit cache few rows have
+// kernels of their own (paged_attention_few.hip), and `Shared` tiles come by
+// registers: a thread loads a block of 32 codes and its exponent byte a tile
+// ahead, converts it (a value is exact in bf16; one conversion for all waves'
+// rows) and writes it to the tile.  2503 tokens over 16007 keys, 32 heads of
+// 128: 565 us, 1.07 PFLOP/s; 495 without the conversions and writes, 500 without
+// the softmax, neither of which hides behind the other's matrix products.
 //
 // Division of the work.  All units' key steps are laid out in one line, head
 // by head, and cut into equal runs, one per work-group, whatever the lengths
@@ -97,8 +103,10 @@ struct Shape {
     // bytes that is four, and half as many parts to join as with two (one
     // sequence of 32768 e4m3 keys: 30 us with two, 25 with four).
     static constexpr int W = SHARED ? SHARING : RB <= 128 ? 4 : DP == 256 && !E4M3 ? 1 : 2;
+    static_assert(SHARED || !MXFP4, "few rows over a 4-bit cache have kernels of their own");
     static constexpr int THREADS = 64 * W;
-    static constexpr int WAVES_PER_SIMD = DP <= 128 ? 2 : 1;
+    // (4-bit tiles of 64 dimensions: 161 registers, and LDS for three work-groups)
+    static constexpr int WAVES_PER_SIMD = MXFP4 && DP <= 64 && SHARING == 4 ? 3 : DP <= 128 ? 2 : 1;
     static constexpr int M = SHARED ? 32 * W : 32;                      // rows of a unit
     static constexpr int KT = SHARED && DP <= 128 ? 64 : 32;            // keys of a wave's tile
     static constexpr int BLOCKS = KT / 32;
@@ -109,11 +117,10 @@ struct Shape {
     static constexpr int RAW = SHARED ? KT / W : KT, ROWS = RAW < RPI ? RPI : RAW;   // rows a wave loads
     // tiles in LDS: two where two work-groups share a compute unit
     // (4-bit ones pass through registers, which hold the next tile)
-    static constexpr int STAGES = MXFP4 ? SHARED ? 2 : 1 : SHARED && (W == 8 || WAVES_PER_SIMD == 1) ? 4 : 2;
+    static constexpr int STAGES = SHARED && !MXFP4 && (W == 8 || WAVES_PER_SIMD == 1) ? 4 : 2;
     static constexpr int LOADS = ROWS / RPI;                            // for K, and as many for V
-    // 4-bit: blocks of a row, those of K and V that a thread loads of its work-group's or its wave's tile
-    static constexpr int NB = DP / kBlock, BLOCK_THREADS = SHARED ? THREADS : 64;
-    static constexpr int BLOCKS_EACH = (2 * KT * NB + BLOCK_THREADS - 1) / BLOCK_THREADS;
+    // 4-bit: blocks of a row, those of a tile's K and V that a thread loads
+    static constexpr int NB = DP / kBlock, BLOCKS_EACH = (2 * KT * NB + THREADS - 1) / THREADS;
     static constexpr int RING = STAGES * 2 * TILE * (SHARED ? 1 : W);   // stages of K and V
     static constexpr int OS = DP + 4;                                   // floats of a row in the joining buffer
     static constexpr int JOIN = SHARED ? 0 : W * M * OS * 4;
@@ -126,7 +133,8 @@ struct Shape {
     // Steps that a run has at least: a shorter one costs more in joining its
     // part than it saves.  What beginning and ending a unit costs, in steps.
     static constexpr int LEAST = SHARED ? 4 : 2;
-    static constexpr int EXTRA = SHARED ? 5 : 3;
+    // (of 4-bit tiles 3: 8 prompts of 300 tokens 31.4 us, 33.6 with 5)
+    static constexpr int EXTRA = SHARED && !MXFP4 ? 5 : 3;
     static constexpr float JOINED = SHARED ? 1.0f : 0.25f;               // what joining a part costs
     static constexpr int SLOT = SHARED ? W * (DP * 32 + 128) : M * DP + 2 * M;   // floats of a partial result
     static constexpr int STEPS = DP / 16;                               // products along the dimension
@@ -139,8 +147,11 @@ struct Shape {
     {
         return CPR == 4 ? (row >> 2) & 3 : CPR == 8 ? (row >> 1) & 7 : row & 15;
     }
+    // (4-bit rows are written by blocks, four a row: rows of a block differ in
+    // the chunk's low bits too)
     static __device__ __forceinline__ int v_swizzle(int row)
     {
+        if (MXFP4) return CPR == 8 ? ((row >> 1) & 1) << 2 | ((row >> 1) & 3) : (row & 3) << 2 | (row & 3);
         if (!E4M3) return CPR == 8 ? ((row >> 1) & 1) << 2 : (row & 3) << 2;
         return CPR == 4 ? ((row >> 3) & 1) << 1 : CPR == 8 ? (row & 2) | ((row >> 3) & 1) << 2
                                                           : (row & 3) << 1 | ((row >> 3) & 1) << 3;
@@ -504,34 +515,45 @@ struct Loader {
 };
 
 // A thread's part of a tile of a 4-bit cache, on its way through registers:
-// blocks x, x + BLOCK_THREADS, ... of the tile's K and then V, block by block
+// blocks x, x + THREADS, ... of the tile's K and then V, block by block
 // of a row and row by row.
 template <class S>
 struct Blocks {
     u32x4 codes[S::BLOCKS_EACH];
     uint32_t exponent[S::BLOCKS_EACH];
     int page[S::BLOCKS_EACH];           // -1: outside the sequence or the cache
+    int ahead[S::BLOCKS_EACH];          // of the next tile to load
 
     static constexpr int EACH = S::KT * S::NB;
 
     __device__ __forceinline__ static bool none(const Loader<S>& ld, int x)
     {
-        return (2 * EACH % S::BLOCK_THREADS != 0 && x >= 2 * EACH) || (!S::FULL && x % S::NB * kBlock >= ld.p.dim);
+        return (2 * EACH % S::THREADS != 0 && x >= 2 * EACH) || (!S::FULL && x % S::NB * kBlock >= ld.p.dim);
     }
 
-    // Begins the loads of the tile whose first key is k0.
+    // Looks up the pages of the tile whose first key is k0.
+    __device__ __forceinline__ void look_up(const Loader<S>& ld, int k0, int thread)
+    {
+#pragma unroll
+        for (int i = 0; i < S::BLOCKS_EACH; ++i) {
+            const int x = thread + i * S::THREADS;
+            ahead[i] = 0;
+            if (!none(ld, x)) ahead[i] = ld.list[((k0 + x % EACH / S::NB) >> ld.p.page_shift) - ld.first_page];
+        }
+    }
+
+    // Begins its loads.
     __device__ __forceinline__ void fetch(const Loader<S>& ld, int k0, int thread)
     {
         const int mask = (1 << ld.p.page_shift) - 1;
 #pragma unroll
         for (int i = 0; i < S::BLOCKS_EACH; ++i) {
-            const int x = thread + i * S::BLOCK_THREADS;
+            const int x = thread + i * S::THREADS;
             codes[i] = u32x4{0, 0, 0, 0};
             exponent[i] = 0;
-            page[i] = -1;
+            page[i] = ahead[i];
             if (none(ld, x)) continue;
             const int y = x % EACH, key = k0 + y / S::NB, b = y % S::NB;
-            page[i] = ld.list[(key >> ld.p.page_shift) - ld.first_page];
             const uint64_t id = uint32_t(max(0, page[i])), slot = uint32_t(key & mask);
             const bool v = x >= EACH;
             // (a generic pointer would make flat loads, waited for with those of LDS)
@@ -542,40 +564,44 @@ struct Blocks {
         }
     }
 
-    // Writes them to the tiles in LDS as bf16, which holds every value.  Rows
-    // outside [lo, hi) hold another's data and become zeros; keys of a page
-    // outside the cache become NaN.  A value that is NaN at a key that only some
-    // rows see would be NaN in the others too: it becomes 0, and rows that see
-    // it get it back at the end (restore).
-    __device__ __forceinline__ void land(const Loader<S>& ld, uint8_t* kt, uint8_t* vt, int k0, int thread) const
+    // Writes them to the tiles in LDS as bf16, which holds every value.
+    __device__ __forceinline__ void land(const Loader<S>& ld, uint8_t* kt, uint8_t* vt, int k0, int thread)
     {
+        bool special = k0 < ld.all_lo || k0 + S::KT > ld.all_hi;
+#pragma unroll
+        for (int i = 0; i < S::BLOCKS_EACH; ++i) special |= bool(__any(page[i] < 0));
+        if (special) {
+            // Rows outside [lo, hi) hold another's data and become zeros; keys of a
+            // page outside the cache become NaN.  A value that is NaN at a key that
+            // only some rows see would be NaN in the others too: it becomes 0, and
+            // rows that see it get it back at the end (restore).
+#pragma unroll
+            for (int i = 0; i < S::BLOCKS_EACH; ++i) {
+                const int x = thread + i * S::THREADS, key = k0 + x % EACH / S::NB;
+                const bool v = x >= EACH, lost = page[i] < 0;
+                const bool outside = key < ld.lo || key >= ld.hi, some = key < ld.all_lo || key >= ld.all_hi;
+                if (lost) exponent[i] = 255;
+                const bool nan = v && some && exponent[i] > 252 && !lost && !outside;
+                if (nan && !none(ld, x)) *ld.poisoned = 1;
+                if (outside || nan || (v && lost)) codes[i] = u32x4{0, 0, 0, 0}, exponent[i] = 0;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < S::BLOCKS_EACH; ++i) {
-            const int x = thread + i * S::BLOCK_THREADS;
+            const int x = thread + i * S::THREADS;
             if (none(ld, x)) continue;
-            const int y = x % EACH, row = y / S::NB, key = k0 + row, b = y % S::NB;
+            const int y = x % EACH, row = y / S::NB, b = y % S::NB;
             const bool v = x >= EACH;
-            const bool outside = key < ld.lo || key >= ld.hi, lost = page[i] < 0;
-            uint32_t e = lost ? 255 : exponent[i];
-            u32x4 c = codes[i];
-            if (outside || (v && lost)) {
-                c = u32x4{0, 0, 0, 0};
-                e = 0;
-            } else if (v && e > 252 && (key < ld.all_lo || key >= ld.all_hi)) {
-                c = u32x4{0, 0, 0, 0};
-                e = 0;
-                *ld.poisoned = 1;
-            }
-            const float scale = block_scale(e);
+            const float scale = block_scale(exponent[i]);
             const int swizzle = v ? S::v_swizzle(row) : S::k_swizzle(row);
             uint8_t* to = (v ? vt : kt) + row * S::RB;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 union { u32x4 u; bf16x2 p[4]; } a;
-                a.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], scale, 0);
-                a.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], scale, 1);
-                a.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], scale, 2);
-                a.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], scale, 3);
+                a.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i][j], scale, 0);
+                a.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i][j], scale, 1);
+                a.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i][j], scale, 2);
+                a.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes[i][j], scale, 3);
                 *reinterpret_cast<u32x4*>(to + (((4 * b + j) ^ swizzle) << 4)) = a.u;
             }
         }
@@ -888,20 +914,22 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
             }
             __syncthreads();
             if constexpr (S::MXFP4) {
-                // the next tile's loads run beside this one's products
-                const int thread = S::SHARED ? opaque(threadIdx.x) : ulane;
-                const int k1 = S::SHARED ? start : start + wave * S::KT;
-                const uint32_t ring = S::SHARED ? 0 : wave * 2 * S::TILE;
+                // The next tile's loads run beside this one's products, the pages
+                // of the one after are looked up before them.
+                const int thread = opaque(threadIdx.x);
                 Blocks<S> next;
-                next.fetch(ld, k1, thread);
+                next.look_up(ld, start, thread);
+                next.fetch(ld, start, thread);
+                if (n > 1) next.look_up(ld, start + S::STEP, thread);
                 for (int i = 0; i < n; ++i) {
-                    const int k0 = k1 + i * S::STEP;
-                    const uint32_t kt = ring + (i % S::STAGES) * 2 * S::TILE;
+                    const int k0 = start + i * S::STEP;
+                    const uint32_t kt = i % S::STAGES * 2 * S::TILE;
                     next.land(ld, lds + kt, lds + kt + S::TILE, k0, thread);
-                    if (i + 1 < n) next.fetch(ld, k0 + S::STEP, thread);
                     wait_lds();
-                    if (S::SHARED) __builtin_amdgcn_s_barrier();
+                    __builtin_amdgcn_s_barrier();
                     asm volatile("" ::: "memory");
+                    if (i + 1 < n) next.fetch(ld, k0 + S::STEP, thread);
+                    if (i + 2 < n) next.look_up(ld, k0 + 2 * S::STEP, thread);
                     run_tile(lds0 + kt, k0);
                     asm volatile("" ::: "memory");
                 }
