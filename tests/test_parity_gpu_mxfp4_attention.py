@@ -134,6 +134,57 @@ def test_chunks_of_many_rows(hq, hk, dim, chunk):
         assert ((lse[i].double() - want[1][0]).abs() <= lse_tol[0]).all()
 
 
+@pytest.mark.parametrize("hq,hk,dim", [(32, 8, 128), (24, 4, 64), (8, 2, 96), (20, 2, 32), (16, 8, 256)])
+@pytest.mark.parametrize("q_lens,kv_lens", [([5, 1, 6], [1500, 2000, 1030]), ([2] * 20, [1100 + 7 * i for i in range(20)])])
+def test_drafted_tokens_of_long_sequences(hq, hk, dim, q_lens, kv_lens):
+    # eight waves a work-group up to 192 (sequence, kv head) pairs
+    print("case", hq, hk, dim, q_lens, flush=True)
+    p = Problem(dim + len(q_lens), q_lens, kv_lens, hq, hk, dim, 16)
+    p.check(p.run())
+    p.check(p.run(window=400), window=400)
+
+
+@pytest.mark.parametrize("q_len,seqs,kv", [(1, 64, 20000), (1, 40, 70001), (5, 48, 20011)])
+def test_runs_of_many_steps(q_len, seqs, kv):
+    # a wave looks pages up for 32 steps at a time; all sequences read the same pages
+    p = Problem(q_len, [q_len], [kv], 8, 2, 128, 16)
+    single = p.run()
+    p.check(single)
+    q = p.q_dev.repeat(seqs, 1, 1)
+    out, lse = torch.empty_like(q), torch.empty(seqs * q_len, 8, device="cuda")
+    ws = torch.zeros(Q.paged_attention_workspace_size(p.cache, seqs * q_len, 8, seqs, q_len, kv), dtype=torch.uint8, device="cuda")
+    starts = torch.arange(0, (seqs + 1) * q_len, q_len, dtype=torch.int32, device="cuda")
+    lens = torch.full((seqs,), kv, dtype=torch.int32, device="cuda")
+    print("case", q_len, seqs, kv, flush=True)
+    Q.paged_attention(p.cache, q, out, starts, lens, p.dev[2].expand(seqs, -1).contiguous(), ws, q_len, kv, lse=lse)
+    torch.cuda.synchronize()
+    for b in range(seqs):
+        p.check((out[b * q_len:(b + 1) * q_len].cpu(), lse[b * q_len:(b + 1) * q_len].cpu()))
+
+
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_rows_far_apart(q_len):
+    # 2^24 bytes from one row of codes, and of exponent bytes, to the next
+    pages, page, dim, hk, kv = 3, 16, 64, 1, 44
+    big = [torch.empty(pages, hk, page, 1 << 24, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    p = Problem(21, [q_len], [kv], 4, hk, dim, page)
+    order = p.dev[2][0].long()
+    parts = []
+    for t, old, width in zip(big, (p.cache.k, p.cache.v, p.cache.k_scale, p.cache.v_scale), (dim // 2, dim // 2, 2, 2)):
+        view = t[..., :width]
+        view.copy_(old[order])
+        parts.append(view)
+    p.cache = Q.KVCache(*parts)
+    p.dev[2] = torch.arange(pages, dtype=torch.int32, device="cuda").view(1, -1)
+    got = p.run()
+    p.check(got)
+    back = [torch.empty(kv, hk, dim, device="cuda") for _ in range(2)]
+    Q.kv_read(p.cache, torch.arange(kv, device="cuda"), *back)
+    torch.cuda.synchronize()
+    for b, t in zip(back, (p.k, p.v)):
+        assert torch.equal(b.cpu().double(), t.transpose(1, 2)[order.cpu()].flatten(0, 1)[:kv])
+
+
 def test_scores_far_apart():
     # scores of some thousands: one key takes all the weight, nothing overflows
     p = Problem(5, [3, 1, 40], [333, 700, 90], 4, 2, 64, 16, magnitude=300.0)
