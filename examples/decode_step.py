@@ -2,7 +2,7 @@
 with cache append, attention over the paged cache, output projection, LM head
 and sampling, for a batch of sequences with prompts of different lengths.
 
-    python examples/decode_step.py [--steps 8] [--kv e4m3]
+    python examples/decode_step.py [--steps 8] [--kv e4m3|mxfp4]
 
 One layer of a 1024-wide model (16 query heads, 8 key/value heads of 128) with
 random Q8G64 weights and a small vocabulary; norms and the residual, which are
@@ -40,6 +40,9 @@ class Block:
         shape = (seqs * pages_each, KV_HEADS, PAGE, DIM)
         if kv == "bf16":
             self.cache = Q.KVCache(*[torch.zeros(shape, dtype=torch.bfloat16, device="cuda") for _ in range(2)])
+        elif kv == "mxfp4":
+            shapes = [shape[:3] + (DIM // 2,)] * 2 + [shape[:3] + (DIM // 32,)] * 2      # codes, exponent bytes
+            self.cache = Q.KVCache(*[torch.zeros(s, dtype=torch.uint8, device="cuda") for s in shapes])
         else:
             # keys and values of these weights are of the order of 10: 448 codes cover some 40
             scales = [torch.full((KV_HEADS,), 0.1, device="cuda") for _ in range(2)]
@@ -95,6 +98,15 @@ class Block:
         self.last = {"q": q, "out": out, "starts": starts, "len": self.len.clone()}
         return self.project(self.head, y.bfloat16())
 
+    def cached(self, seq: int, dtype=torch.bfloat16):
+        """Keys and values of one sequence as the cache holds them, [tokens][heads][dim]:
+        for another worker, or a cache of another type."""
+        i = torch.arange(int(self.len[seq]), device="cuda")
+        slots = self.table[seq, i // PAGE].long() * PAGE + i % PAGE
+        k, v = [torch.empty(len(i), KV_HEADS, DIM, dtype=dtype, device="cuda") for _ in range(2)]
+        Q.kv_read(self.cache, slots, k, v)
+        return k, v
+
     def sample(self, logits, u, **settings):
         idx = torch.empty(self.seqs, dtype=torch.int32, device="cuda")
         Q.sample_f32(logits, u, idx, self.sample_space, **settings)
@@ -123,7 +135,7 @@ def generate(block, prompts, steps, seed=0, watch=None):
 def main():
     args = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     args.add_argument("--steps", type=int, default=8)
-    args.add_argument("--kv", choices=("bf16", "e4m3"), default="bf16")
+    args.add_argument("--kv", choices=("bf16", "e4m3", "mxfp4"), default="bf16")
     opts = args.parse_args()
     lengths = [37, 5, 120, 64]
     block = Block(len(lengths), max(lengths) + opts.steps, opts.kv)
