@@ -84,7 +84,7 @@ def test_single_tokens(hq, hk, dim, page, kv_lens):
 
 
 @pytest.mark.parametrize("hq,hk,dim,page", [(8, 2, 128, 16), (7, 1, 64, 32), (4, 4, 96, 16), (2, 1, 256, 64), (3, 1, 96, 8),
-                                            (2, 2, 192, 1)])
+                                            (2, 2, 192, 1), (5, 1, 32, 16), (2, 1, 160, 16), (3, 1, 224, 4)])
 @pytest.mark.parametrize("q_lens,kv_lens", [
     ([5, 3, 1], [400, 3, 90]), ([0, 2, 0, 9], [10, 2, 0, 333]), ([7], [4]), ([70, 1, 33], [70, 500, 200]),
     ([130], [135]), ([1, 200, 0, 3, 64], [257, 300, 64, 1, 64])])
@@ -332,6 +332,24 @@ def test_replays_in_a_graph():
         eager = p.run(workspace=ws, max_kv=900)
         assert torch.equal(got, eager[0])
         p.check(eager)
+
+
+def test_two_streams_at_once():
+    # calls that overlap, each with a workspace of its own
+    problems = [Problem(70, [1] * 6, [900, 20, 3000, 1, 77, 512], 8, 2, 128, 16), Problem(71, [300, 2], [700, 4000], 8, 2, 128, 16),
+                Problem(72, [4] * 3, [4000, 1500, 90], 16, 2, 64, 16)]
+    want = [p.run() for p in problems]
+    streams = [torch.cuda.Stream() for _ in problems]
+    spaces = [torch.zeros(Q.paged_attention_workspace_size(p.cache, p.q_start[-1], p.hq, len(p.q_lens), p.max_q, p.max_kv),
+                          dtype=torch.uint8, device="cuda") for p in problems]
+    outs = [torch.empty(p.q_start[-1], p.hq, p.dim, dtype=torch.bfloat16, device="cuda") for p in problems]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for p, s, w, o in zip(problems, streams, spaces, outs):
+            Q.paged_attention(p.cache, p.q_dev, o, *p.dev, w, p.max_q, p.max_kv, stream=s)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o.cpu(), w[0])
 
 
 def test_offsets_past_32_bits():

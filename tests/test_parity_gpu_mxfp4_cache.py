@@ -167,6 +167,29 @@ def test_borders_zeros_and_special_values():
         assert torch.equal(mx.decode(a, got[i + 1][keep]).nan_to_num(nan=9e99), mx.decode(b, exps[keep]).nan_to_num(nan=9e99))
 
 
+def test_a_long_append_and_read():
+    # past 2^23 tokens a call goes in several launches
+    tokens, dim = (1 << 23) + 5, 32
+    g = torch.Generator(device="cuda").manual_seed(3)
+    row = torch.randn(1, 3, dim, generator=g, device="cuda").bfloat16()
+    src = row.expand(tokens, 3, dim)
+    parts = [torch.zeros(2, 1, 16, n, dtype=torch.uint8, device="cuda") for n in (dim // 2, dim // 2, 1, 1)]
+    cache = Q.KVCache(*parts)
+    slots = torch.full((tokens,), -1, dtype=torch.int64, device="cuda")
+    slots[0], slots[-1], slots[1 << 23] = 3, 20, 31
+    q_out = torch.full((tokens, 1, dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    Q.rope_append(cache, Q.Rope(dim), src[:, :1], src[:, 1:2], src[:, 2:], torch.zeros(tokens, dtype=torch.int32, device="cuda"),
+                  slots, q_out)
+    back = torch.full((tokens, 1, dim), 7.0, device="cuda")
+    Q.kv_read(cache, slots, v_out=back)
+    torch.cuda.synchronize()
+    want = mx.decode(*mx.encode(row[:, 2:].cpu().double()))[0]
+    assert (q_out == row[:, :1]).all()
+    for t in (0, 1 << 23, tokens - 1):
+        assert torch.equal(back[t].cpu().double(), want)
+    assert int((back != 7).any(-1).sum()) == 3
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "mxfp4"])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("tokens,hk,dim,page,strided", [(1, 1, 32, 1, 0), (3, 8, 128, 16, 0), (70, 2, 96, 4, 1),
@@ -181,6 +204,7 @@ def test_read(kind, dtype, tokens, hk, dim, page, strided):
         k, v = torch.randn(2, pages, hk, page, dim, generator=g).to({"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}[kind])
         k.view(torch.uint8)[0, 0, 0, 0] = 255              # NaN in either type (its low byte in bf16: an ordinary number)
         if kind == "bf16":
+            v[0, 0, 0, :8] = torch.tensor([1e-40, -1e-40, float("inf"), -float("inf"), float("nan"), 3e38, -0.0, 1e-38])
             cache = Q.KVCache(k.cuda(), v.cuda())
             want = [k.double(), v.double()]
         else:
