@@ -511,6 +511,17 @@ __device__ __forceinline__ void join_parts(float* slots, int first, int rest, in
     }
 }
 
+// One step of a wave's running sum and largest value: with what lies in the
+// lane that CTRL names, in the rows of lanes ROWS (elsewhere with zero).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ void scan_step(int64_t& sum, int& most)
+{
+    const uint32_t lo = uint32_t(__builtin_amdgcn_update_dpp(0, int(sum), CTRL, ROWS, 0xf, false));
+    const uint32_t hi = uint32_t(__builtin_amdgcn_update_dpp(0, int(sum >> 32), CTRL, ROWS, 0xf, false));
+    sum += int64_t(uint64_t(hi) << 32 | lo);
+    most = max(most, __builtin_amdgcn_update_dpp(0, most, CTRL, ROWS, 0xf, false));
+}
+
 template <class S>
 __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel(BlockArgs p)
 {
@@ -533,12 +544,13 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel
         longest = max(longest, cost);
     }
     int64_t upto = mine;
-#pragma unroll 1
-    for (int off = 1; off < 64; off <<= 1) {
-        const int64_t a = __shfl_up((long long)upto, off, 64);
-        if (lane >= off) upto += a;
-        longest = max(longest, __shfl_xor(longest, off, 64));
-    }
+    scan_step<0x111, 0xf>(upto, longest);      // lanes 1, 2, 4 and 8 before in their sixteen,
+    scan_step<0x112, 0xf>(upto, longest);
+    scan_step<0x114, 0xf>(upto, longest);
+    scan_step<0x118, 0xf>(upto, longest);
+    scan_step<0x142, 0xa>(upto, longest);      // the last of the sixteen before, of the half before
+    scan_step<0x143, 0xc>(upto, longest);
+    longest = __builtin_amdgcn_readlane(longest, 63);
     const auto of_lane = [](int64_t x, int l) {
         return int64_t(uint64_t(uint32_t(__builtin_amdgcn_readlane(int(x >> 32), l))) << 32 | uint32_t(__builtin_amdgcn_readlane(int(x), l)));
     };
@@ -755,19 +767,27 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel
                 }
                 __syncthreads();
                 if (*last_part) {
-                    // The unit's parts in run order, PARTS parts' loads at a time.
-                    // Past the last part they read nowhere: at a branch the loads
-                    // before it would be waited for.
+                    // The unit's parts, PARTS parts' loads at a time.  Past the last
+                    // part they read nowhere: at a branch the loads before it would
+                    // be waited for.  Many parts of few rows: groups of threads
+                    // take PARTS of them in turn, and their sums meet in LDS (one
+                    // sequence of 131072 keys: 33.4 us, 35.2 without).
                     const int parts = run_of(begin + S::EXTRA + u.steps - 1) - wf + 1;
                     // only the first can have begun in its run, all others continue one
                     const int slot0 = wf * 2 + (run_start(wf) > begin ? 0 : 1);
+                    const int items = rows * S::QUADS, log_items = 32 - __builtin_clz(items - 1);
+                    int groups = 1;
+                    while (S::R == 1 && groups * S::PARTS < parts && (groups * 2 << log_items) <= S::THREADS) groups *= 2;
+                    const int me = opaque(threadIdx.x), group = groups > 1 ? me >> log_items : 0;
+                    f32x4* sums = reinterpret_cast<f32x4*>(lds);               // [group][item]
+                    f32x2* refs = reinterpret_cast<f32x2*>(sums + S::THREADS);
 #pragma unroll 1
-                    for (int i = opaque(threadIdx.x); i < rows * S::QUADS; i += S::THREADS) {
+                    for (int i = groups > 1 ? me - (group << log_items) : me; i < items && group < groups; i += S::THREADS) {
                         const int row = i / S::QUADS, d = i % S::QUADS * 4;
                         float m = -INFINITY, l = 0.0f;
                         f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-                        for (int x = 0; x < parts; x += S::PARTS) {
+                        for (int x = group * S::PARTS; x < parts; x += groups * S::PARTS) {
                             f32x2 pm[S::PARTS];
                             f32x4 v[S::PARTS];
 #pragma unroll
@@ -794,7 +814,25 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel
                                 a += v[e] * share;
                             }
                         }
-                        put_out(row, d, a, m, l);
+                        if (groups == 1) put_out(row, d, a, m, l);
+                        else sums[me] = a, refs[me] = f32x2{m, l};
+                        if (groups > 1) break;
+                    }
+                    if (groups > 1) {
+                        __syncthreads();
+                        if (me < items) {
+                            f32x2 r = refs[me];
+                            f32x4 a = sums[me];
+#pragma unroll 1
+                            for (int x = 1; x < groups; ++x) {
+                                const f32x2 o = refs[me + (x << log_items)];
+                                const float mn = fmaxf(r[0], o[0]), ref = mn == -INFINITY ? 0.0f : mn;
+                                const float keep = __builtin_amdgcn_exp2f(r[0] - ref), share = __builtin_amdgcn_exp2f(o[0] - ref);
+                                r = f32x2{mn, r[1] * keep + o[1] * share};
+                                a = a * keep + sums[me + (x << log_items)] * share;
+                            }
+                            put_out(me / S::QUADS, me % S::QUADS * 4, a, r[0], r[1]);
+                        }
                     }
                 }
             }
