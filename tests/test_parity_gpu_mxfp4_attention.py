@@ -282,7 +282,7 @@ def test_calls_of_all_cache_types_share_a_workspace():
             assert torch.equal(got[0], want[i][0]) and torch.equal(got[1], want[i][1]), i
 
 
-@pytest.mark.parametrize("seqs", [128, 129, 300, 1100])
+@pytest.mark.parametrize("seqs", [63, 64, 65, 128, 129, 300, 1100])
 @pytest.mark.parametrize("chunks", [0, 1, 2])
 def test_many_sequences(seqs, chunks):
     # past 128 sequences lengths are read again for each unit; single tokens alone, with a few chunks, with long ones

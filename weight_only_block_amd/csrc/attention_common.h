@@ -100,6 +100,28 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b)
     return q;
 }
 
+// One step of a wave's running sum and largest value: with what lies in the
+// lane that CTRL names, in the rows of lanes ROWS (elsewhere with zero).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ void scan_step(int64_t& sum, int& most)
+{
+    const uint32_t lo = uint32_t(__builtin_amdgcn_update_dpp(0, int(sum), CTRL, ROWS, 0xf, false));
+    const uint32_t hi = uint32_t(__builtin_amdgcn_update_dpp(0, int(sum >> 32), CTRL, ROWS, 0xf, false));
+    sum += int64_t(uint64_t(hi) << 32 | lo);
+    most = max(most, __builtin_amdgcn_update_dpp(0, most, CTRL, ROWS, 0xf, false));
+}
+
+// The sum of the lanes up to each one, and the largest of them (none negative).
+__device__ __forceinline__ void scan_lanes(int64_t& sum, int& most)
+{
+    scan_step<0x111, 0xf>(sum, most);      // lanes 1, 2, 4 and 8 before in their sixteen,
+    scan_step<0x112, 0xf>(sum, most);
+    scan_step<0x114, 0xf>(sum, most);
+    scan_step<0x118, 0xf>(sum, most);
+    scan_step<0x142, 0xa>(sum, most);      // the last of the sixteen before, of the half before
+    scan_step<0x143, 0xc>(sum, most);
+}
+
 // The same value in every lane, in scalar registers.
 __device__ __forceinline__ int64_t uniform(int64_t x)
 {

@@ -125,7 +125,7 @@ struct Shape {
     static constexpr int OS = DP + 4;                                   // floats of a row in the joining buffer
     static constexpr int JOIN = SHARED ? 0 : W * M * OS * 4;
     static constexpr int BUFFER = RING > JOIN ? RING : JOIN;
-    static constexpr int LDS = BUFFER + kListPages * 4 + 2 * W * 32 * 4 + 64 + kListSeqs * 12;
+    static constexpr int LDS = BUFFER + kListPages * 4 + 2 * W * 32 * 4 + 64 + kListSeqs * (MXFP4 ? 16 : 12);
     // work-groups that a compute unit holds (160 KB of LDS, two waves of up to
     // 256 registers a SIMD or one of 512)
     static constexpr int BY_LDS = 160 * 1024 / LDS, BY_WAVES = 4 * WAVES_PER_SIMD / W;
@@ -692,7 +692,35 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
     // units: those of some sequences, or where sequences have many tiles and
     // fit the list, its share of all units.
     int b0, t0 = 0, mine_units = 0;
-    if (S::SHARED && p.seqs <= kListSeqs) {
+    if (S::MXFP4 && p.seqs <= kListSeqs) {
+        // Every wave sums the tiles of all sequences, two a lane, and each thread
+        // finds its first unit's sequence by halving (20 sequences in 4 us, in 6
+        // by going through them).
+        int* ends = reinterpret_cast<int*>(seqs + kListSeqs);
+        int before = 0;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int b = lane + 64 * half;
+            Seq s = {0, 0, 0};
+            if (b < p.seqs) s = load_seq(p, b);
+            int64_t upto = seq_tiles<S>(p, s);
+            int most = 0;
+            scan_lanes(upto, most);
+            if (wave == 0 && b < p.seqs) seqs[b] = s, ends[b] = before + int(upto);
+            before += __builtin_amdgcn_readlane(int(upto), 63);
+        }
+        __syncthreads();
+        const int per = (before + S::THREADS - 1) / S::THREADS, u0 = min(int(threadIdx.x) * per, before);
+        mine_units = min(per, before - u0);
+        int lo = 0, hi = p.seqs - 1;             // the first sequence that ends past u0 (or the last one)
+        while (lo < hi) {
+            const int middle = (lo + hi) / 2;
+            if (ends[middle] > u0) hi = middle;
+            else lo = middle + 1;
+        }
+        b0 = lo;
+        t0 = u0 - (lo > 0 ? ends[lo - 1] : 0);
+    } else if (S::SHARED && p.seqs <= kListSeqs) {
         for (int b = threadIdx.x; b < p.seqs; b += S::THREADS) seqs[b] = load_seq(p, b);
         __syncthreads();
         int units = 0;

@@ -7,8 +7,11 @@
 // parts and workspace these kernels share: a unit is (kv head, sequence) with
 // up to 16 R rows (tokens x query heads of the kv head), all units' steps lie
 // in one line, and each work-group takes an equal run of it.  What bounds it:
-// the cache's bytes on long contexts (three sequences of up to 131071 keys,
-// 400 MB: 74 us), and below some 10 us a chain of dependent accesses.
+// the cache's bytes on long contexts (three sequences of up to 131071 keys, 400
+// MB: 70 us, of which some 8 pass before the first keys arrive and while parts
+// are joined: 6.4 TB/s between, where a plain read reaches 6.8), and on short
+// ones a chain of dependent accesses (one sequence of 1023 keys: lengths, page
+// ids, keys, the parts' stores, their count and their join, 8.5 us).
 //
 // Products.  S^T = K Q^T and O^T = V^T P^T, 16x16x32.  Lane l holds of key
 // l % 16 the 8 T dimensions from 8 T (l / 16) on, as they lie in memory: a
@@ -18,8 +21,7 @@
 // lane's values have to be of one dimension and eight keys: they are written to
 // LDS as bf16 rows and read back through the transposing reads, keys in the
 // order that the scores' lanes hold them (4 g .. 4 g + 3 of two tiles of 16).
-// Every value is exact in bf16, 12% of a second fp32 product's worth of vector
-// instructions a tile.
+// Every value is exact in bf16.
 //
 // A wave works out the plan, looks up its pages (lane j holds the page of its
 // tile j) and streams its tiles without the work-group's other waves; they meet
@@ -223,11 +225,10 @@ struct Tile {
     {
         if constexpr (S::T == 8) return scales[t / 4];
         if constexpr (S::NS == 1) return scales[0];
+        // (loaded before the choice: a choice of addresses would put them in memory)
+        const float first = scales[0], second = scales[1], third = scales[S::NS - 1];
         const int b = (S::T * g + t) / 4 - S::T * g / 4;
-        float x = scales[0];
-#pragma unroll
-        for (int i = 1; i < S::NS; ++i) x = b >= i ? scales[i] : x;
-        return x;
+        return b == 0 ? first : b == 1 ? second : third;
     }
 
     __device__ __forceinline__ static bf16x8 values(uint32_t codes, float scale)
@@ -511,17 +512,6 @@ __device__ __forceinline__ void join_parts(float* slots, int first, int rest, in
     }
 }
 
-// One step of a wave's running sum and largest value: with what lies in the
-// lane that CTRL names, in the rows of lanes ROWS (elsewhere with zero).
-template <int CTRL, int ROWS>
-__device__ __forceinline__ void scan_step(int64_t& sum, int& most)
-{
-    const uint32_t lo = uint32_t(__builtin_amdgcn_update_dpp(0, int(sum), CTRL, ROWS, 0xf, false));
-    const uint32_t hi = uint32_t(__builtin_amdgcn_update_dpp(0, int(sum >> 32), CTRL, ROWS, 0xf, false));
-    sum += int64_t(uint64_t(hi) << 32 | lo);
-    most = max(most, __builtin_amdgcn_update_dpp(0, most, CTRL, ROWS, 0xf, false));
-}
-
 template <class S>
 __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel(BlockArgs p)
 {
@@ -544,12 +534,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel
         longest = max(longest, cost);
     }
     int64_t upto = mine;
-    scan_step<0x111, 0xf>(upto, longest);      // lanes 1, 2, 4 and 8 before in their sixteen,
-    scan_step<0x112, 0xf>(upto, longest);
-    scan_step<0x114, 0xf>(upto, longest);
-    scan_step<0x118, 0xf>(upto, longest);
-    scan_step<0x142, 0xa>(upto, longest);      // the last of the sixteen before, of the half before
-    scan_step<0x143, 0xc>(upto, longest);
+    scan_lanes(upto, longest);
     longest = __builtin_amdgcn_readlane(longest, 63);
     const auto of_lane = [](int64_t x, int l) {
         return int64_t(uint64_t(uint32_t(__builtin_amdgcn_readlane(int(x >> 32), l))) << 32 | uint32_t(__builtin_amdgcn_readlane(int(x), l)));
