@@ -9,11 +9,11 @@
 namespace qg {
 
 // What the kernels of few rows on a 4-bit cache are chosen and sized by:
-// `second`, more than 16 rows a sequence and kv head (up to 32); `even`, 16
-// keys of a tile lie in one page, and offsets within it in 32 bits.
+// `rows`, the most of a sequence and kv head; `even`, 16 keys of a tile lie in
+// one page, and offsets within it in 32 bits.
 struct FewSize {
-    int dim, kv_heads, seqs;
-    bool second, even;
+    int dim, kv_heads, seqs, rows;
+    bool even;
     int64_t max_kv;
 };
 size_t attention_few_need(const FewSize& z);    // of this shape

@@ -46,6 +46,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "attention_common.h"
@@ -64,6 +65,8 @@ constexpr int kListSeqs = 128;             // sequences whose lengths are kept i
 // with eight; 2048 over 8192: 262 and 250; 512 over 8192: 91 both; 128 over
 // 4096: 39 and 46.
 constexpr int64_t kManyRows = 2048;
+constexpr int64_t kFewRows = 512;         // of a sequence and kv head, see few_rows()
+constexpr double kFewWork = 2.4e8;         // row tiles times keys times dimensions
 
 __device__ __forceinline__ uint32_t lds_offset(const void* p)
 {
@@ -1258,12 +1261,26 @@ hipError_t run(const AttnParams& a, const BlockArgs& all, hipStream_t s)
 // Waves that share key tiles.  Up to 32 rows a sequence and kv head stream
 // the cache once either way: none (32 sequences of up to 9000 bf16 keys, 28
 // rows: 82 us, shared 90; a few short ones are faster shared, 36 and 28).
-// Over a 4-bit cache they have kernels of their own, by 16 rows: -1 up to 16.
-int sharing(const CacheView& cache, int64_t tokens, int64_t max_q, int group, int seqs)
+int sharing(int64_t tokens, int64_t max_q, int group, int seqs)
 {
-    if (cache.mxfp4 && max_q * group <= 16) return -1;
     if (max_q * group <= 32) return 0;
     return tokens * group >= kManyRows * seqs ? 8 : 4;
+}
+
+// Over a 4-bit cache few rows have kernels of their own, in tiles of 16 or 32
+// rows that each read the cache, the second and later ones from the last-level
+// cache.  They begin and end a unit sooner, and no row of a tile is left
+// without a token: up to 64 rows they are always faster (one sequence of 30000
+// keys, 42 rows: 25 us, shared 55; 32 of 8000: 40 and 50; 32 of 6000, 64 rows a
+// head of 8: 82 and 104), on up to 512 rows while a call is short (64 tokens
+// over 8192 keys, 256 rows: 27 and 39; 6 sequences of up to 95 tokens over up to
+// 2589 keys: 31 and 38; 96 rows, 16 sequences of 4000 keys, which this leaves
+// shared: 58 and 53).
+bool few_rows(const CacheView& cache, int64_t tokens, int64_t max_q, int group, int seqs, int64_t max_kv)
+{
+    const int64_t rows = max_q * group;
+    if (!cache.mxfp4 || rows > kFewRows) return false;
+    return rows <= 64 || double(tokens * group / 32 + seqs) * cache.kv_heads * double(max_kv) * cache.head_dim <= kFewWork;
 }
 
 // Calls f with the shape for a cache and a call's rows.
@@ -1295,10 +1312,10 @@ auto with_shape(const CacheView& cache, int waves, F f)
 
 namespace {
 
-FewSize few_size(const CacheView& cache, const BlockView& blocks, int waves, int seqs, int64_t max_kv)
+FewSize few_size(const CacheView& cache, const BlockView& blocks, int64_t rows, int seqs, int64_t max_kv)
 {
     const bool even = cache.page_shift >= 4 && cache.slot_stride < (int64_t(1) << 25) && blocks.slot_stride < (int64_t(1) << 24);
-    return {cache.head_dim, cache.kv_heads, seqs, waves == 0, even, max_kv};
+    return {cache.head_dim, cache.kv_heads, seqs, int(rows), even, max_kv};
 }
 
 size_t shared_bytes(const CacheView& cache, int waves, int64_t tokens, int group, int seqs, int64_t max_kv)
@@ -1314,9 +1331,10 @@ size_t attention_workspace_need(const CacheView& cache, const BlockView& blocks,
                                 int64_t max_q, int64_t max_kv)
 {
     const int group = q_heads / cache.kv_heads;
-    const int waves = sharing(cache, tokens, max_q < tokens ? max_q : tokens, group, seqs);
-    if (cache.mxfp4 && waves <= 0) return attention_few_need(few_size(cache, blocks, waves, seqs, max_kv));
-    return shared_bytes(cache, waves, tokens, group, seqs, max_kv);
+    if (max_q > tokens) max_q = tokens;
+    if (few_rows(cache, tokens, max_q, group, seqs, max_kv))
+        return attention_few_need(few_size(cache, blocks, max_q * group, seqs, max_kv));
+    return shared_bytes(cache, sharing(tokens, max_q, group, seqs), tokens, group, seqs, max_kv);
 }
 
 // The largest need of any shape within the bounds: each kernel shape's grows
@@ -1325,13 +1343,17 @@ size_t attention_workspace_bytes(const CacheView& cache, const BlockView& blocks
                                  int64_t max_q, int64_t max_kv)
 {
     const int group = q_heads / cache.kv_heads;
+    if (max_q > tokens) max_q = tokens;
     size_t most = 0;
-    for (int waves : {-1, 0, 4, 8}) {
-        if (waves > sharing(cache, tokens, max_q < tokens ? max_q : tokens, group, 1)) break;
-        if (waves < 0 && !cache.mxfp4) continue;
-        const size_t n = cache.mxfp4 && waves <= 0 ? attention_few_bytes(few_size(cache, blocks, waves, seqs, max_kv))
-                                                   : shared_bytes(cache, waves, tokens, group, seqs, max_kv);
-        if (n > most) most = n;
+    if (cache.mxfp4) {
+        for (int64_t rows : {int64_t(16), kFewRows})
+            most = std::max(most, attention_few_bytes(few_size(cache, blocks, std::min(rows, max_q * group), seqs, max_kv)));
+        // (no smaller call has more rows or more work)
+        if (few_rows(cache, tokens, max_q, group, seqs, max_kv)) return most;
+    }
+    for (int waves : {0, 4, 8}) {
+        if (waves > sharing(tokens, max_q, group, 1)) break;
+        if (waves > 0 || !cache.mxfp4) most = std::max(most, shared_bytes(cache, waves, tokens, group, seqs, max_kv));
     }
     return most;
 }
@@ -1378,9 +1400,9 @@ hipError_t launch_attention(const AttnParams& a, hipStream_t s)
     p.block_page = uint32_t(a.blocks.page_stride);
     p.block_head = uint32_t(a.blocks.head_stride);
     p.block_slot = uint32_t(a.blocks.slot_stride);
-    const int waves = sharing(a.cache, a.tokens, a.max_q, a.group, a.seqs);
-    if (a.cache.mxfp4 && waves <= 0)
-        return launch_attention_few(few_size(a.cache, a.blocks, waves, a.seqs, a.max_kv), &p, s);
+    if (few_rows(a.cache, a.tokens, a.max_q, a.group, a.seqs, a.max_kv))
+        return launch_attention_few(few_size(a.cache, a.blocks, a.max_q * a.group, a.seqs, a.max_kv), &p, s);
+    const int waves = sharing(a.tokens, a.max_q, a.group, a.seqs);
     return with_shape(a.cache, waves, [&](auto shape) { return run<decltype(shape)>(a, p, s); });
 }
 

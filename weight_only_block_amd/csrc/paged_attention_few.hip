@@ -1,12 +1,12 @@
-// Attention of few rows (single and drafted tokens) over a 4-bit paged cache,
-// on the matrix cores.
+// Attention of few rows (single and drafted tokens, short chunks) over a 4-bit
+// paged cache, on the matrix cores.
 //
 //   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q . k_j - m)
 //
 // with m a running reference, as in paged_attention.hip, whose line of work,
-// parts and workspace these kernels share: a unit is (kv head, sequence) with
-// up to 16 R rows (tokens x query heads of the kv head), all units' steps lie
-// in one line, and each work-group takes an equal run of it.  What bounds it:
+// parts and workspace these kernels share: a unit is (kv head, sequence, row
+// tile) with up to 16 R rows (tokens x query heads of the kv head), all units'
+// steps lie in one line, and each work-group takes an equal run of it.  What bounds it:
 // the cache's bytes on long contexts (three sequences of up to 131071 keys, 400
 // MB: 70 us, of which some 8 pass before the first keys arrive and while parts
 // are joined: 6.4 TB/s between, where a plain read reaches 6.8), and on short
@@ -49,10 +49,12 @@ constexpr int kAhead = 4;          // LDS reads ahead of their matrix products
 constexpr int kDeviceScope = 16, kOnce = 2;
 constexpr uint32_t kNowhere = 0x1fffffffu;   // floats: past every buffer below
 
-// 32 T dimensions, 16 R rows; EVEN: 16 keys of a tile lie in one page; W waves
-// a work-group.
-template <int T_, int R_, bool EVEN_, int W_>
+// 32 T dimensions, tiles of 16 R rows; EVEN: 16 keys of a tile lie in one page;
+// W waves a work-group; TILED: a sequence may have more than one tile of rows
+// (of its own, as it costs 0.3 to 0.7 us: 12 sequences of 24 rows 20.4 and 21.1).
+template <int T_, int R_, bool EVEN_, int W_, bool TILED_>
 struct Few {
+    static constexpr bool TILED = TILED_;
     static constexpr int T = T_, R = R_, DP = 32 * T;
     static constexpr bool EVEN = EVEN_;
     static constexpr int RB = T <= 2 ? 64 * T : T <= 4 ? 256 : 512;     // bytes of a row of V in LDS, a power of two
@@ -113,10 +115,17 @@ __device__ __forceinline__ Span make_span(const Args& p, const Seq& s)
     return x;
 }
 
+// Tiles of M rows, each a unit of its own.
+template <class S>
+__device__ __forceinline__ int tiles_of(const Args& p, const Seq& s)
+{
+    return !S::TILED ? 1 : int(uint32_t(s.n * p.group + S::M - 1) / S::M);
+}
+
 template <class S>
 __device__ __forceinline__ int cost_of(const Args& p, const Seq& s)
 {
-    return s.n > 0 ? make_span<S>(p, s).steps + S::EXTRA : 0;
+    return s.n > 0 ? tiles_of<S>(p, s) * (make_span<S>(p, s).steps + S::EXTRA) : 0;
 }
 
 // Where a sequence's keys lie for one kv head.
@@ -437,81 +446,6 @@ __device__ __forceinline__ f32x2 get2(float* base, uint32_t at)
     return __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(parts_buffer(base), at * 4, 0, kDeviceScope));
 }
 
-// Joins a unit's parts, the first at slot `first`, part x > 0 at slot rest + 2 x,
-// in an order that depends on their number and the rows alone.  A thread has
-// up to ITEMS times four values; the loads of PARTS parts, of all of them, are
-// in flight together, and what is past the rows or the parts reads nowhere (at
-// a branch the loads before it would be waited for).  Few rows: groups of
-// threads take PARTS parts in turn, and their sums meet in LDS.
-template <class S, class F>
-__device__ __forceinline__ void join_parts(float* slots, int first, int rest, int parts, int rows, uint8_t* lds, F out)
-{
-    const int tid = opaque(threadIdx.x), items = rows * S::QUADS;
-    int groups = 1;
-    while (items * groups * 2 <= S::THREADS && groups * S::PARTS < parts) groups *= 2;
-    const int group = groups > 1 ? tid / items : 0, item = tid - group * items;
-    f32x4 a[S::ITEMS];
-    float m[S::ITEMS], l[S::ITEMS];
-#pragma unroll
-    for (int i = 0; i < S::ITEMS; ++i) a[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f}, m[i] = -INFINITY, l[i] = 0.0f;
-#pragma unroll 1
-    for (int x = group * S::PARTS; x < (group < groups ? parts : 0); x += groups * S::PARTS) {
-        f32x2 pm[S::ITEMS][S::PARTS];
-        f32x4 v[S::ITEMS][S::PARTS];
-#pragma unroll
-        for (int e = 0; e < S::PARTS; ++e) {
-            const uint32_t from = uint32_t(x + e ? rest + 2 * (x + e) : first) * S::SLOT;
-#pragma unroll
-            for (int i = 0; i < S::ITEMS; ++i) {
-                const int at = item + i * S::THREADS;
-                const bool none = x + e >= parts || at >= items;
-                pm[i][e] = get2(slots, none ? kNowhere : from + S::M * S::DP + 2 * (at / S::QUADS));
-                v[i][e] = get4(slots, none ? kNowhere : from + at * 4);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < S::ITEMS; ++i) {
-            float mn = m[i];
-#pragma unroll
-            for (int e = 0; e < S::PARTS; ++e) {
-                if (x + e >= parts) pm[i][e][0] = -INFINITY;
-                mn = fmaxf(mn, pm[i][e][0]);
-            }
-            const float ref = mn == -INFINITY ? 0.0f : mn, keep = __builtin_amdgcn_exp2f(m[i] - ref);
-            m[i] = mn;
-            l[i] *= keep;
-            a[i] *= keep;
-#pragma unroll
-            for (int e = 0; e < S::PARTS; ++e) {
-                const float share = __builtin_amdgcn_exp2f(pm[i][e][0] - ref);
-                l[i] += pm[i][e][1] * share;
-                a[i] += v[i][e] * share;
-            }
-        }
-    }
-    if (groups > 1) {
-        f32x4* sums = reinterpret_cast<f32x4*>(lds);                   // [groups][items]
-        f32x2* refs = reinterpret_cast<f32x2*>(sums + S::THREADS);
-        if (group < groups) sums[tid] = a[0], refs[tid] = f32x2{m[0], l[0]};
-        __syncthreads();
-        if (group > 0) return;
-#pragma unroll 1
-        for (int e = 1; e < groups; ++e) {
-            const f32x2 r = refs[e * items + item];
-            const float mn = fmaxf(m[0], r[0]), ref = mn == -INFINITY ? 0.0f : mn;
-            const float keep = __builtin_amdgcn_exp2f(m[0] - ref), share = __builtin_amdgcn_exp2f(r[0] - ref);
-            m[0] = mn;
-            l[0] = l[0] * keep + r[1] * share;
-            a[0] = a[0] * keep + sums[e * items + item] * share;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < S::ITEMS; ++i) {
-        const int at = item + i * S::THREADS;
-        if (at < items) out(at / S::QUADS, at % S::QUADS * 4, a[i], m[i], l[i]);
-    }
-}
-
 template <class S>
 __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel(BlockArgs p)
 {
@@ -574,7 +508,9 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel
     int64_t left = r - of_lane(upto - mine, owner);
     Seq s = get_seq(b);
     for (int cost; left >= (cost = cost_of<S>(p, s)); s = get_seq(++b)) left -= cost;
-    int off = int(left);
+    int tile = 0, off = int(left);
+    if (S::TILED)
+        for (const int unit = make_span<S>(p, s).steps + S::EXTRA; off >= unit; ++tile) off -= unit;
 
     while (true) {
         s.q0 = __builtin_amdgcn_readfirstlane(s.q0);
@@ -585,7 +521,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel
         const int from = max(0, off - S::EXTRA), count = max(0, off + take - S::EXTRA) - from;
         if (count > 0) {       // (else only what stands for the unit's beginning)
             const int ulane = opaque(lane), col = ulane & 15, g = ulane >> 4;
-            const int rows = s.n * p.group;
+            const int row0 = S::TILED ? tile * S::M : 0, rows = min(S::M, s.n * p.group - row0);
             Place place{p, p.table + uint64_t(uint32_t(b)) * p.table_stride, 0, 0, 0, 0, 0};
             place.pages = int((uint32_t(s.kv) + (1u << p.page_shift) - 1) >> p.page_shift);
             const uint64_t head_bytes = uint64_t(uint32_t(kvh)) * p.head16 << 4, head_blocks = uint64_t(uint32_t(kvh)) * p.block_head;
@@ -607,7 +543,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel
 #pragma unroll
             for (int x = 0; x < S::R; ++x) {
                 // rows past the last repeat it and are never written
-                const uint32_t row = uint32_t(min(16 * x + col, rows - 1)), step = by_group(p, row);
+                const uint32_t row = uint32_t(row0 + min(16 * x + col, rows - 1)), step = by_group(p, row);
                 const uint32_t head = uint32_t(kvh) * uint32_t(p.group) + (row - step * uint32_t(p.group));
                 const uint16_t* qrow = p.q + uint64_t(uint32_t(s.q0) + step) * p.q_token + uint64_t(head) * p.q_head + 8 * S::T * g;
                 const int pos = s.kv - s.n + int(step);
@@ -665,10 +601,10 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel
                 if (live) accumulate<S>(st, sc, masked, vt, k0, c, ulane);
                 asm volatile("" ::: "memory");
             };
-            Tile<S> tile;
-            if (n > 0) fetch(tile, 0);
+            Tile<S> keys_values;
+            if (n > 0) fetch(keys_values, 0);
 #pragma unroll 1
-            for (int i = 0; i < n; ++i) step(tile, i);
+            for (int i = 0; i < n; ++i) step(keys_values, i);
             if (poisoned) restore<S>(st, place, u, u.base + from * S::STEP, u.base + (from + count) * S::STEP, wave);
 
             // ---- the waves' sums meet in LDS; whole units go to the output, parts
@@ -678,8 +614,8 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel
             float* slots = reinterpret_cast<float*>(p.workspace + kCounterBytes);
             const uint32_t slot = uint32_t(run * 2 + (off > 0 ? 0 : 1)) * S::SLOT;
             const auto put_out = [&](int row, int d, f32x4 a, float m, float l) {
-                const uint32_t step = by_group(p, uint32_t(row));
-                const uint32_t head = uint32_t(kvh) * uint32_t(p.group) + (uint32_t(row) - step * uint32_t(p.group));
+                const uint32_t step = by_group(p, uint32_t(row0 + row));
+                const uint32_t head = uint32_t(kvh) * uint32_t(p.group) + (uint32_t(row0 + row) - step * uint32_t(p.group));
                 // rows that see nothing have l = 0 and o = 0
                 a *= l == 0.0f ? 0.0f : 1.0f / l;
                 uint16_t* o = p.out + uint64_t(uint32_t(s.q0) + step) * p.o_token + uint64_t(head) * p.o_head + d;
@@ -826,6 +762,10 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel
         at += take;
         if (at >= end) break;
         off = 0;
+        if (S::TILED) {
+            if (++tile < tiles_of<S>(p, s)) continue;
+            tile = 0;
+        }
         do {
             if (++b == p.seqs) b = 0, ++kvh;
             s = get_seq(b);
@@ -836,7 +776,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel
 template <class S>
 int64_t workers(const FewSize& z)
 {
-    const int64_t units = int64_t(z.seqs) * z.kv_heads;
+    const int64_t units = int64_t(z.seqs) * z.kv_heads * ((z.rows + S::M - 1) / S::M);
     const int64_t steps = (z.max_kv + 15 + S::STEP - 1) / S::STEP + 1 + S::EXTRA;
     const int64_t most = kComputeUnits * S::PER_CU, need = units * steps / S::LEAST + 1;
     return need < most ? (need + 7) / 8 * 8 : most;
@@ -849,38 +789,43 @@ int64_t workers(const FewSize& z)
 // us against 20.6; 6 over up to 6007, 12 sequences: 20.9 against 23.0; 8 over
 // 2000: 15.4 against 17.4; 24 over 8000: 53.5 against 53.7; 32 over up to 4000:
 // 28.6 against 26.9; 100 over up to 2000: 42.2 against 35.4; 4 over up to 900:
-// 14.0 against 13.1).
+// 14.0 against 13.1), with several tiles of rows as with one (48 rows, 16
+// sequences of 4000 keys and 8 heads: 33.0 against 42.2).
 bool wide_groups(const FewSize& z)
 {
-    return z.second && z.even && z.dim <= 128 && int64_t(z.seqs) * z.kv_heads <= 192 && z.max_kv > 1024;
+    return z.rows > 16 && z.even && z.dim <= 128 && int64_t(z.seqs) * z.kv_heads <= 192 && z.max_kv > 1024;
 }
 
 template <class F>
 auto with_few(const FewSize& z, bool wide, F f)
 {
-    const auto by_dim = [&](auto r, auto even) {
+    const auto by_dim = [&](auto r, auto even, auto tiled) {
         constexpr int R = decltype(r)::value;
-        constexpr bool E = decltype(even)::value;
+        constexpr bool E = decltype(even)::value, TILED = decltype(tiled)::value;
         switch (z.dim / kBlock) {
-        case 1: return f(Few<1, R, E, 4>());
-        case 2: return f(Few<2, R, E, 4>());
-        case 3: return f(Few<3, R, E, 4>());
-        case 4: return f(Few<4, R, E, 4>());
-        case 5: return f(Few<5, R, E, 4>());
-        case 6: return f(Few<6, R, E, 4>());
-        case 7: return f(Few<7, R, E, 4>());
-        default: return f(Few<8, R, E, 4>());
+        case 1: return f(Few<1, R, E, 4, TILED>());
+        case 2: return f(Few<2, R, E, 4, TILED>());
+        case 3: return f(Few<3, R, E, 4, TILED>());
+        case 4: return f(Few<4, R, E, 4, TILED>());
+        case 5: return f(Few<5, R, E, 4, TILED>());
+        case 6: return f(Few<6, R, E, 4, TILED>());
+        case 7: return f(Few<7, R, E, 4, TILED>());
+        default: return f(Few<8, R, E, 4, TILED>());
         }
     };
-    if (!z.even) return by_dim(std::integral_constant<int, 2>(), std::false_type());
-    if (!z.second) return by_dim(std::integral_constant<int, 1>(), std::true_type());
-    if (!wide) return by_dim(std::integral_constant<int, 2>(), std::true_type());
-    switch (z.dim / kBlock) {
-    case 1: return f(Few<1, 2, true, 8>());
-    case 2: return f(Few<2, 2, true, 8>());
-    case 3: return f(Few<3, 2, true, 8>());
-    default: return f(Few<4, 2, true, 8>());
-    }
+    const auto by_rows = [&](auto tiled) {
+        constexpr bool TILED = decltype(tiled)::value;
+        if (!wide) return by_dim(std::integral_constant<int, 2>(), std::true_type(), tiled);
+        switch (z.dim / kBlock) {
+        case 1: return f(Few<1, 2, true, 8, TILED>());
+        case 2: return f(Few<2, 2, true, 8, TILED>());
+        case 3: return f(Few<3, 2, true, 8, TILED>());
+        default: return f(Few<4, 2, true, 8, TILED>());
+        }
+    };
+    if (!z.even) return by_dim(std::integral_constant<int, 2>(), std::false_type(), std::true_type());
+    if (z.rows <= 16) return by_dim(std::integral_constant<int, 1>(), std::true_type(), std::false_type());
+    return z.rows <= 32 ? by_rows(std::false_type()) : by_rows(std::true_type());
 }
 
 }  // namespace
