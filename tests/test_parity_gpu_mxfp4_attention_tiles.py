@@ -47,6 +47,17 @@ def test_head_dimensions_and_pages(dim, page, q_lens, kv_lens):
         p.check(got)
 
 
+@pytest.mark.parametrize("dim,page", [(160, 16), (192, 1), (224, 32), (256, 16), (256, 4)])
+@pytest.mark.parametrize("q_lens,kv_lens,window", [([300], [340], 0), ([230, 0, 300], [1000, 20, 300], 0), ([300], [900], 45),
+                                                   ([520, 1], [521, 300], 0)])
+def test_wide_heads_of_many_rows(dim, page, q_lens, kv_lens, window):
+    # past 1024 rows a sequence eight waves share a tile, which read most of their queries from LDS
+    p = Problem(dim + page, q_lens, kv_lens, 5, 1, dim, page, nhd=page == 16)
+    print("case", dim, page, q_lens, window, flush=True)
+    for scale in (0.05, -0.05):
+        p.check(p.run(window=window, scale=scale), window=window, scale=scale)
+
+
 @pytest.mark.parametrize("window", [1, 2, 17, 64, 100, 10000])
 @pytest.mark.parametrize("q_lens,kv_lens", [([30, 1], [300, 65]), ([44, 9, 0, 1], [45, 65, 0, 700])])
 def test_windows(window, q_lens, kv_lens):

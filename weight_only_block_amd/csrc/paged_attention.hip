@@ -63,8 +63,11 @@ constexpr int kListSeqs = 128;             // sequences whose lengths are kept i
 // of four: 256 rows to a tile halve its reads, but a unit's beginning and end
 // cost more.  4099 tokens over 12301 keys (16396 rows): 735 us with four, 655
 // with eight; 2048 over 8192: 262 and 250; 512 over 8192: 91 both; 128 over
-// 4096: 39 and 46.
-constexpr int64_t kManyRows = 2048;
+// 4096: 39 and 46.  Over a 4-bit cache with more than 128 dimensions only eight
+// leave a SIMD two waves: 300 tokens over 9000 keys (1200 rows) 161 us with
+// four, 138 with eight; 700 over 6000 (1400 rows) 122 and 117; 260 over 4000
+// (520 rows) 66 and 95.
+constexpr int64_t kManyRows = 2048, kManyWideRows = 1024;
 constexpr int64_t kFewRows = 512;         // of a sequence and kv head, see few_rows()
 constexpr double kFewWork = 2.4e8;         // row tiles times keys times dimensions
 
@@ -108,10 +111,15 @@ struct Shape {
     static constexpr int W = SHARED ? SHARING : RB <= 128 ? 4 : DP == 256 && !E4M3 ? 1 : 2;
     static_assert(SHARED || !MXFP4, "few rows over a 4-bit cache have kernels of their own");
     static constexpr int THREADS = 64 * W;
+    // WIDE: a SIMD's two waves of 256 dimensions have registers for 6 of their 16
+    // query fragments, LDS holds the others (2000 tokens over 4000 keys, 16 heads:
+    // 134 us, 185 with one wave of 512 registers a SIMD, 201 with its tiles of 32
+    // keys; 146 with four reads ahead, whose registers spill)
+    static constexpr bool WIDE = MXFP4 && DP == 256 && SHARING == 8;
     // (4-bit tiles of 64 dimensions: 161 registers, and LDS for three work-groups)
-    static constexpr int WAVES_PER_SIMD = MXFP4 && DP <= 64 && SHARING == 4 ? 3 : DP <= 128 ? 2 : 1;
+    static constexpr int WAVES_PER_SIMD = MXFP4 && DP <= 64 && SHARING == 4 ? 3 : DP <= 128 || WIDE ? 2 : 1;
     static constexpr int M = SHARED ? 32 * W : 32;                      // rows of a unit
-    static constexpr int KT = SHARED && DP <= 128 ? 64 : 32;            // keys of a wave's tile
+    static constexpr int KT = SHARED && (DP <= 128 || (MXFP4 && !WIDE)) ? 64 : 32;   // keys of a wave's tile
     static constexpr int BLOCKS = KT / 32;
     static constexpr int STEP = SHARED ? KT : KT * W;                   // keys of a work-group's step
     static constexpr int CPR = RB / 16;                                 // 16-byte chunks of it
@@ -122,13 +130,16 @@ struct Shape {
     // (4-bit ones pass through registers, which hold the next tile)
     static constexpr int STAGES = SHARED && !MXFP4 && (W == 8 || WAVES_PER_SIMD == 1) ? 4 : 2;
     static constexpr int LOADS = ROWS / RPI;                            // for K, and as many for V
+    static constexpr int STEPS = DP / 16;                               // products along the dimension
+    static constexpr int QREG = WIDE ? 6 : STEPS, QUERIES = W * (STEPS - QREG) * 1024;   // and bytes in LDS
+    static constexpr int AHEAD = WIDE ? 2 : kAhead;                     // as kAhead, of K and of these
     // 4-bit: blocks of a row, those of a tile's K and V that a thread loads
     static constexpr int NB = DP / kBlock, BLOCKS_EACH = (2 * KT * NB + THREADS - 1) / THREADS;
     static constexpr int RING = STAGES * 2 * TILE * (SHARED ? 1 : W);   // stages of K and V
     static constexpr int OS = DP + 4;                                   // floats of a row in the joining buffer
     static constexpr int JOIN = SHARED ? 0 : W * M * OS * 4;
     static constexpr int BUFFER = RING > JOIN ? RING : JOIN;
-    static constexpr int LDS = BUFFER + kListPages * 4 + 2 * W * 32 * 4 + 64 + kListSeqs * (MXFP4 ? 16 : 12);
+    static constexpr int LDS = BUFFER + kListPages * 4 + 2 * W * 32 * 4 + 64 + kListSeqs * (MXFP4 ? 16 : 12) + QUERIES;
     // work-groups that a compute unit holds (160 KB of LDS, two waves of up to
     // 256 registers a SIMD or one of 512)
     static constexpr int BY_LDS = 160 * 1024 / LDS, BY_WAVES = 4 * WAVES_PER_SIMD / W;
@@ -140,7 +151,6 @@ struct Shape {
     static constexpr int EXTRA = SHARED && !MXFP4 ? 5 : 3;
     static constexpr float JOINED = SHARED ? 1.0f : 0.25f;               // what joining a part costs
     static constexpr int SLOT = SHARED ? W * (DP * 32 + 128) : M * DP + 2 * M;   // floats of a partial result
-    static constexpr int STEPS = DP / 16;                               // products along the dimension
     static constexpr int DB = DP / 32;
 
     // Swizzles: the chunk of a row's 16 bytes is moved so that what 32 lanes of
@@ -220,7 +230,7 @@ struct Probs {
 
 // Scores of a key tile (32 or 64 keys) for the wave's rows.
 template <class S>
-__device__ __forceinline__ void scores(const State<S>& st, Scores<S>& sc, const uint8_t* kt, int lane)
+__device__ __forceinline__ void scores(const State<S>& st, Scores<S>& sc, const uint8_t* kt, const uint8_t* queries, int lane)
 {
     const int col = lane & 31, h = lane >> 5;
 #pragma unroll
@@ -230,23 +240,25 @@ __device__ __forceinline__ void scores(const State<S>& st, Scores<S>& sc, const 
     const int ksw = S::k_swizzle(col);
     const uint8_t* row = kt + col * S::RB;
     // Blocks alternate, so that a product does not wait on the one before it.
-    // Reads run kAhead products ahead: left to itself the compiler puts each
+    // Reads run AHEAD products ahead: left to itself the compiler puts each
     // next to its product, which then waits for it.
     constexpr int READS = S::E4M3 ? S::STEPS / 2 * S::BLOCKS : S::STEPS * S::BLOCKS;
-    u32x4 f[READS];
+    u32x4 f[READS], q[S::STEPS];
     const auto read = [&](int i) {
         const int t = i / S::BLOCKS, b = i % S::BLOCKS;
         f[i] = *reinterpret_cast<const u32x4*>(row + b * 32 * S::RB + (((2 * t + h) ^ ksw) << 4));
+        if (b == 0 && t >= S::QREG) q[t] = *reinterpret_cast<const u32x4*>(queries + (t - S::QREG) * 1024 + lane * 16);
     };
 #pragma unroll
-    for (int i = 0; i < (kAhead < READS ? kAhead : READS); ++i) read(i);
+    for (int i = 0; i < (S::AHEAD < READS ? S::AHEAD : READS); ++i) read(i);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < READS; ++i) {
         const int t = i / S::BLOCKS, b = i % S::BLOCKS;
-        if (i + kAhead < READS) read(i + kAhead);
+        if (i + S::AHEAD < READS) read(i + S::AHEAD);
         if (!S::E4M3) {
-            sc.s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, f[i]), st.q[t], sc.s[b], 0, 0, 0);
+            sc.s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, f[i]),
+                                                              t < S::QREG ? st.q[t] : __builtin_bit_cast(bf16x8, q[t]), sc.s[b], 0, 0, 0);
         } else {
             // one 16-byte read is two steps: step 2 t + e takes dimensions 32 t + 16 h + 8 e on
 #pragma unroll
@@ -399,12 +411,12 @@ __device__ __forceinline__ void output(State<S>& st, const Probs<S>& pb, Values<
 // A key tile (K and V, 32 or 64 keys from k0) against the wave's rows.
 // `masked`: some row does not see some key.
 template <class S>
-__device__ __forceinline__ void compute(State<S>& st, const uint8_t* kt, const uint8_t* vt, int k0, float c, bool masked,
-                                        int lane)
+__device__ __forceinline__ void compute(State<S>& st, const uint8_t* kt, const uint8_t* vt, const uint8_t* queries, int k0, float c,
+                                        bool masked, int lane)
 {
     Scores<S> sc;
     Probs<S> pb;
-    scores<S>(st, sc, kt, lane);
+    scores<S>(st, sc, kt, queries, lane);
     Values<S> v(vt, lane);
     v.begin();
     if (masked) mask<S>(st, sc, k0, lane);
@@ -767,7 +779,11 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
         return false;
     });
     int64_t upto = mine;
-    for (int off = 1; off < 64; off <<= 1) {
+    if (S::MXFP4) {
+        scan_lanes(upto, longest);
+        longest = __builtin_amdgcn_readlane(longest, 63);
+    }
+    for (int off = 1; off < 64 && !S::MXFP4; off <<= 1) {
         const int64_t a = __shfl_up((long long)upto, off, 64);
         if (lane >= off) upto += a;
         longest = max(longest, __shfl_xor(longest, off, 64));
@@ -922,11 +938,15 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void attention_kerne
             for (int t = 0; t < S::STEPS; ++t) st.q[t] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, st.q[t]) ^ 0x80008000u);
         }
         if (c < 1e-37f) c = 1e-37f;
+        uint8_t* queries = lds + S::LDS - S::QUERIES + wave * (S::QUERIES / S::W);
+#pragma unroll
+        for (int t = S::QREG; t < S::STEPS; ++t)
+            *reinterpret_cast<u32x4*>(queries + (t - S::QREG) * 1024 + ulane * 16) = __builtin_bit_cast(u32x4, st.q[t]);
 
         const auto run_tile = [&](uint32_t at_lds, int k0) {
             if (!busy || k0 >= any_hi || k0 + S::KT <= any_lo) return;
             const uint8_t* kt = lds + (at_lds - lds0);
-            compute<S>(st, kt, kt + S::TILE, k0, c, k0 < all_lo || k0 + S::KT > all_hi, ulane);
+            compute<S>(st, kt, kt + S::TILE, queries, k0, c, k0 < all_lo || k0 + S::KT > all_hi, ulane);
         };
 
         // ---- segments of the run whose page ids fit the list
@@ -1261,10 +1281,10 @@ hipError_t run(const AttnParams& a, const BlockArgs& all, hipStream_t s)
 // Waves that share key tiles.  Up to 32 rows a sequence and kv head stream
 // the cache once either way: none (32 sequences of up to 9000 bf16 keys, 28
 // rows: 82 us, shared 90; a few short ones are faster shared, 36 and 28).
-int sharing(int64_t tokens, int64_t max_q, int group, int seqs)
+int sharing(const CacheView& cache, int64_t tokens, int64_t max_q, int group, int seqs)
 {
     if (max_q * group <= 32) return 0;
-    return tokens * group >= kManyRows * seqs ? 8 : 4;
+    return tokens * group >= (cache.mxfp4 && cache.head_dim > 128 ? kManyWideRows : kManyRows) * seqs ? 8 : 4;
 }
 
 // Over a 4-bit cache few rows have kernels of their own, in tiles of 16 or 32
@@ -1290,7 +1310,8 @@ auto with_shape(const CacheView& cache, int waves, F f)
     const int dim = cache.head_dim;
     const auto by_dim = [&](auto e, auto w) {
         constexpr Kind E = decltype(e)::value;
-        constexpr int W = decltype(w)::value, W256 = W == 8 ? 4 : W;   // (a wave of 256 dimensions takes a whole SIMD's registers)
+        // (a wave of 256 dimensions takes a whole SIMD's registers, but for WIDE)
+        constexpr int W = decltype(w)::value, W256 = W == 8 && E != kMxfp4 ? 4 : W;
         if (dim == 64) return f(Shape<64, E, W, true>());
         if (dim == 128) return f(Shape<128, E, W, true>());
         if (dim == 256) return f(Shape<256, E, W256, true>());
@@ -1334,7 +1355,7 @@ size_t attention_workspace_need(const CacheView& cache, const BlockView& blocks,
     if (max_q > tokens) max_q = tokens;
     if (few_rows(cache, tokens, max_q, group, seqs, max_kv))
         return attention_few_need(few_size(cache, blocks, max_q * group, seqs, max_kv));
-    return shared_bytes(cache, sharing(tokens, max_q, group, seqs), tokens, group, seqs, max_kv);
+    return shared_bytes(cache, sharing(cache, tokens, max_q, group, seqs), tokens, group, seqs, max_kv);
 }
 
 // The largest need of any shape within the bounds: each kernel shape's grows
@@ -1352,7 +1373,7 @@ size_t attention_workspace_bytes(const CacheView& cache, const BlockView& blocks
         if (few_rows(cache, tokens, max_q, group, seqs, max_kv)) return most;
     }
     for (int waves : {0, 4, 8}) {
-        if (waves > sharing(tokens, max_q, group, 1)) break;
+        if (waves > sharing(cache, tokens, max_q, group, 1)) break;
         if (waves > 0 || !cache.mxfp4) most = std::max(most, shared_bytes(cache, waves, tokens, group, seqs, max_kv));
     }
     return most;
@@ -1402,7 +1423,7 @@ hipError_t launch_attention(const AttnParams& a, hipStream_t s)
     p.block_slot = uint32_t(a.blocks.slot_stride);
     if (few_rows(a.cache, a.tokens, a.max_q, a.group, a.seqs, a.max_kv))
         return launch_attention_few(few_size(a.cache, a.blocks, a.max_q * a.group, a.seqs, a.max_kv), &p, s);
-    const int waves = sharing(a.tokens, a.max_q, a.group, a.seqs);
+    const int waves = sharing(a.cache, a.tokens, a.max_q, a.group, a.seqs);
     return with_shape(a.cache, waves, [&](auto shape) { return run<decltype(shape)>(a, p, s); });
 }
 
