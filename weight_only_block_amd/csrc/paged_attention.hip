@@ -1290,9 +1290,10 @@ int sharing(const CacheView& cache, int64_t tokens, int64_t max_q, int group, in
 // Over a 4-bit cache few rows have kernels of their own, in tiles of 16 or 32
 // rows that each read the cache, the second and later ones from the last-level
 // cache.  They begin and end a unit sooner, and no row of a tile is left
-// without a token: up to 64 rows they are always faster (one sequence of 30000
-// keys, 42 rows: 25 us, shared 55; 32 of 8000: 40 and 50; 32 of 6000, 64 rows a
-// head of 8: 82 and 104), on up to 512 rows while a call is short (64 tokens
+// without a token.  Up to 64 rows, or as many in the mean, they are always
+// faster (one sequence of 30000 keys, 42 rows: 25 us, shared 55; 32 of 8000: 40
+// and 50; 32 of 6000, 64 rows a head of 8: 82 and 104; 21 of up to 134 rows and
+// 6687 keys: 27 and 43), on up to 512 rows while a call is short (64 tokens
 // over 8192 keys, 256 rows: 27 and 39; 6 sequences of up to 95 tokens over up to
 // 2589 keys: 31 and 38; 96 rows, 16 sequences of 4000 keys, which this leaves
 // shared: 58 and 53).
@@ -1300,7 +1301,8 @@ bool few_rows(const CacheView& cache, int64_t tokens, int64_t max_q, int group, 
 {
     const int64_t rows = max_q * group;
     if (!cache.mxfp4 || rows > kFewRows) return false;
-    return rows <= 64 || double(tokens * group / 32 + seqs) * cache.kv_heads * double(max_kv) * cache.head_dim <= kFewWork;
+    if (rows <= 64 || tokens * group <= int64_t(64) * seqs) return true;
+    return double(tokens * group / 32 + seqs) * cache.kv_heads * double(max_kv) * cache.head_dim <= kFewWork;
 }
 
 // Calls f with the shape for a cache and a call's rows.
@@ -1369,8 +1371,8 @@ size_t attention_workspace_bytes(const CacheView& cache, const BlockView& blocks
     if (cache.mxfp4) {
         for (int64_t rows : {int64_t(16), kFewRows})
             most = std::max(most, attention_few_bytes(few_size(cache, blocks, std::min(rows, max_q * group), seqs, max_kv)));
-        // (no smaller call has more rows or more work)
-        if (few_rows(cache, tokens, max_q, group, seqs, max_kv)) return most;
+        // (past 64 rows smaller calls may be shared: in the mean they can have more)
+        if (max_q * group <= 64) return most;
     }
     for (int waves : {0, 4, 8}) {
         if (waves > sharing(cache, tokens, max_q, group, 1)) break;
