@@ -378,6 +378,7 @@ qg_status qgemv_q8g64_argmax_noalloc(const void *w_packed, const uint16_t *x_bf1
  * stride. */
 #define QG_KV_BF16 0
 #define QG_KV_E4M3 1
+/* (2 is no type) */
 #define QG_KV_MXFP4 3
 typedef struct qg_kv_cache {
     void *k;
@@ -470,9 +471,9 @@ qg_status qg_rope_append(const qg_kv_cache *cache, const qg_rope *rope, const vo
  *               come several times; a token whose slot is outside the cache
  *               leaves its rows as they were
  * For another cache's type, another machine, or work on keys that other calls
- * of this library do not do.  4-bit and bf16 values are exact in either type,
- * but for those beyond its range (fp32 holds all; bf16 rounds none); an 8-bit
- * one is code * scale in fp32, rounded once more to bf16 where asked for.
+ * of this library do not do.  4-bit and bf16 values are exact in either type;
+ * an 8-bit one is code * scale in fp32, rounded once more to bf16 where asked
+ * for.
  * Errors as qg_rope_append's. */
 qg_status qg_kv_read(const qg_kv_cache *cache, const int64_t *slots, void *k_out, void *v_out, int32_t out_dtype,
                      int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,

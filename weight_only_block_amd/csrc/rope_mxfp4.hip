@@ -9,6 +9,10 @@
 // fall to the side of the definition: keys are rotated in fp64 from angles that
 // are exact (as in rope.hip), and both decisions are integer comparisons.
 // Queries take the same fp32 steps as with the other caches.
+//
+// What bounds it: of many tokens the memory, at a copy's rate (6001 tokens of 32
+// + 8 heads of 128 in bf16, 129 MB: 26 us, a copy 25.5); of a few the call on
+// the host (one token 7.3 us of it, 4 on the GPU).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -111,22 +115,41 @@ __device__ __forceinline__ void load_pairs(const void* src, int64_t at, const Ru
     }
 }
 
+// A token's angles, each worked out by one thread of the work-group: in 32 bits
+// for queries by the lower half of it, in 64 for keys by the upper (8191 tokens
+// of 32 + 8 heads, written and read back: 49 us, 51 where each thread works out
+// its queries' angles; 6613 tokens of 14 + 2 heads of 96 in the second kernel
+// below: 23 us, 38 where it does so with its keys' too).
+struct Table {
+    float cs[kMaxRotPairs], sn[kMaxRotPairs];
+    double key_cs[kMaxRotPairs], key_sn[kMaxRotPairs];
+
+    __device__ __forceinline__ void fill(const RopeParams& p, uint64_t pos, bool queries, bool keys)
+    {
+        static_assert(kThreads == 2 * kMaxRotPairs, "a thread a pair");
+        const int i = threadIdx.x % kMaxRotPairs;
+        if (i < p.rot_dim / 2) {
+            if (threadIdx.x >= kMaxRotPairs) {
+                if (keys) turn(pos, p.turns[i], p.amplitude, &key_cs[i], &key_sn[i]);
+            } else if (queries) {
+                turn(pos, p.turns[i], p.amplitude, &cs[i], &sn[i]);
+            }
+        }
+        __syncthreads();
+    }
+};
+
+// Those of a run's dimensions.
 template <class T>
 struct Angles {
     T cs[kRun], sn[kRun];      // sin with the sign that the partner takes
 
-    template <bool INTER>
-    __device__ __forceinline__ void fill(const RopeParams& p, uint64_t pos, const Run& r)
+    __device__ __forceinline__ void fill(const T* all_cs, const T* all_sn, const Run& r)
     {
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
             cs[i] = T(1), sn[i] = T(0);
-            if (INTER && i % 2) {      // rot_dim is even: both of a pair turn
-                cs[i] = cs[i - 1], sn[i] = -sn[i - 1];
-            } else if (r.turns[i]) {
-                turn(pos, p.turns[r.pair[i]], p.amplitude, &cs[i], &sn[i]);
-                if (!r.second[i]) sn[i] = -sn[i];
-            }
+            if (r.turns[i]) cs[i] = all_cs[r.pair[i]], sn[i] = r.second[i] ? all_sn[r.pair[i]] : -all_sn[r.pair[i]];
         }
     }
 };
@@ -186,12 +209,11 @@ __device__ __forceinline__ void store_block(const double* x, int d, uint8_t* cod
 // whole 64s, or pairs of neighbours with rot_dim in whole 8s.  As rope.hip's
 // wide kernel: a thread holds one eighth-of-a-dimension place, two runs of four
 // elements, of every LANES-th head.  Runs that turn with one another lie in
-// blocks of eight threads each, runs of neighbours in one of four threads.  The
-// keys' angles in fp64 are worked out once a token, by one thread each.
+// blocks of eight threads each, runs of neighbours in one of four threads.
 template <bool F32, bool INTER>
 __global__ __launch_bounds__(kThreads) void rope_append_mxfp4_wide(RopeParams p, BlockView blocks)
 {
-    __shared__ double angle[2][kMaxRotPairs];
+    __shared__ __align__(16) Table table;
     const int64_t token = blockIdx.x;
     const int dim = p.cache.head_dim, places = dim / 8;
     const int lanes = kThreads / places;             // heads at a time
@@ -203,8 +225,7 @@ __global__ __launch_bounds__(kThreads) void rope_append_mxfp4_wide(RopeParams p,
     // (one round of heads a work-group, or all of them)
     const int round = blockIdx.y;
     const bool keys = live && (gridDim.y == 1 || (round >= p.q_heads / lanes && round <= (p.q_heads + kv_heads - 1) / lanes));
-    if (keys)
-        for (int i = threadIdx.x; i < p.rot_dim / 2; i += kThreads) turn(pos, p.turns[i], p.amplitude, &angle[0][i], &angle[1][i]);
+    table.fill(p, pos, gridDim.y == 1 || round * lanes < p.q_heads, keys);
     const bool turns = 8 * j < p.rot_dim, split = turns && !INTER;
     const int a = split ? 4 * j : 8 * j, b = split ? a + p.rot_dim / 2 : a + 4;
     const int step = lanes * gridDim.y;
@@ -213,7 +234,7 @@ __global__ __launch_bounds__(kThreads) void rope_append_mxfp4_wide(RopeParams p,
         float cs[4], sn[4];
         if (turns) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) turn(pos, p.turns[4 * j + i], p.amplitude, &cs[i], &sn[i]);
+            for (int i = 0; i < 4; ++i) cs[i] = table.cs[4 * j + i], sn[i] = table.sn[4 * j + i];
         }
         for (; head < p.q_heads; head += step) {
             const int64_t at = token * p.q_token + head * p.q_head;
@@ -235,7 +256,6 @@ __global__ __launch_bounds__(kThreads) void rope_append_mxfp4_wide(RopeParams p,
         }
     }
     if (!live) return;               // (all threads of the work-group)
-    if (keys) __syncthreads();
     const int64_t row = slot & ((int64_t(1) << p.cache.page_shift) - 1);
     const int64_t cell = (page * p.cache.page_stride + row * p.cache.slot_stride) / 2;
     const int64_t block = page * blocks.page_stride + row * blocks.slot_stride;
@@ -253,7 +273,7 @@ __global__ __launch_bounds__(kThreads) void rope_append_mxfp4_wide(RopeParams p,
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int e = INTER ? 2 * i : i, o = INTER ? 2 * i + 1 : i + 4;
-                const double c = angle[0][4 * j + i], s = angle[1][4 * j + i], u = double(x[e]), v = double(x[o]);
+                const double c = table.key_cs[4 * j + i], s = table.key_sn[4 * j + i], u = double(x[e]), v = double(x[o]);
                 y[e] = to_odd(__builtin_fma(u, c, -(v * s)));
                 y[o] = to_odd(__builtin_fma(v, c, u * s));
             }
@@ -296,7 +316,6 @@ __global__ __launch_bounds__(kThreads) void rope_append_mxfp4(RopeParams p, Bloc
     const int64_t token = blockIdx.x;
     const int dim = p.cache.head_dim, places = dim / kRun, lanes = kThreads / places;
     const int j = threadIdx.x % places, lane = threadIdx.x / places;
-    if (lane >= lanes) return;                     // whole blocks of threads
     const int q_rounds = (p.q_heads + lanes - 1) / lanes, kv_rounds = (p.cache.kv_heads + lanes - 1) / lanes;
     const uint64_t pos = uint64_t(int64_t(p.pos[token]));
     const int64_t slot = p.slots[token], page = slot >> p.cache.page_shift;
@@ -305,11 +324,15 @@ __global__ __launch_bounds__(kThreads) void rope_append_mxfp4(RopeParams p, Bloc
     const int64_t cell = (page * p.cache.page_stride + row * p.cache.slot_stride) / 2;
     const int64_t block = page * blocks.page_stride + row * blocks.slot_stride;
     const Run run = make_run<INTER>(j * kRun, p.rot_dim);
+    __shared__ Table table;
 
     int round = blockIdx.y;
+    const bool all = gridDim.y == 1;               // rounds, or one
+    table.fill(p, pos, all || round < q_rounds, live && (all || (round >= q_rounds && round < q_rounds + kv_rounds)));
+    if (lane >= lanes) return;                     // whole blocks of threads
     if (round < q_rounds) {
         Angles<float> a;
-        a.template fill<INTER>(p, pos, run);
+        a.fill(table.cs, table.sn, run);
         for (; round < q_rounds; round += gridDim.y) {
             const int h = round * lanes + lane;
             if (h >= p.q_heads) continue;
@@ -333,7 +356,7 @@ __global__ __launch_bounds__(kThreads) void rope_append_mxfp4(RopeParams p, Bloc
     round -= q_rounds;
     if (round < kv_rounds) {
         Angles<double> a;
-        a.template fill<INTER>(p, pos, run);
+        a.fill(table.key_cs, table.key_sn, run);
         for (; round < kv_rounds; round += gridDim.y) {
             const int h = round * lanes + lane;
             if (h >= p.cache.kv_heads) continue;
