@@ -123,9 +123,15 @@ __device__ __forceinline__ int tiles_of(const Args& p, const Seq& s)
 }
 
 template <class S>
+__device__ __forceinline__ int unit_cost(const Args& p, const Seq& s)
+{
+    return s.n > 0 ? make_span<S>(p, s).steps + S::EXTRA : 0;
+}
+
+template <class S>
 __device__ __forceinline__ int cost_of(const Args& p, const Seq& s)
 {
-    return s.n > 0 ? tiles_of<S>(p, s) * (make_span<S>(p, s).steps + S::EXTRA) : 0;
+    return tiles_of<S>(p, s) * unit_cost<S>(p, s);
 }
 
 // Where a sequence's keys lie for one kv head.
@@ -463,9 +469,8 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel
     int longest = 0;
     for (int b = b0; b < min(b0 + per, p.seqs); ++b) {
         own = load_seq(p, b);
-        const int cost = cost_of<S>(p, own);
-        mine += cost;
-        longest = max(longest, cost);
+        mine += cost_of<S>(p, own);
+        longest = max(longest, unit_cost<S>(p, own));
     }
     int64_t upto = mine;
     scan_lanes(upto, longest);
@@ -510,7 +515,7 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES_PER_SIMD) void few_rows_kernel
     for (int cost; left >= (cost = cost_of<S>(p, s)); s = get_seq(++b)) left -= cost;
     int tile = 0, off = int(left);
     if (S::TILED)
-        for (const int unit = make_span<S>(p, s).steps + S::EXTRA; off >= unit; ++tile) off -= unit;
+        for (const int unit = unit_cost<S>(p, s); off >= unit; ++tile) off -= unit;
 
     while (true) {
         s.q0 = __builtin_amdgcn_readfirstlane(s.q0);
