@@ -58,6 +58,29 @@ def test_wide_heads_of_many_rows(dim, page, q_lens, kv_lens, window):
         p.check(p.run(window=window, scale=scale), window=window, scale=scale)
 
 
+@pytest.mark.parametrize("dim,page", [(32, 16), (64, 16), (64, 1), (96, 8), (128, 16), (128, 64)])
+@pytest.mark.parametrize("q_lens,kv_lens,window", [([300], [340], 0), ([600, 0, 500], [1000, 20, 500], 0), ([300], [900], 45),
+                                                   ([520, 1], [521, 300], 0)])
+def test_eight_waves_to_a_tile(dim, page, q_lens, kv_lens, window):
+    # 2048 rows a sequence and more, and a bound by which the call is a long one; with its own four waves
+    p = Problem(dim + page, q_lens, kv_lens, 8, 1, dim, page, nhd=page == 16)
+    print("case", dim, page, q_lens, window, flush=True)
+    for got in both(p, window=window):
+        p.check(got, window=window)
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("name", ["k", "v"])
+def test_nan_in_a_tile_of_eight_waves(dim, name):
+    p = Problem(17, [600], [700], 8, 2, dim, 16)
+    clean = both(p)
+    p.set_exponent(0, 650, 1, name, 255)
+    dims = (torch.arange(dim) // 32 == 1) if name == "v" else torch.ones(dim, dtype=torch.bool)
+    for got, was in zip(both(p), clean):
+        assert torch.isnan(got[0][550:][..., dims].float()).all()
+        assert torch.equal(got[0][550:][..., ~dims], was[0][550:][..., ~dims]) and torch.equal(got[0][:550], was[0][:550])
+
+
 @pytest.mark.parametrize("window", [1, 2, 17, 64, 100, 10000])
 @pytest.mark.parametrize("q_lens,kv_lens", [([30, 1], [300, 65]), ([44, 9, 0, 1], [45, 65, 0, 700])])
 def test_windows(window, q_lens, kv_lens):

@@ -70,6 +70,7 @@ constexpr int kListSeqs = 128;             // sequences whose lengths are kept i
 // four, 138 with eight; 700 over 6000 (1400 rows) 122 and 117; 260 over 4000
 // (520 rows) 66 and 95.
 constexpr int64_t kManyRows = 2048, kManyWideRows = 1024;
+constexpr double kShortWork = 1e8;         // rows times keys, see sharing()
 constexpr int64_t kFewRows = 512;         // of a sequence and kv head, see few_rows()
 constexpr double kFewWork = 2.4e8;         // row tiles times keys times dimensions
 
@@ -1283,9 +1284,13 @@ hipError_t run(const AttnParams& a, const BlockArgs& all, hipStream_t s)
 // Waves that share key tiles.  Up to 32 rows a sequence and kv head stream
 // the cache once either way: none (32 sequences of up to 9000 bf16 keys, 28
 // rows: 82 us, shared 90; a few short ones are faster shared, 36 and 28).
-int sharing(const CacheView& cache, int64_t tokens, int64_t max_q, int group, int seqs)
+// Over a 4-bit cache short calls keep four, whose units are more (994 tokens of 14
+// and 2 heads: 32 us with eight, 29 with four; 872 of 32 and 8: 32 and 29; 1500:
+// 43 and 41; 512 over 8192 keys, which this gives eight: 85 and 88).
+int sharing(const CacheView& cache, int64_t tokens, int64_t max_q, int group, int seqs, int64_t max_kv)
 {
     if (max_q * group <= 32) return 0;
+    if (cache.mxfp4 && cache.head_dim <= 128 && double(tokens) * group * cache.kv_heads * double(max_kv) < kShortWork) return 4;
     return tokens * group >= (cache.mxfp4 && cache.head_dim > 128 ? kManyWideRows : kManyRows) * seqs ? 8 : 4;
 }
 
@@ -1359,7 +1364,7 @@ size_t attention_workspace_need(const CacheView& cache, const BlockView& blocks,
     if (max_q > tokens) max_q = tokens;
     if (few_rows(cache, tokens, max_q, group, seqs, max_kv))
         return attention_few_need(few_size(cache, blocks, max_q * group, seqs, max_kv));
-    return shared_bytes(cache, sharing(cache, tokens, max_q, group, seqs), tokens, group, seqs, max_kv);
+    return shared_bytes(cache, sharing(cache, tokens, max_q, group, seqs, max_kv), tokens, group, seqs, max_kv);
 }
 
 // The largest need of any shape within the bounds: each kernel shape's grows
@@ -1377,7 +1382,7 @@ size_t attention_workspace_bytes(const CacheView& cache, const BlockView& blocks
         if (max_q * group <= 64) return most;
     }
     for (int waves : {0, 4, 8}) {
-        if (waves > sharing(cache, tokens, max_q, group, 1)) break;
+        if (waves > sharing(cache, tokens, max_q, group, 1, max_kv)) break;
         if (waves > 0 || !cache.mxfp4) most = std::max(most, shared_bytes(cache, waves, tokens, group, seqs, max_kv));
     }
     return most;
@@ -1427,7 +1432,7 @@ hipError_t launch_attention(const AttnParams& a, hipStream_t s)
     p.block_slot = uint32_t(a.blocks.slot_stride);
     if (few_rows(a.cache, a.tokens, a.max_q, a.group, a.seqs, a.max_kv))
         return launch_attention_few(few_size(a.cache, a.blocks, a.max_q * a.group, a.seqs, a.max_kv), &p, s);
-    const int waves = sharing(a.cache, a.tokens, a.max_q, a.group, a.seqs);
+    const int waves = sharing(a.cache, a.tokens, a.max_q, a.group, a.seqs, a.max_kv);
     return with_shape(a.cache, waves, [&](auto shape) { return run<decltype(shape)>(a, p, s); });
 }
 
