@@ -331,15 +331,21 @@ __device__ __forceinline__ bool consume(const State<S>& st, Tile<S>& tile, f32x4
     return poisoned;
 }
 
-// Probabilities of the scores (bf16 for the matrix cores, each off by at most
-// half a step, 2^-8 of it; their sum takes them unrounded), and the values
-// weighed by them.
+// Probabilities of the scores and the values weighed by them.  The matrix cores
+// take bf16, half a step of which is 2^-8 of a probability; such errors do not
+// cancel beside values that cancel likewise: outputs were off by 0.0018 to 0.0021
+// of their norm, by 0.0016 to 0.0017 where the exact one is rounded once.  So a
+// probability goes in as two, the second what rounding the first left (2^-16 of
+// it is lost), for 1 to 5% of the time of single and drafted tokens (40 ragged
+// ones 26.2 and 26.7 us, 3 of up to 131071 keys 70.5 and 73.6, 12 x 6 tokens 20.5
+// and 21.6) and up to 14% where tiles of 32 rows stream long contexts (8 tokens
+// over 80000 keys 42.5 and 48).
 template <class S>
 __device__ __forceinline__ void accumulate(State<S>& st, f32x4 (&sc)[S::R][2], bool masked, const uint8_t* vt, int k0, float c,
                                            int lane)
 {
     const int col = lane & 15, g = lane >> 4;
-    bf16x8 pb[S::R];
+    bf16x8 pb[S::R][2];
 #pragma unroll
     for (int r = 0; r < S::R; ++r) {
         if (masked) {
@@ -369,7 +375,7 @@ __device__ __forceinline__ void accumulate(State<S>& st, f32x4 (&sc)[S::R][2], b
             for (int n = 0; n < 2 * S::T; ++n) st.o[r][n] *= keep;
         }
         const float ref = st.m[r] == -INFINITY ? 0.0f : st.m[r];
-        union { bf16x8 v; uint32_t u[4]; } pr;
+        union { bf16x8 v; uint32_t u[4]; } pr, rest;
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
@@ -378,9 +384,12 @@ __device__ __forceinline__ void accumulate(State<S>& st, f32x4 (&sc)[S::R][2], b
                 const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[r][a][2 * x + 1], c, -ref));
                 st.l[r] += p0;
                 st.l[r] += p1;
-                pr.u[2 * a + x] = pack_bf16(p0, p1);
+                const uint32_t both = pack_bf16(p0, p1);
+                pr.u[2 * a + x] = both;
+                rest.u[2 * a + x] = pack_bf16(p0 - __uint_as_float(both << 16), p1 - __uint_as_float(both & 0xffff0000u));
             }
-        pb[r] = pr.v;
+        pb[r][0] = pr.v;
+        pb[r][1] = rest.v;
     }
 
     const int key = 4 * g + col / 4;
@@ -399,7 +408,10 @@ __device__ __forceinline__ void accumulate(State<S>& st, f32x4 (&sc)[S::R][2], b
     for (int n = 0; n < 2 * S::T; ++n) {
         if (n + kAhead < 2 * S::T) read(n + kAhead);
 #pragma unroll
-        for (int r = 0; r < S::R; ++r) st.o[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[n].v, pb[r], st.o[r][n], 0, 0, 0);
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int r = 0; r < S::R; ++r)
+                st.o[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[n].v, pb[r][e], st.o[r][n], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
     }
 }
