@@ -570,6 +570,9 @@ qg_status qg_sample_f32(const float *logits, int64_t m, int64_t N, int64_t ldx, 
  * which kernel ran).  Every successful qgemv_* call bumps the counter of the
  * kernel variant it launched.  Variant names: "<fmt>[_grouped[_swiglu]|_argmax]_m<m>_g<G>_r<R>"
  * with fmt one of q8g64, q4g32, q8g128, q8pc, e.g. "q8g64_m1_g32_r2".
+ * qg_paged_attention bumps "attention_split" (each wave streams keys of its
+ * own), "attention_tiles4" or "attention_tiles8" (four or eight waves share key
+ * tiles) or "attention_rows" (row tiles over a 4-bit cache).
  * qg_route_count returns 0 for unknown names. */
 void     qg_route_counts_reset(void);
 uint64_t qg_route_count(const char *variant);

@@ -15,6 +15,7 @@
 
 #include "../../include/qgemv.h"
 #include "argmax.h"
+#include "decode_ops.h"
 #include "launch.h"
 #include "read_stream.h"
 
@@ -471,6 +472,7 @@ void qg_route_counts_reset(void)
     for (int k = 0; k < kKinds; ++k)
         for (int m = 0; m < kMs; ++m)
             for (int g = 0; g < kGs; ++g) g_route[k][m][g].store(0);
+    qg::attention_route_reset();
 }
 
 uint64_t qg_route_count(const char* variant)
@@ -483,6 +485,8 @@ uint64_t qg_route_count(const char* variant)
                 format_variant(k, m + 1, 1 << g, buf, sizeof buf);
                 if (strcmp(buf, variant) == 0) return g_route[k][m][g].load();
             }
+    for (int r = 0; r < qg::kAttentionRoutes; ++r)
+        if (strcmp(qg::kAttentionRouteNames[r], variant) == 0) return qg::attention_route_count(r);
     return 0;
 }
 

@@ -142,6 +142,14 @@ size_t attention_workspace_bytes(const CacheView& cache, const BlockView& blocks
                                  int64_t max_q, int64_t max_kv);
 hipError_t launch_attention(const AttnParams& p, hipStream_t s);
 
+// Successful launches by kernel, for tests: waves that stream keys of their own;
+// tiles that four or eight waves share; row tiles of a 4-bit cache.
+enum AttentionRoute { kSplit, kTiles4, kTiles8, kRowTiles, kAttentionRoutes };
+constexpr const char* kAttentionRouteNames[kAttentionRoutes] = {"attention_split", "attention_tiles4", "attention_tiles8",
+                                                                 "attention_rows"};
+uint64_t attention_route_count(int route);
+void attention_route_reset();
+
 struct SampleParams {
     const float* x;
     int64_t m, N, ldx;

@@ -49,6 +49,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "attention_common.h"
@@ -1388,6 +1389,20 @@ size_t attention_workspace_bytes(const CacheView& cache, const BlockView& blocks
     return most;
 }
 
+static std::atomic<uint64_t> g_routes[kAttentionRoutes];
+
+uint64_t attention_route_count(int route) { return g_routes[route].load(); }
+void attention_route_reset()
+{
+    for (auto& n : g_routes) n.store(0);
+}
+
+static hipError_t counted(int route, hipError_t e)
+{
+    if (e == hipSuccess) g_routes[route].fetch_add(1, std::memory_order_relaxed);
+    return e;
+}
+
 hipError_t launch_attention(const AttnParams& a, hipStream_t s)
 {
     const int unit = a.cache.mxfp4 ? 32 : a.cache.e4m3 ? 16 : 8;   // elements in 16 bytes
@@ -1431,9 +1446,12 @@ hipError_t launch_attention(const AttnParams& a, hipStream_t s)
     p.block_head = uint32_t(a.blocks.head_stride);
     p.block_slot = uint32_t(a.blocks.slot_stride);
     if (few_rows(a.cache, a.tokens, a.max_q, a.group, a.seqs, a.max_kv))
-        return launch_attention_few(few_size(a.cache, a.blocks, a.max_q * a.group, a.seqs, a.max_kv), &p, s);
+        return counted(kRowTiles, launch_attention_few(few_size(a.cache, a.blocks, a.max_q * a.group, a.seqs, a.max_kv), &p, s));
     const int waves = sharing(a.cache, a.tokens, a.max_q, a.group, a.seqs, a.max_kv);
-    return with_shape(a.cache, waves, [&](auto shape) { return run<decltype(shape)>(a, p, s); });
+    return with_shape(a.cache, waves, [&](auto shape) {
+        using S = decltype(shape);
+        return counted(!S::SHARED ? kSplit : S::W == 4 ? kTiles4 : kTiles8, run<S>(a, p, s));
+    });
 }
 
 }  // namespace qg
