@@ -121,7 +121,7 @@ def test_long_sequences_split_over_the_chip(q_len):
 
 @pytest.mark.parametrize("hq,hk,dim,chunk", [(8, 1, 128, 300), (4, 2, 64, 1100), (2, 1, 256, 600)])
 def test_chunks_of_many_rows(hq, hk, dim, chunk):
-    # past 2048 rows a sequence eight waves share a tile; rows checked as calls of their own prefix would give them
+    # (calls this short have tiles of four waves, of 256 dimensions of eight); rows checked as calls of their own prefix would give them
     kv = chunk + 333
     p = Problem(chunk, [chunk], [kv], hq, hk, dim, 16)
     print("case", hq, hk, dim, chunk, flush=True)
@@ -285,7 +285,7 @@ def test_calls_of_all_cache_types_share_a_workspace():
 @pytest.mark.parametrize("seqs", [63, 64, 65, 128, 129, 300, 1100])
 @pytest.mark.parametrize("chunks", [0, 1, 2])
 def test_many_sequences(seqs, chunks):
-    # past 128 sequences lengths are read again for each unit; single tokens alone, with a few chunks, with long ones
+    # all in row tiles, as the mean is below 64 rows; single tokens alone, with a few chunks, with long ones
     g = torch.Generator().manual_seed(seqs + chunks)
     q_lens = (torch.rand(seqs, generator=g) < 0.9).int().tolist()
     kv_lens = torch.randint(0, 70, (seqs,), generator=g).tolist()

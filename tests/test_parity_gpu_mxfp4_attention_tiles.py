@@ -1,8 +1,10 @@
 """Attention over a 4-bit cache with more rows a sequence and kv head than one
 tile holds: in row tiles that each stream the cache, and in the tiles that
-waves share.  Which of the two a call takes goes by its bounds, so every
-problem here of more than 64 rows runs once with its own and once with a
-max_kv far above its lengths."""
+waves share.  Which of the two a call takes goes by its bounds: problems here
+run once with their own and once with a max_kv far above their lengths, by which
+those of 65 to 512 rows and more than 64 in the mean of their sequences change
+kernels.  test_parity_gpu_mxfp4_attention_routes.py names the kernel that each
+of its problems runs on."""
 import math
 
 import pytest
