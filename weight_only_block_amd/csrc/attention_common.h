@@ -161,8 +161,14 @@ struct BlockArgs : Args {
 
 enum Kind { kBf16, kE4m3, kMxfp4 };
 
-// x / group, exact while x * group is below 2^31: x is a row of a unit beside
-// the heads before its first, below 255 + group, and group below 2^15.
+// Rows of a sequence and kv head (tokens x group) up to which a 4-bit cache's
+// calls may go in row tiles, see few_rows() of paged_attention.hip.
+constexpr int64_t kFewRows = 512;
+
+// x / group, exact while x * group is below 2^31.  In the shared tiles x is a row
+// of a unit beside the heads before its first, below 255 + group, and group below
+// 2^15; in row tiles a row of the whole sequence, below kFewRows, as is group - 1.
+static_assert((255 + (int64_t(1) << 15)) << 15 < int64_t(1) << 31 && kFewRows * kFewRows < int64_t(1) << 31, "by_group is exact");
 __device__ __forceinline__ uint32_t by_group(const Args& p, uint32_t x) { return __umulhi(2 * x, p.by_group); }
 
 __device__ __forceinline__ Seq load_seq(const Args& p, int b)

@@ -72,7 +72,6 @@ constexpr int kListSeqs = 128;             // sequences whose lengths are kept i
 // (520 rows) 66 and 95.
 constexpr int64_t kManyRows = 2048, kManyWideRows = 1024;
 constexpr double kShortWork = 1e8;         // rows times keys, see sharing()
-constexpr int64_t kFewRows = 512;         // of a sequence and kv head, see few_rows()
 constexpr double kFewWork = 2.4e8;         // row tiles times keys times dimensions
 
 __device__ __forceinline__ uint32_t lds_offset(const void* p)

@@ -78,10 +78,8 @@ struct Few {
     static constexpr int LEAST = 2, EXTRA = 3;
     static constexpr float JOINED = 0.25f;
     static constexpr int SLOT = M * DP + 2 * M;                         // floats of a partial result
-    // Joining: four values at a time, so many of them a thread, and parts whose
-    // loads are in flight together.
-    static constexpr int QUADS = DP / 4, ITEMS = (M * QUADS + THREADS - 1) / THREADS;
-    static constexpr int PARTS = 8;
+    // Joining: four values at a time, and parts whose loads are in flight together.
+    static constexpr int QUADS = DP / 4, PARTS = 8;
 
     // The chunk of 8 dimensions is moved so that 16 keys of one chunk (what a
     // wave's quarter writes) and 8 keys of two neighbours (what a half reads)
