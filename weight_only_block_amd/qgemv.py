@@ -802,6 +802,8 @@ def _dtypes():
     # where this torch has it
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     kinds.current_stream = staticmethod(raw or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+    kinds.current_device = staticmethod(getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device)
+    kinds.device = staticmethod(torch.cuda.device)
     _DT = kinds
     return kinds
 
@@ -834,6 +836,18 @@ def _stream_of(stream, device: int):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _entry(fn, device: int):
+    """The library's entry as a call for tensors of that device: a launch on a
+    default stream goes to the current device, whatever the tensors' is."""
+    if _DT.current_device() == device:
+        return fn
+
+    def there(*args):
+        with _DT.device(device):
+            return fn(*args)
+    return there
+
+
 def rope_append(cache: KVCache, rope: Rope, q, k, v, pos, slots, q_out, stream=None, check=True):
     """Rotates q [tokens][heads][dim] into q_out (bfloat16) and k into the
     cache at each token's slot, and copies v there, in one launch up to 2^23 tokens.
@@ -862,10 +876,11 @@ def rope_append(cache: KVCache, rope: Rope, q, k, v, pos, slots, q_out, stream=N
     _fits(slots, where, "slots", dt.i64, (tokens,), dev)
     if tokens == 0:
         return QG_OK
-    st = lib().qg_rope_append(cache._ref, rope._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                              SRC_F32 if kind == dt.f32 else SRC_BF16, sq[0], sq[1], sk[0], sk[1],
-                              sv[0], sv[1], pos.data_ptr(), slots.data_ptr(), q_out.data_ptr(), so[0], so[1], tokens,
-                              heads, _stream_of(stream, dev))
+    entry = _entry(lib().qg_rope_append, dev)
+    st = entry(cache._ref, rope._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+               SRC_F32 if kind == dt.f32 else SRC_BF16, sq[0], sq[1], sk[0], sk[1],
+               sv[0], sv[1], pos.data_ptr(), slots.data_ptr(), q_out.data_ptr(), so[0], so[1], tokens,
+               heads, _stream_of(stream, dev))
     if check and st:
         _check(st, where)
     return st
@@ -890,8 +905,9 @@ def kv_read(cache: KVCache, slots, k_out=None, v_out=None, stream=None, check=Tr
     sv = (0, 0) if v_out is None else _fits(v_out, where, "v_out", kind, rows, dev)
     if tokens == 0:
         return QG_OK
-    st = lib().qg_kv_read(cache._ref, slots.data_ptr(), _ptr(k_out), _ptr(v_out), SRC_F32 if kind == dt.f32 else SRC_BF16,
-                          sk[0], sk[1], sv[0], sv[1], tokens, _stream_of(stream, dev))
+    entry = _entry(lib().qg_kv_read, dev)
+    st = entry(cache._ref, slots.data_ptr(), _ptr(k_out), _ptr(v_out), SRC_F32 if kind == dt.f32 else SRC_BF16,
+               sk[0], sk[1], sv[0], sv[1], tokens, _stream_of(stream, dev))
     if check and st:
         _check(st, where)
     return st
@@ -939,11 +955,12 @@ def paged_attention(cache: KVCache, q, out, q_start, kv_len, page_table, workspa
     room = _space(workspace, where, dev)
     if tokens == 0 or seqs == 0:
         return QG_OK
-    st = lib().qg_paged_attention(cache._ref, q.data_ptr(), sq[0], sq[1], out.data_ptr(), so[0], so[1], _ptr(lse),
-                                  lse_row, q_start.data_ptr(), kv_len.data_ptr(),
-                                  page_table.data_ptr(), row, cols, tokens, heads, seqs, max_q, max_kv,
-                                  dim ** -0.5 if scale is None else scale, window, workspace.data_ptr(), room,
-                                  _stream_of(stream, dev))
+    entry = _entry(lib().qg_paged_attention, dev)
+    st = entry(cache._ref, q.data_ptr(), sq[0], sq[1], out.data_ptr(), so[0], so[1], _ptr(lse),
+               lse_row, q_start.data_ptr(), kv_len.data_ptr(),
+               page_table.data_ptr(), row, cols, tokens, heads, seqs, max_q, max_kv,
+               dim ** -0.5 if scale is None else scale, window, workspace.data_ptr(), room,
+               _stream_of(stream, dev))
     if check and st:
         _check(st, where)
     return st
@@ -987,8 +1004,9 @@ def sample_f32(logits, u, idx_out, workspace, temperature=None, top_k=None, top_
         if m == 0:
             return QG_OK
         ldx = N
-    st = lib().qg_sample_f32(logits.data_ptr(), m, N, ldx, u.data_ptr(), _ptr(temperature), _ptr(top_k), _ptr(top_p),
-                             _ptr(min_p), idx_out.data_ptr(), workspace.data_ptr(), room, _stream_of(stream, dev))
+    entry = _entry(lib().qg_sample_f32, dev)
+    st = entry(logits.data_ptr(), m, N, ldx, u.data_ptr(), _ptr(temperature), _ptr(top_k), _ptr(top_p),
+               _ptr(min_p), idx_out.data_ptr(), workspace.data_ptr(), room, _stream_of(stream, dev))
     if check and st:
         _check(st, where)
     return st
