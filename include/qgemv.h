@@ -511,7 +511,7 @@ qg_status qg_kv_read(const qg_kv_cache *cache, const int64_t *slots, void *k_out
  *               Calls that share one must not overlap in time.
  * Scores, softmax statistics and sums are fp32 (values above 2^120 / keys in
  * magnitude may sum past its range); probabilities enter the second product as
- * bf16, with QG_KV_MXFP4 and max_q * q_heads / kv_heads up to 64 as two bf16
+ * bf16, with QG_KV_MXFP4 and max_q * q_heads / kv_heads up to 32 as two bf16
  * numbers (2^-16 of one is lost).  The split of a sequence over work-groups and the order of every sum
  * depend on the arguments alone: a result is the same bits from run to run.
  * Where starts do not ascend, which rows are written, and by which sequence, is

@@ -60,6 +60,8 @@ struct Few {
     static constexpr int RB = T <= 2 ? 64 * T : T <= 4 ? 256 : 512;     // bytes of a row of V in LDS, a power of two
     static constexpr int W = W_, THREADS = 64 * W;
     static constexpr int M = 16 * R;
+    // bf16 numbers that a probability enters the second product as
+    static constexpr int NP = TILED && EVEN ? 1 : 2;
     static constexpr int KT = 32, STEP = KT * W;                        // keys of a wave's tiles, of a step
     static constexpr int TILE = KT * RB;
     // exponent bytes that a lane's 8 T dimensions of a key reach into
@@ -330,20 +332,24 @@ __device__ __forceinline__ bool consume(const State<S>& st, Tile<S>& tile, f32x4
 }
 
 // Probabilities of the scores and the values weighed by them.  The matrix cores
-// take bf16, half a step of which is 2^-8 of a probability; such errors do not
-// cancel beside values that cancel likewise: outputs were off by 0.0018 to 0.0021
-// of their norm, by 0.0016 to 0.0017 where the exact one is rounded once.  So a
-// probability goes in as two, the second what rounding the first left (2^-16 of
-// it is lost), for 1 to 5% of the time of single and drafted tokens (40 ragged
-// ones 26.2 and 26.7 us, 3 of up to 131071 keys 70.5 and 73.6, 12 x 6 tokens 20.5
-// and 21.6) and up to 14% where tiles of 32 rows stream long contexts (8 tokens
-// over 80000 keys 42.5 and 48).
+// take bf16, half a step of which is 2^-8 of a probability.  Such errors do not
+// cancel beside values that cancel likewise: outputs are off by 0.0018 to 0.0022
+// of their norm, by 0.0016 to 0.0017 where the exact one is rounded once.  So
+// probabilities of up to 32 rows go in as two numbers, the second what rounding
+// the first left (2^-16 is lost), for 1 to 5% of the time of single and drafted
+// tokens (40 ragged ones 26.2 and 26.7 us, 3 of up to 131071 keys 70.5 and 73.6,
+// 12 x 6 tokens 20.5 and 21.6) and up to 14% over long contexts (8 tokens over
+// 80000 keys 42.5 and 48).  Tiles of more rows, bound by the matrix cores and
+// vector instructions, would take up to a fifth longer (64 rows, 32 sequences of
+// 6000 keys: 84 and 99 us), and have one, as chunks have.  (fp16 would cost
+// nothing, but has no bits for probabilities far below a row's largest, all that
+// remains where its value is zero.)
 template <class S>
 __device__ __forceinline__ void accumulate(State<S>& st, f32x4 (&sc)[S::R][2], bool masked, const uint8_t* vt, int k0, float c,
                                            int lane)
 {
     const int col = lane & 15, g = lane >> 4;
-    bf16x8 pb[S::R][2];
+    bf16x8 pb[S::R][S::NP];
 #pragma unroll
     for (int r = 0; r < S::R; ++r) {
         if (masked) {
@@ -384,10 +390,10 @@ __device__ __forceinline__ void accumulate(State<S>& st, f32x4 (&sc)[S::R][2], b
                 st.l[r] += p1;
                 const uint32_t both = pack_bf16(p0, p1);
                 pr.u[2 * a + x] = both;
-                rest.u[2 * a + x] = pack_bf16(p0 - __uint_as_float(both << 16), p1 - __uint_as_float(both & 0xffff0000u));
+                if (S::NP > 1) rest.u[2 * a + x] = pack_bf16(p0 - __uint_as_float(both << 16), p1 - __uint_as_float(both & 0xffff0000u));
             }
         pb[r][0] = pr.v;
-        pb[r][1] = rest.v;
+        if constexpr (S::NP > 1) pb[r][1] = rest.v;
     }
 
     const int key = 4 * g + col / 4;
@@ -406,7 +412,7 @@ __device__ __forceinline__ void accumulate(State<S>& st, f32x4 (&sc)[S::R][2], b
     for (int n = 0; n < 2 * S::T; ++n) {
         if (n + kAhead < 2 * S::T) read(n + kAhead);
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < S::NP; ++e)
 #pragma unroll
             for (int r = 0; r < S::R; ++r)
                 st.o[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[n].v, pb[r][e], st.o[r][n], 0, 0, 0);
