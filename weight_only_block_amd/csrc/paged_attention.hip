@@ -324,8 +324,12 @@ __device__ __forceinline__ void raise(State<S>& st, float top, float c)
 }
 
 // Probabilities, which become bf16 for the matrix cores (each off by at most
-// half a step, 2^-8 of it; over many keys the errors cancel), and their sum,
-// which takes them unrounded.
+// half a step, 2^-8 of it), and their sum, which takes them unrounded.  The
+// errors cancel over many keys as far as the values do: outputs are off by 0.0019
+// to 0.0023 of their norm, where one rounding of the exact output leaves 0.0017.
+// Two bf16 numbers a probability would bring that, for a third more time (4-bit
+// cache, 2503 tokens over 16007 keys 560 and 762 us, chunks and single tokens of
+// 20 sequences 32 and 38).
 template <class S>
 __device__ __forceinline__ void probs(State<S>& st, const Scores<S>& sc, Probs<S>& pb, float c)
 {

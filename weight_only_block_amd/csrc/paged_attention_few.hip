@@ -8,10 +8,10 @@
 // tile) with up to 16 R rows (tokens x query heads of the kv head), all units'
 // steps lie in one line, and each work-group takes an equal run of it.  What bounds it:
 // the cache's bytes on long contexts (three sequences of up to 131071 keys, 400
-// MB: 70 us, of which some 8 pass before the first keys arrive and while parts
-// are joined: 6.4 TB/s between, where a plain read reaches 6.8), and on short
+// MB: 73 us, of which some 8 pass before the first keys arrive and while parts
+// are joined: 6.1 TB/s between, where a plain read reaches 6.8), and on short
 // ones a chain of dependent accesses (one sequence of 1023 keys: lengths, page
-// ids, keys, the parts' stores, their count and their join, 8.5 us).
+// ids, keys, the parts' stores, their count and their join, 8.7 us).
 //
 // Products.  S^T = K Q^T and O^T = V^T P^T, 16x16x32.  Lane l holds of key
 // l % 16 the 8 T dimensions from 8 T (l / 16) on, as they lie in memory: a
@@ -806,12 +806,12 @@ int64_t workers(const FewSize& z)
 // Pages of fewer than 16 tokens, and rows gigabytes apart, have one kernel.
 // Second sixteens of rows make parts twice as large: eight waves a work-group
 // leave half as many parts, but half as many runs, which lose where each begins
-// and ends several units (5 tokens over 8000 keys, 2 sequences of 8 heads: 17.2
-// us against 20.6; 6 over up to 6007, 12 sequences: 20.9 against 23.0; 8 over
-// 2000: 15.4 against 17.4; 24 over 8000: 53.5 against 53.7; 32 over up to 4000:
-// 28.6 against 26.9; 100 over up to 2000: 42.2 against 35.4; 4 over up to 900:
-// 14.0 against 13.1), with several tiles of rows as with one (48 rows, 16
-// sequences of 4000 keys and 8 heads: 33.0 against 42.2).
+// and ends several units (5 tokens over 8000 keys, 2 sequences of 8 heads: 17.8
+// us against 21.4; 6 over up to 6007, 12 sequences: 21.8 against 23.9; 8 over
+// 2000: 15.9 against 17.6; 24 over 8000: 59.8 against 59.3; 32 over up to 4000:
+// 30.5 against 28.5; 100 over up to 2000: 44.9 against 37.0; 4 over up to 900:
+// 14.3 against 13.2), with several tiles of rows as with one (48 rows, 16
+// sequences of 4000 keys and 8 heads: 31.7 against 41.1).
 bool wide_groups(const FewSize& z)
 {
     return z.rows > 16 && z.even && z.dim <= 128 && int64_t(z.seqs) * z.kv_heads <= 192 && z.max_kv > 1024;
