@@ -3,7 +3,8 @@
 // A thread holds 16 bytes of an output row and what they come from.  Of many
 // tokens the writes bound it: 90001 tokens of 8 heads of 128 from a 4-bit cache
 // to bf16, 98 MB read and 369 MB written, 98 us (74 where they were read just
-// before; a copy moves as much in 92, a fill writes the output in 54); of a few
+// before; a copy moves as much in 92, a fill writes the output in 54), from a bf16
+// cache 132 us and from an 8-bit one 100 (737 and 553 MB moved); of a few
 // the call on the host (513 tokens 6 us, 3.5 of it on the GPU).  Rows are
 // written past the caches: what reads them next is another kernel's product.
 #include <hip/hip_runtime.h>

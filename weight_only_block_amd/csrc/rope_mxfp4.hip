@@ -10,9 +10,10 @@
 // are exact (as in rope.hip), and both decisions are integer comparisons.
 // Queries take the same fp32 steps as with the other caches.
 //
-// What bounds it: of many tokens the memory, at a copy's rate (6001 tokens of 32
-// + 8 heads of 128 in bf16, 129 MB: 26 us, a copy 25.5); of a few the call on
-// the host (one token 7.3 us of it, 4 on the GPU).
+// What bounds it: of many tokens the memory (6001 tokens of 32 + 8 heads of 128
+// in bf16, 129 MB: 28.6 us, 24.2 where they lie in the last-level cache, a copy
+// 25.5; vector instructions busy in 56% of the cycles); of a few the call on the
+// host (one token 8.3 us of it, 4.4 on the GPU).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
